@@ -23,7 +23,9 @@ OP_FWD, OP_BWD, OP_DECODE = 0, 1, 2
 
 EXPORTED = ("gbs_version", "gbs_status_string", "gbs_last_error", "gbs_workspace_bytes",
             "gbs_clear_error", "gbs_check", "gbs_select", "gbs_fwd", "gbs_bwd", "gbs_decode",
-            "gbs_set_timer", "gbs_launch_count", "gbs_selftest_wait_timeout")
+            "gbs_set_timer", "gbs_launch_count", "gbs_selftest_wait_timeout",
+            "gbs_qkv_rope_workspace_bytes", "gbs_qkv_rope_fwd", "gbs_qkv_rope_bwd", "gbs_kv4_append",
+            "gbs_kv4_read", "gbs_kv4_workspace_bytes", "gbs_kv4_decode")
 
 
 class GbsError(RuntimeError):
@@ -46,6 +48,27 @@ class KvLayout(ctypes.Structure):
                 ("group_shared", ctypes.c_int)]
 
 
+class Heads(ctypes.Structure):
+    """gbs_heads: a [B, heads, N, d] tensor by pointer and strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class RopeParams(ctypes.Structure):
+    """gbs_rope_params."""
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("n_axes", ctypes.c_int), ("axis", ctypes.c_ubyte * 64), ("max_pos", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("w_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class Kv4CacheDesc(ctypes.Structure):
+    """gbs_kv4_cache."""
+    _fields_ = [("kc", ctypes.c_void_p), ("kp", ctypes.c_void_p), ("vc", ctypes.c_void_p),
+                ("vp", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("cap", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -59,6 +82,7 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(Params)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+    H, C4 = ctypes.POINTER(Heads), ctypes.POINTER(Kv4CacheDesc)
     sigs = {
         "gbs_version": (i32, []),
         "gbs_status_string": (ctypes.c_char_p, [i32]),
@@ -74,6 +98,14 @@ def load_library(path: str = LIB_PATH):
                                 vp]),
         "gbs_set_timer": (i32, [i32, vp, vp]),
         "gbs_launch_count": (ctypes.c_uint64, []),
+        "gbs_qkv_rope_workspace_bytes": (sz, [ctypes.POINTER(RopeParams)]),
+        "gbs_qkv_rope_fwd": (i32, [ctypes.POINTER(RopeParams)] + [H] * 3 + [vp] * 5 + [H] * 3 + [vp] * 2),
+        "gbs_qkv_rope_bwd": (i32, [ctypes.POINTER(RopeParams)] + [H] * 2 + [vp] * 5 + [H] * 6
+                             + [vp] * 3 + [sz, vp]),
+        "gbs_kv4_append": (i32, [P, C4, H, H, i32, vp, vp, vp, vp]),
+        "gbs_kv4_read": (i32, [P, C4, H, H, i32, vp, vp, vp, vp]),
+        "gbs_kv4_workspace_bytes": (sz, [P]),
+        "gbs_kv4_decode": (i32, [P, C4, vp, i32, vp, vp, vp, vp, i32, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -104,6 +136,7 @@ _DEVICE_TYPES = ("cuda",)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
+_F16 = (torch.float16,)
 
 
 def _invalid(where, detail):
@@ -393,3 +426,357 @@ def decode_noalloc(q, Kc, Vc, S, L=None, block=64, topk=32, scale=0.0, num_split
     _check(f(ctypes.byref(p), _ptr(q), _ptr(Kc), _ptr(Vc), _ptr(S), _ptr(O), _ptr(LSE), num_splits,
              _stream(stream)), "gbs_decode_noalloc")
     return O, LSE
+
+
+# ------------------------------------------- projections to attention, 4-bit cache
+
+
+def _on(device, stream):
+    """The context of a call's own allocations and launches: ``device`` current
+    and, if given, ``stream`` too, so that temporaries belong to the stream that
+    uses them. None where both are current already."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+def _called(device, stream, fn):
+    ctx = _on(device, stream)
+    if ctx is None:
+        return fn(_stream())
+    with ctx:
+        return fn(_stream())
+
+
+def _heads(where, name, t, shape, dtypes, device, n_dim=1, out=False):
+    """A [B, *, *, d] tensor with contiguous channels as gbs_heads; ``n_dim`` is
+    its token dimension (1: [B, N, H, d], 2: [B, H, N, d])."""
+    if not isinstance(t, torch.Tensor):
+        raise _invalid(where, f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise _invalid(where, f"{name} is on {t.device}; expected {device}")
+    if t.dtype not in dtypes:
+        raise _invalid(where, f"{name} has dtype {t.dtype}; expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != shape:
+        raise _invalid(where, f"{name} has shape {tuple(t.shape)}; expected {shape}")
+    s = t.stride()
+    if s[3] != 1:
+        raise _invalid(where, f"{name} must have contiguous channels")
+    # the stride of a dimension of one is never followed
+    st = [s[i] if shape[i] > 1 else 0 for i in range(3)]
+    if out:
+        need = shape[3]
+        for step, n in sorted((st[i], shape[i]) for i in range(3) if shape[i] > 1):
+            if step < need:
+                raise _invalid(where, f"{name} is written and has elements that share memory")
+            need = step * n
+    return Heads(t.data_ptr(), st[0], st[3 - n_dim], st[n_dim])
+
+
+def _opt(h):
+    return None if h is None else ctypes.byref(h)
+
+
+def rope_tables(max_pos, rot, base=10000.0, device="cuda"):
+    """(cos, sin) [max_pos, rot / 2] fp32 of the angles pos * base^(-2 i / rot),
+    computed in 64 bits (an fp32 angle of a far position is off by whole degrees)."""
+    half = rot // 2
+    freq = base ** (-torch.arange(half, dtype=torch.float64, device=device) / max(half, 1))
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return angle.cos().float(), angle.sin().float()
+
+
+def rope_axes(sections, interleaved=False):
+    """The axis of every rotated pair from the number of pairs per axis: blocks
+    (all of axis 0, then axis 1, ...), or dealt out in turn while an axis has
+    pairs left."""
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
+def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved):
+    """(params, device) of a qkv_rope call, its small tensors checked."""
+    dev = _device(where, "q", q)
+    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise _invalid(where, "q and k must be 4-D: [B, N, H, d]")
+    B, N, Hq, d = q.shape
+    _act_dtype(where, "q", q)
+    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+        raise _invalid(where, "cos must be [max_pos, rot / 2]")
+    max_pos, half = cos.shape
+    for name, t in (("cos", cos), ("sin", sin)):
+        _need(where, name, t, (max_pos, half), _F32, dev)
+    if not isinstance(pos, torch.Tensor) or pos.dim() not in (2, 3):
+        raise _invalid(where, "pos must be [B, N] or [B, N, axes]")
+    n_axes = 1 if pos.dim() == 2 else pos.shape[2]
+    _need(where, "pos", pos, (B, N) if pos.dim() == 2 else (B, N, n_axes), _I32, dev)
+    if half > 64:
+        raise _invalid(where, f"cos has {half} columns; at most d / 2 = {d // 2} pairs are rotated")
+    axes = [0] * half if axes is None else axes
+    if len(axes) != half:
+        raise _invalid(where, f"axes has {len(axes)} entries; expected one of each of the {half} pairs")
+    if not all(0 <= a < n_axes for a in axes):
+        raise _invalid(where, f"an axis is outside [0, {n_axes})")
+    if (wq is None) != (wk is None):
+        raise _invalid(where, "give both weights or neither")
+    w_dtype = torch.float32
+    if wq is not None:
+        _need(where, "wq", wq, (d,), (torch.float32, torch.bfloat16), dev)
+        _need(where, "wk", wk, (d,), (wq.dtype,), dev)
+        w_dtype = wq.dtype
+    p = RopeParams(B, N, Hq, k.shape[2], d, 2 * half, int(bool(interleaved)), n_axes,
+                   (ctypes.c_ubyte * 64)(*axes), max_pos, DTYPES[q.dtype], DTYPES[w_dtype], float(eps))
+    return p, dev
+
+
+def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, interleaved=False, out=None,
+             ws=None, stream=None):
+    """Norm of every query and key head (weights ``wq``, ``wk`` [d]; None: no norm)
+    and rotary positions, from a projection's q [B, N, Hq, d], k and v
+    [B, N, Hkv, d] (any strides with contiguous channels, such as parts of one
+    packed tensor; v may be None) to Q [B, Hq, N, d], K and V [B, Hkv, N, d].
+
+    ``cos``, ``sin``: fp32 [max_pos, rot / 2] (``rope_tables``); the first rot
+    channels are rotated in pairs of halves or, ``interleaved``, of neighbours.
+    ``pos``: int32 [B, N], or [B, N, axes] with ``axes`` the axis of every pair
+    (``rope_axes``). ``out``: (Q, K, V) to write to, strided too. Returns (Q, K, V)."""
+    where = "gbs_qkv_rope_fwd"
+    lib = load_library()
+    p, dev = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved)
+    B, N, Hq, d, Hkv, act = p.B, p.N, p.Hq, p.d, p.Hkv, (q.dtype,)
+    hq = _heads(where, "q", q, (B, N, Hq, d), act, dev)
+    hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev)
+    hv = None if v is None else _heads(where, "v", v, (B, N, Hkv, d), act, dev)
+    if out is not None and (len(out) != 3 or (out[2] is None) != (v is None)):
+        raise _invalid(where, "out must be (Q, K, V), V None exactly if v is")
+    if ws is not None:
+        _need(where, "ws", ws, None, _U8, dev)
+        if ws.numel() < 256:
+            raise GbsError(5, where, "ws must have at least 256 bytes")
+
+    def go(st):
+        Q, K, V = out if out is not None else (
+            torch.empty(B, Hq, N, d, dtype=q.dtype, device=dev),
+            torch.empty(B, Hkv, N, d, dtype=q.dtype, device=dev),
+            None if v is None else torch.empty(B, Hkv, N, d, dtype=q.dtype, device=dev))
+        oq = _heads(where, "Q", Q, (B, Hq, N, d), act, dev, 2, True)
+        ok = _heads(where, "K", K, (B, Hkv, N, d), act, dev, 2, True)
+        ov = None if v is None else _heads(where, "V", V, (B, Hkv, N, d), act, dev, 2, True)
+        _check(lib.gbs_qkv_rope_fwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _opt(hv), _ptr(wq),
+                                    _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos), ctypes.byref(oq),
+                                    ctypes.byref(ok), _opt(ov), _ptr(ws), st), where)
+        return Q, K, V
+
+    return _called(dev, stream, go)
+
+
+def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, eps=1e-6, axes=None,
+                      interleaved=False, grads=None, ws=None, stream=None):
+    """Backward of ``qkv_rope`` with the same arguments: from dQ [B, Hq, N, d], dK and
+    dV [B, Hkv, N, d] (what ``backward`` returns; dV may be None) to
+    (dq, dk, dv, dwq, dwk): dq [B, N, Hq, d], dk, dv [B, N, Hkv, d] and fp32
+    dwq, dwk [d] (None without weights). ``grads``: (dq, dk, dv) to write to,
+    such as parts of one packed tensor."""
+    where = "gbs_qkv_rope_bwd"
+    lib = load_library()
+    p, dev = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved)
+    B, N, Hq, d, Hkv, act = p.B, p.N, p.Hq, p.d, p.Hkv, (q.dtype,)
+    hq = _heads(where, "q", q, (B, N, Hq, d), act, dev)
+    hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev)
+    zq = _heads(where, "dQ", dQ, (B, Hq, N, d), act, dev, 2)
+    zk = _heads(where, "dK", dK, (B, Hkv, N, d), act, dev, 2)
+    zv = None if dV is None else _heads(where, "dV", dV, (B, Hkv, N, d), act, dev, 2)
+    if grads is not None and (len(grads) != 3 or (grads[2] is None) != (dV is None)):
+        raise _invalid(where, "grads must be (dq, dk, dv), dv None exactly if dV is")
+    if ws is not None:
+        _need(where, "ws", ws, None, _U8, dev)
+
+    def go(st):
+        dq, dk, dv = grads if grads is not None else (
+            torch.empty(B, N, Hq, d, dtype=q.dtype, device=dev),
+            torch.empty(B, N, Hkv, d, dtype=q.dtype, device=dev),
+            None if dV is None else torch.empty(B, N, Hkv, d, dtype=q.dtype, device=dev))
+        oq = _heads(where, "dq", dq, (B, N, Hq, d), act, dev, 1, True)
+        ok = _heads(where, "dk", dk, (B, N, Hkv, d), act, dev, 1, True)
+        ov = None if dV is None else _heads(where, "dv", dv, (B, N, Hkv, d), act, dev, 1, True)
+        dwq, dwk = (None, None) if wq is None else torch.empty(2, d, dtype=torch.float32, device=dev).unbind()
+        scratch = ws
+        if scratch is None:
+            scratch = torch.empty(lib.gbs_qkv_rope_workspace_bytes(ctypes.byref(p)) or 256, dtype=torch.uint8,
+                                  device=dev)
+        _check(lib.gbs_qkv_rope_bwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _ptr(wq), _ptr(wk),
+                                    _ptr(cos), _ptr(sin), _ptr(pos), ctypes.byref(zq), ctypes.byref(zk),
+                                    _opt(zv), ctypes.byref(oq), ctypes.byref(ok), _opt(ov), _ptr(dwq),
+                                    _ptr(dwk), _ptr(scratch), scratch.numel(), st), where)
+        return dq, dk, dv, dwq, dwk
+
+    return _called(dev, stream, go)
+
+
+def qkv_rope_workspace_bytes(q, k, rot):
+    """Bytes of ``ws`` for ``qkv_rope_backward`` (``qkv_rope`` takes the same one)."""
+    B, N, Hq, d = q.shape
+    p = RopeParams(B, N, Hq, k.shape[2], d, rot, 0, 1, (ctypes.c_ubyte * 64)(), 1, DTYPES[q.dtype], 1, 0.0)
+    n = int(load_library().gbs_qkv_rope_workspace_bytes(ctypes.byref(p)))
+    if n == 0:
+        raise GbsError(1, "gbs_qkv_rope_workspace_bytes", load_library().gbs_last_error().decode())
+    return n
+
+
+def kv4_cache(B, Hkv, d, L=None, num_pages=None, block=64, device="cuda"):
+    """A 4-bit cache (codes and parameters of keys, then of values) of zeros:
+    contiguous for B sequences of up to L tokens, or ``num_pages`` pages."""
+    if (L is None) == (num_pages is None):
+        raise _invalid("kv4_cache", "give either L or num_pages")
+    rows = (num_pages, Hkv, block) if L is None else (B, Hkv, -(-L // block) * block)
+    out = []
+    for _ in range(2):
+        out += [torch.zeros(*rows, d // 2, dtype=torch.uint8, device=device),
+                torch.zeros(*rows, d // 32, 2, dtype=torch.float16, device=device)]
+    return tuple(out)
+
+
+def _check_kv4(where, cache, B, d, device, block, block_table):
+    """(gbs_kv4_cache, Hkv, longest length that fits) of a 4-bit cache: four
+    tensors, codes [B, Hkv, cap, d / 2] uint8 and parameters [B, Hkv, cap, d / 32, 2]
+    fp16 of keys and of values, or pages [num_pages, Hkv, block, ...]."""
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
+        raise _invalid(where, "cache must be (key codes, key parameters, value codes, value parameters)")
+    kc = cache[0]
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
+        raise _invalid(where, "key codes must be 4-D")
+    first, Hkv, rows, _ = kc.shape
+    if block_table is None:
+        if first != B or rows % block:
+            raise _invalid(where, f"key codes have shape {tuple(kc.shape)}; expected ({B}, Hkv, a multiple of "
+                                  f"{block}, {d // 2})")
+    elif rows != block:
+        raise _invalid(where, f"a page of the key codes has {rows} rows; expected {block}")
+    for i, name in enumerate(("key codes", "key parameters", "value codes", "value parameters")):
+        if i % 2:
+            _need(where, name, cache[i], (first, Hkv, rows, d // 32, 2), _F16, device)
+        else:
+            _need(where, name, cache[i], (first, Hkv, rows, d // 2), _U8, device)
+    table = None
+    if block_table is not None:
+        _need(where, "block_table", block_table, None, _I32, device)
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise _invalid(where, f"block_table must be [B={B}, max_blocks]")
+        table = block_table.data_ptr()
+    desc = Kv4CacheDesc(*(t.data_ptr() for t in cache), table, 0 if table is None else block_table.shape[1],
+                        0 if table is None else first, rows)
+    return desc, Hkv, rows if block_table is None else block_table.shape[1] * block
+
+
+def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out):
+    dev = _device(where, "K", K)
+    if K.dim() != 4:
+        raise _invalid(where, "K must be [B, Hkv, T, d]")
+    B, _, T, d = K.shape
+    _act_dtype(where, "K", K)
+    desc, Hkv, L = _check_kv4(where, cache, B, d, dev, block, block_table)
+    hk = _heads(where, "K", K, (B, Hkv, T, d), (K.dtype,), dev, 2, out)
+    hv = _heads(where, "V", V, (B, Hkv, T, d), (K.dtype,), dev, 2, out)
+    _need(where, "start", start, (B,), _I32, dev)
+    if count is not None:
+        _need(where, "count", count, (B,), _I32, dev)
+    if ws is not None:
+        _need(where, "ws", ws, None, _U8, dev)
+        if ws.numel() < 256:
+            raise GbsError(5, where, "ws must have at least 256 bytes")
+    if T == 0:
+        return lambda st: None
+    p = make_params(B, Hkv, Hkv, L, d, block, dtype=K.dtype)
+    return lambda st: _check(fn(ctypes.byref(p), ctypes.byref(desc), ctypes.byref(hk), ctypes.byref(hv), T,
+                                _ptr(start), _ptr(count), _ptr(ws), st), where)
+
+
+def kv4_append(K, V, cache, start, block_table=None, count=None, block=64, ws=None, stream=None):
+    """Writes K and V [B, Hkv, T, d] (any strides with contiguous channels) into a
+    4-bit cache (``kv4_cache``), token t of sequence b at position start[b] + t
+    (``start`` int32 [B]); with ``count`` (int32 [B]) only its first count[b]
+    tokens. ``block_table`` (int32 [B, max_blocks]) makes the cache page pools."""
+    fn = load_library().gbs_kv4_append
+    _called(_device("gbs_kv4_append", "K", K), stream,
+            _kv4_rows("gbs_kv4_append", fn, K, V, cache, start, block_table, count, ws, block, False))
+
+
+def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16, block=64, out=None, ws=None,
+             stream=None):
+    """The values of T tokens of every sequence from position ``start`` on:
+    (K, V) [B, Hkv, T, d] of ``dtype`` (``out`` to write to, strided too); tokens
+    from count[b] on are zeros."""
+    where = "gbs_kv4_read"
+    fn = load_library().gbs_kv4_read
+    dev = _device(where, "start", start)
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4 or not isinstance(cache[0], torch.Tensor) \
+            or cache[0].dim() != 4:
+        raise _invalid(where, "cache must be (key codes, key parameters, value codes, value parameters)")
+    if dtype not in DTYPES:
+        raise _invalid(where, f"dtype {dtype}; expected torch.bfloat16 or torch.float32")
+    if T < 0:
+        raise _invalid(where, "T must not be negative")
+
+    def go(st):
+        shape = (start.shape[0], cache[0].shape[1], T, 2 * cache[0].shape[3])
+        K, V = out if out is not None else (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
+        _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, True)(st)
+        return K, V
+
+    return _called(dev, stream, go)
+
+
+def kv4_workspace_bytes(params: Params) -> int:
+    return int(load_library().gbs_kv4_workspace_bytes(ctypes.byref(params)))
+
+
+def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block_table=None, seq_lens=None,
+               group_shared=False, out=None, lse=None, ws=None, tau=None, stream=None):
+    """gbs_kv4_decode: ``decode_ex`` over a 4-bit cache (``kv4_cache``). q [B, Hq, d]
+    (bf16 or fp32), S [B, Hq, ceil(L / block)] (group-shared: [B, Hkv, ..]) fp32,
+    ``L`` the longest length; ``seq_lens`` int32 [B] may hold 0 for an idle slot,
+    whose O is 0 and LSE -inf. Returns (O, LSE)."""
+    where = "gbs_kv4_decode"
+    lib = load_library()
+    dev = _device(where, "q", q)
+    if q.dim() != 3:
+        raise _invalid(where, "q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    act = _act_dtype(where, "q", q)
+    _need(where, "q", q, (B, Hq, d), act, dev)
+    desc, Hkv, most = _check_kv4(where, cache, B, d, dev, block, block_table)
+    if not 1 <= L <= most:
+        raise _invalid(where, f"L = {L} is outside [1, {most}], what the cache holds")
+    _need(where, "S", S, (B, Hkv if group_shared else Hq, -(-L // block)), _F32, dev)
+    if seq_lens is not None:
+        _need(where, "seq_lens", seq_lens, (B,), _I32, dev)
+    if out is not None:
+        _need(where, "O", out, (B, Hq, d), act, dev)
+    if lse is not None:
+        _need(where, "LSE", lse, (B, Hq), _F32, dev)
+    if ws is not None:
+        _need(where, "ws", ws, None, _U8, dev)
+    p = make_params(B, Hq, Hkv, L, d, block, topk, "sparse" if tau is None else "threshold", q.dtype, scale,
+                    0.0 if tau is None else tau)
+
+    def go(st):
+        O = out if out is not None else torch.empty_like(q)
+        LSE = lse if lse is not None else torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        scratch = ws
+        if scratch is None:
+            scratch = torch.empty(kv4_workspace_bytes(p) or 256, dtype=torch.uint8, device=dev)
+        _check(lib.gbs_kv4_decode(ctypes.byref(p), ctypes.byref(desc), _ptr(seq_lens), 1 if group_shared else 0,
+                                  _ptr(q), _ptr(S), _ptr(O), _ptr(LSE), num_splits, _ptr(scratch),
+                                  scratch.numel(), st), where)
+        return O, LSE
+
+    return _called(dev, stream, go)

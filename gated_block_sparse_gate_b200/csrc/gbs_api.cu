@@ -183,6 +183,30 @@ unsigned int* err_word(void* ws) { return reinterpret_cast<unsigned int*>(ws); }
 namespace gbs {
 void set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 gbs_status resolve_params(const gbs_params* in, int op, Problem* out) { return resolve(in, op, out); }
+gbs_status fail_status(gbs_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return s;
+}
+gbs_status resolve_heads(const gbs_heads* t, const char* name, int esize, bool optional, Heads* out) {
+  *out = Heads();
+  if (!t || !t->ptr) {
+    if (optional && !t) return GBS_OK;
+    return fail(GBS_ERR_INVALID_ARG, "%s is NULL", name);
+  }
+  if (!aligned16(t->ptr)) return fail(GBS_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  const int64_t st[] = {t->stride_b, t->stride_h, t->stride_n};
+  for (int64_t x : st)
+    if (x < 0 || x > ((int64_t)1 << 42) || (x * esize) % 16)
+      return fail(GBS_ERR_INVALID_ARG, "a stride of %s is not a multiple of 16 bytes in [0, 2^42]", name);
+  out->ptr = t->ptr;
+  out->sb = t->stride_b;
+  out->sh = t->stride_h;
+  out->sn = t->stride_n;
+  return GBS_OK;
+}
 
 cudaError_t decode_auto_splits(const Problem& p, bool grouped, int n_ent, int* splits) {
   // Shares of at most 17 blocks per CTA, and at least two waves of the split

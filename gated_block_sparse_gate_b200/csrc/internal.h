@@ -95,6 +95,27 @@ int decode_heads_per_cta(const Problem& p, bool grouped);
 // Decode split CTAs resident per SM for this configuration.
 int decode_resident_ctas(const Problem& p, bool grouped);
 
+// A [B, heads, N, d] tensor by its strides (elements), as the kernels take it.
+struct Heads {
+  void* ptr = nullptr;
+  long long sb = 0, sh = 0, sn = 0;
+};
+// Validates a gbs_heads (NULL unless `optional`, alignment, strides) into *out.
+gbs_status resolve_heads(const gbs_heads* t, const char* name, int esize, bool optional, Heads* out);
+// Sets gbs_last_error() from a format and returns `s`.
+gbs_status fail_status(gbs_status s, const char* fmt, ...);
+
+// 4-bit cache: where the rows of (sequence, kv head) live.
+struct Kv4 {
+  uint8_t* kc = nullptr;
+  uint32_t* kp = nullptr;  // one word per group: fp16 scale (low half), fp16 minimum
+  uint8_t* vc = nullptr;
+  uint32_t* vp = nullptr;
+  const int32_t* btab = nullptr;
+  int max_blocks = 0, num_pages = 0, cap = 0;
+  unsigned int* err = nullptr;
+};
+
 // Tensor-core path (sm_100a, bf16). Returns cudaErrorNotSupported when the
 // configuration is outside what the kernel handles.
 cudaError_t launch_fwd_tc(const Problem& p, const void* Q, const void* K, const void* V,

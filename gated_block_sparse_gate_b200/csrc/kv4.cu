@@ -1,0 +1,514 @@
+// kv4.cu — key/value cache held in 4 bits: rows written, read back, and the
+// gated sparse decode over it.
+//
+// A group of 32 channels of one token and head is stored as fp16 (scale s,
+// minimum m) and codes n in 0..15; a code stands for m + s n. Channel c has
+// nibble c % 4 of the row's 16-bit word (c % 32) / 4 * (d / 32) + c / 32.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gbs {
+namespace {
+
+constexpr int kBS = 64;
+constexpr float kMaxValue = 60000.f;  // below fp16's largest, so that m + 15 s cannot overflow it
+
+// Four channels of a row as one load.
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+struct RowArgs {
+  int B, Hkv, T, N;
+  Kv4 c;
+  Heads t[2];  // keys, values [B, Hkv, T, d]
+  const int32_t *start, *count;
+};
+
+// Index of token t of sequence b, head h among the cache's rows, or -1.
+__device__ __forceinline__ long long cache_row(const RowArgs& a, int b, int h, int t) {
+  const int s = __ldg(a.start + b);
+  const long long pos = (long long)s + t;
+  if (pos < 0 || pos >= a.N) {
+    set_error(a.c.err, GBS_ERR_INVALID_ARG);
+    return -1;
+  }
+  if (!a.c.btab) return ((long long)b * a.Hkv + h) * a.c.cap + pos;
+  const int page = __ldg(a.c.btab + (size_t)b * a.c.max_blocks + pos / kBS);
+  if (page < 0 || page >= a.c.num_pages) {
+    set_error(a.c.err, GBS_ERR_INVALID_ARG);
+    return -1;
+  }
+  return ((long long)page * a.Hkv + h) * kBS + pos % kBS;
+}
+
+__device__ __forceinline__ int token_count(const RowArgs& a, int b) {
+  if (!a.count) return a.T;
+  const int n = __ldg(a.count + b);
+  if (n < 0 || n > a.T) {
+    set_error(a.c.err, GBS_ERR_INVALID_ARG);
+    return n < 0 ? 0 : a.T;
+  }
+  return n;
+}
+
+// fp16((hi - m) / 15) as through 64 bits: the fp32 product is within 2^-22 of the
+// quotient, so it decides unless the fp16 on both sides of it differ.
+__device__ __forceinline__ __half group_scale(float hi, float m) {
+  const float q = (hi - m) * (1.f / 15.f);
+  const __half a = __float2half_rn(q * (1.f - 0x1p-20f)), b = __float2half_rn(q * (1.f + 0x1p-20f));
+  if (__half_as_ushort(a) == __half_as_ushort(b)) return a;
+  return __float2half_rn((float)(((double)hi - (double)m) / 15.0));
+}
+
+// (x - m) / s rounded and limited as in 64 bits: fp32 is off by less than 2^-16
+// in 0..15, so only quotients that near to a half are computed in 64 bits.
+__device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv) {
+  const float t = (x - m) * inv;
+  float n = rintf(t);
+  if (fabsf(fabsf(t - n) - 0.5f) < 0x1p-14f) n = (float)rint(((double)x - (double)m) / (double)s);
+  return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+}
+
+// One row by D / 4 lanes, four channels each; a group's 8 lanes find its
+// extremes by shuffles.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int LANES = D / 4, NG = D / 32;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
+  const int lane = threadIdx.x % LANES, grp = lane / 8, chunk = lane % 8;
+  const long long rows = (long long)a.B * a.Hkv * a.T;
+  const Heads& src = blockIdx.y ? a.t[1] : a.t[0];
+  long long at = -1;
+  float x[4] = {};
+  if (row < rows) {
+    const int t = (int)(row % a.T), bh = (int)(row / a.T), b = bh / a.Hkv, h = bh % a.Hkv;
+    if (t < token_count(a, b)) at = cache_row(a, b, h, t);
+    if (at >= 0)
+      load4(reinterpret_cast<const T*>(src.ptr) + b * src.sb + h * src.sh + t * src.sn + 4 * lane, x);
+  }
+  float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+  float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  int bad = isnan(x[0]) || isnan(x[1]) || isnan(x[2]) || isnan(x[3]);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+  }
+  if (at < 0) return;
+  lo = fminf(fmaxf(lo, -kMaxValue), kMaxValue);
+  hi = fminf(fmaxf(hi, -kMaxValue), kMaxValue);
+  const __half m = __float2half_rn(lo);
+  const float mf = __half2float(m);
+  const __half s = group_scale(hi, mf);
+  const float sf = __half2float(s);
+  uint32_t word = 0, param = 0x7fff7fffu;
+  if (!bad) {
+    param = (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(m) << 16;
+    const float inv = 1.f / sf;
+    if (sf > 0.f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) word |= code_of(x[i], mf, sf, inv) << (4 * i);
+  }
+  uint16_t* codes = reinterpret_cast<uint16_t*>(blockIdx.y ? a.c.vc : a.c.kc);
+  uint32_t* params = blockIdx.y ? a.c.vp : a.c.kp;
+  codes[at * (D / 4) + chunk * NG + grp] = (uint16_t)word;
+  if (chunk == 0) params[at * NG + grp] = param;
+}
+
+__device__ __forceinline__ float low_half(uint32_t w) {
+  return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
+}
+__device__ __forceinline__ float high_half(uint32_t w) {
+  return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int LANES = D / 4, NG = D / 32;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
+  const int lane = threadIdx.x % LANES, grp = lane / 8, chunk = lane % 8;
+  if (row >= (long long)a.B * a.Hkv * a.T) return;
+  const Heads& dst = blockIdx.y ? a.t[1] : a.t[0];
+  const int t = (int)(row % a.T), bh = (int)(row / a.T), b = bh / a.Hkv, h = bh % a.Hkv;
+  const long long at = t < token_count(a, b) ? cache_row(a, b, h, t) : -1;
+  float x[4] = {};
+  if (at >= 0) {
+    const uint32_t word = reinterpret_cast<const uint16_t*>(blockIdx.y ? a.c.vc : a.c.kc)[at * (D / 4) + chunk * NG + grp];
+    const uint32_t param = (blockIdx.y ? a.c.vp : a.c.kp)[at * NG + grp];
+    const float s = low_half(param), m = high_half(param);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fmaf(s, (float)(word >> (4 * i) & 15u), m);
+  }
+  store4(reinterpret_cast<T*>(dst.ptr) + b * dst.sb + h * dst.sh + t * dst.sn + 4 * lane, x);
+}
+
+// ------------------------------------------------------------------ decode
+
+struct DecodeArgs {
+  Problem p;
+  Kv4 c;
+  Selection sel;
+  const int32_t* seq_lens;
+  const void* q;
+  void* O;
+  float *LSE, *part_ml, *part_acc;
+  int grouped, splits;
+};
+
+__device__ __forceinline__ int sequence_length(const DecodeArgs& a, int b) {
+  if (!a.seq_lens) return a.p.N;
+  const int L = __ldg(a.seq_lens + b);
+  if (L < 0 || L > a.p.N) {
+    set_error(a.c.err, GBS_ERR_INVALID_ARG);
+    return L < 0 ? 0 : a.p.N;
+  }
+  return L;
+}
+
+// First cache row of block c of (b, kvh), or -1 for a page outside the pool.
+__device__ __forceinline__ long long block_row(const DecodeArgs& a, int b, int kvh, int c) {
+  if (!a.c.btab) return ((long long)b * a.p.Hkv + kvh) * a.c.cap + c * kBS;
+  const int page = __ldg(a.c.btab + (size_t)b * a.c.max_blocks + c);
+  if (page < 0 || page >= a.c.num_pages) {
+    set_error(a.c.err, GBS_ERR_INVALID_ARG);
+    return -1;
+  }
+  return ((long long)page * a.p.Hkv + kvh) * kBS;
+}
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// One query head and split per CTA, all in fp32. A lane holds 32 channels of a
+// row (16 code bytes), so D / 32 lanes hold a row and a warp 32 / (D / 32) rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int NG = D / 32, LANES = NG, ROWS = 128 / LANES;
+  __shared__ float s_acc[4][D], s_m[4], s_l[4];
+  const Problem& p = a.p;
+  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, split = blockIdx.y, kvh = hq / p.G;
+  const int srow = a.grouped ? b * p.Hkv + kvh : blockIdx.x;
+  const int lane = threadIdx.x % LANES, row_in = threadIdx.x / LANES;
+  const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
+  const int n_hist = L > 0 ? dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err) : 0;
+  const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
+  const int e0 = split * per, e1 = min(n_ent, e0 + per);
+  // 16-bit word 8 lane + i / 4 holds channels 4 chunk + i % 4 of group grp
+  float q[32], acc[32] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int hw = 8 * lane + i / 4, c = 32 * (hw % NG) + 4 * (hw / NG) + i % 4;
+    q[i] = to_f32<T>(reinterpret_cast<const T*>(a.q)[((size_t)b * p.Hq + hq) * D + c]) * p.scale_log2;
+  }
+  for (int e = e0; e < e1; ++e) {
+    const bool is_cur = e == n_hist;
+    const int c = is_cur ? cur : dcheck(a.sel.idx[(size_t)srow * p.topk + e], 0, cur - 1, a.c.err);
+    const float bias = is_cur ? 0.f : a.sel.logg[(size_t)srow * p.topk + e] * GBS_LOG2E;
+    const long long row0 = block_row(a, b, kvh, c);
+    if (row0 < 0) continue;
+    const int nrows = is_cur ? L - cur * kBS : kBS;
+    for (int r = row_in; r < kBS; r += ROWS) {
+      float z = 0.f;
+      const bool there = r < nrows;
+      const long long at = row0 + (there ? r : 0);
+      const uint4 kw = __ldg(reinterpret_cast<const uint4*>(a.c.kc + at * (D / 2)) + lane);
+      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+      float ks[NG], km[NG], vs[NG], vm[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t kp = __ldg(a.c.kp + at * NG + g), vp = __ldg(a.c.vp + at * NG + g);
+        ks[g] = low_half(kp); km[g] = high_half(kp);
+        vs[g] = low_half(vp); vm[g] = high_half(vp);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int g = (i / 4) % NG;
+        z = fmaf(q[i], fmaf(ks[g], (float)(w[i / 8] >> (4 * (i % 8)) & 15u), km[g]), z);
+      }
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      if (!there) continue;
+      z += bias;
+      if (z > m) {
+        const float f = exp2f(m - z);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] *= f;
+        m = z;
+      }
+      // a NaN or infinite score leaves m where it was and makes the row's sum NaN
+      const float pr = exp2f(z - m);
+      l += pr;
+      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(a.c.vc + at * (D / 2)) + lane);
+      const uint32_t x[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int g = (i / 4) % NG;
+        acc[i] = fmaf(pr, fmaf(vs[g], (float)(x[i / 8] >> (4 * (i % 8)) & 15u), vm[g]), acc[i]);
+      }
+    }
+  }
+  // join the rows of a warp, then the warps
+  float M = m;
+#pragma unroll
+  for (int o = LANES; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+  l *= f;
+#pragma unroll
+  for (int o = LANES; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const int warp = threadIdx.x / 32;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float v = m == -INFINITY ? acc[i] : acc[i] * f;
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int hw = 8 * lane + i / 4;
+    if (threadIdx.x % 32 < LANES) s_acc[warp][32 * (hw % NG) + 4 * (hw / NG) + i % 4] = v;
+  }
+  if (threadIdx.x % 32 == 0) s_m[warp] = M, s_l[warp] = l;
+  __syncthreads();
+  float MM = -INFINITY, ll = 0.f;
+  for (int w = 0; w < 4; ++w) MM = fmaxf(MM, s_m[w]);
+  float fw[4];
+  for (int w = 0; w < 4; ++w) {
+    fw[w] = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - MM);
+    ll += s_l[w] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
+  }
+  const size_t row = (size_t)b * p.Hq + hq, part = row * a.splits + split;
+  for (int c = threadIdx.x; c < D; c += 128) {
+    float v = 0.f;
+    for (int w = 0; w < 4; ++w) v += s_acc[w][c] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
+    a.part_acc[part * D + c] = v;
+  }
+  if (threadIdx.x == 0) {
+    a.part_ml[part * 2] = MM;
+    a.part_ml[part * 2 + 1] = ll;
+  }
+}
+
+// Joins the splits of a row: one warp each. A row without a key (a length of 0)
+// gives 0 and -infinity.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant__ DecodeArgs a) {
+  const int row = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (row >= a.p.B * a.p.Hq) return;
+  float M = -INFINITY, l = 0.f, acc[D / 32] = {};
+  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[((size_t)row * a.splits + s) * 2]);
+  for (int s = 0; s < a.splits; ++s) {
+    const size_t part = (size_t)row * a.splits + s;
+    const float m = a.part_ml[part * 2], f = m == -INFINITY ? 1.f : exp2f(m - M);
+    l += a.part_ml[part * 2 + 1] * f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] += a.part_acc[part * D + lane + 32 * i] * f;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    store_out(reinterpret_cast<T*>(a.O) + (size_t)row * D + lane + 32 * i, acc[i] * inv);
+  if (lane == 0) a.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
+}
+
+template <typename T, int D>
+cudaError_t launch_decode4(const DecodeArgs& a, cudaStream_t st) {
+  const int rows = a.p.B * a.p.Hq;
+  timer_begin(GBS_OP_DECODE, st);
+  kv4_decode_simt_kernel<T, D><<<dim3(rows, a.splits), 128, 0, st>>>(a);
+  timer_end(GBS_OP_DECODE, st);
+  note_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  kv4_combine_kernel<T, D><<<(rows + 3) / 4, 128, 0, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ arguments
+
+gbs_status resolve_cache(const Problem& p, const gbs_kv4_cache* in, Kv4* out) {
+  if (!in) return fail_status(GBS_ERR_INVALID_ARG, "cache is NULL");
+  const void* ptrs[] = {in->kc, in->kp, in->vc, in->vp};
+  const char* names[] = {"kc", "kp", "vc", "vp"};
+  for (int i = 0; i < 4; ++i) {
+    if (!ptrs[i]) return fail_status(GBS_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if ((uintptr_t)ptrs[i] & 15u) return fail_status(GBS_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  if (in->block_table) {
+    if (in->max_blocks < p.Nb)
+      return fail_status(GBS_ERR_INVALID_ARG, "max_blocks (%d) is below ceil(N / block) = %d", in->max_blocks, p.Nb);
+    if (in->num_pages <= 0) return fail_status(GBS_ERR_INVALID_ARG, "num_pages must be positive");
+    if ((uintptr_t)in->block_table & 3u)
+      return fail_status(GBS_ERR_INVALID_ARG, "block_table is not 4-byte aligned");
+  } else if (in->cap < p.N || in->cap % p.bs) {
+    return fail_status(GBS_ERR_INVALID_ARG, "cap (%d) must be a multiple of block and at least N = %d", in->cap, p.N);
+  }
+  out->kc = static_cast<uint8_t*>(in->kc);
+  out->kp = static_cast<uint32_t*>(in->kp);
+  out->vc = static_cast<uint8_t*>(in->vc);
+  out->vp = static_cast<uint32_t*>(in->vp);
+  out->btab = in->block_table;
+  out->max_blocks = in->max_blocks;
+  out->num_pages = in->num_pages;
+  out->cap = in->cap;
+  return GBS_OK;
+}
+
+gbs_status cuda_done(cudaError_t e, const char* where) {
+  return e == cudaSuccess ? GBS_OK : fail_status(GBS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
+
+// Append (READ = false) and read share everything but their kernel.
+template <bool READ>
+gbs_status rows_call(const char* where, const gbs_params* in, const gbs_kv4_cache* cache, const gbs_heads* K,
+                     const gbs_heads* V, int T, const int32_t* start, const int32_t* count, void* ws,
+                     void* stream) {
+  set_last_error("");
+  Problem p{};
+  gbs_status s = resolve_params(in, GBS_OP_DECODE, &p);
+  if (s != GBS_OK) return s;
+  RowArgs a{};
+  if ((s = resolve_cache(p, cache, &a.c)) != GBS_OK) return s;
+  const int es = p.dtype == GBS_BF16 ? 2 : 4;
+  if ((s = resolve_heads(K, "K", es, false, &a.t[0])) != GBS_OK) return s;
+  if ((s = resolve_heads(V, "V", es, false, &a.t[1])) != GBS_OK) return s;
+  if (T < 0) return fail_status(GBS_ERR_INVALID_ARG, "T must not be negative");
+  if (!start) return fail_status(GBS_ERR_INVALID_ARG, "start is NULL");
+  if (((uintptr_t)start | (uintptr_t)count) & 3u)
+    return fail_status(GBS_ERR_INVALID_ARG, "start or count is not 4-byte aligned");
+  if ((uintptr_t)ws & 255u) return fail_status(GBS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  const long long rows = (long long)p.B * p.Hkv * T;
+  if (rows > INT32_MAX) return fail_status(GBS_ERR_INVALID_ARG, "problem too large: B * Hkv * T must be below 2^31");
+  if (rows == 0) return GBS_OK;
+  a.B = p.B; a.Hkv = p.Hkv; a.T = T; a.N = p.N;
+  a.start = start; a.count = count;
+  a.c.err = static_cast<unsigned int*>(ws);
+  const int rows_per_cta = 256 / (p.d / 4);
+  const dim3 grid((unsigned)((rows + rows_per_cta - 1) / rows_per_cta), 2);
+  cudaStream_t st = (cudaStream_t)stream;
+#define GBS_ROWS(T_, D_)                                       \
+  do {                                                         \
+    if (READ) kv4_read_kernel<T_, D_><<<grid, 256, 0, st>>>(a); \
+    else kv4_append_kernel<T_, D_><<<grid, 256, 0, st>>>(a);   \
+  } while (0)
+  if (p.dtype == GBS_BF16) {
+    if (p.d == 64) GBS_ROWS(__nv_bfloat16, 64);
+    else GBS_ROWS(__nv_bfloat16, 128);
+  } else {
+    if (p.d == 64) GBS_ROWS(float, 64);
+    else GBS_ROWS(float, 128);
+  }
+#undef GBS_ROWS
+  note_launch();
+  return cuda_done(cudaGetLastError(), where);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t carve_kv4(const Problem& p, char* base, DecodeArgs* a) {
+  size_t off = 256;  // the device error word
+  const size_t rows = (size_t)p.B * p.Hq;
+  auto take = [&](size_t bytes) {
+    char* at = base + off;
+    off += up256(bytes);
+    return at;
+  };
+  a->sel.idx = reinterpret_cast<int32_t*>(take(rows * p.topk * 4));
+  a->sel.cnt = reinterpret_cast<int32_t*>(take(rows * 4));
+  a->sel.logg = reinterpret_cast<float*>(take(rows * p.topk * 4));
+  a->part_ml = reinterpret_cast<float*>(take(rows * kMaxDecodeSplits * 8));
+  a->part_acc = reinterpret_cast<float*>(take(rows * kMaxDecodeSplits * p.d * 4));
+  return off;
+}
+
+}  // namespace
+}  // namespace gbs
+
+using namespace gbs;
+
+extern "C" gbs_status gbs_kv4_append(const gbs_params* p, const gbs_kv4_cache* cache, const gbs_heads* K,
+                                     const gbs_heads* V, int T, const int32_t* start, const int32_t* count,
+                                     void* ws, void* stream) {
+  return rows_call<false>("gbs_kv4_append", p, cache, K, V, T, start, count, ws, stream);
+}
+
+extern "C" gbs_status gbs_kv4_read(const gbs_params* p, const gbs_kv4_cache* cache, const gbs_heads* K,
+                                   const gbs_heads* V, int T, const int32_t* start, const int32_t* count,
+                                   void* ws, void* stream) {
+  return rows_call<true>("gbs_kv4_read", p, cache, K, V, T, start, count, ws, stream);
+}
+
+extern "C" size_t gbs_kv4_workspace_bytes(const gbs_params* in) {
+  set_last_error("");
+  Problem p{};
+  if (resolve_params(in, GBS_OP_DECODE, &p) != GBS_OK) return 0;
+  DecodeArgs a{};
+  return carve_kv4(p, nullptr, &a);
+}
+
+extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* cache, const int32_t* seq_lens,
+                                     int group_shared, const void* q, const float* S, void* O, float* LSE,
+                                     int num_splits, void* ws, size_t ws_bytes, void* stream) {
+  set_last_error("");
+  DecodeArgs a{};
+  Problem& p = a.p;
+  gbs_status s = resolve_params(in, GBS_OP_DECODE, &p);
+  if (s != GBS_OK) return s;
+  if ((s = resolve_cache(p, cache, &a.c)) != GBS_OK) return s;
+  const void* ptrs[] = {q, S, O, LSE};
+  const char* names[] = {"q", "S", "O", "LSE"};
+  for (int i = 0; i < 4; ++i) {
+    if (!ptrs[i]) return fail_status(GBS_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if ((uintptr_t)ptrs[i] & 15u) return fail_status(GBS_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  if (num_splits < 0 || num_splits > kMaxDecodeSplits)
+    return fail_status(GBS_ERR_INVALID_ARG, "num_splits %d outside [0, %d]", num_splits, kMaxDecodeSplits);
+  if (group_shared != 0 && group_shared != 1) return fail_status(GBS_ERR_INVALID_ARG, "group_shared must be 0 or 1");
+  if ((uintptr_t)seq_lens & 3u) return fail_status(GBS_ERR_INVALID_ARG, "seq_lens is not 4-byte aligned");
+  const size_t need = carve_kv4(p, static_cast<char*>(ws), &a);
+  if (!ws) return fail_status(GBS_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+  if ((uintptr_t)ws & 255u) return fail_status(GBS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  if (ws_bytes < need) return fail_status(GBS_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  a.c.err = static_cast<unsigned int*>(ws);
+  a.seq_lens = seq_lens;
+  a.q = q; a.O = O; a.LSE = LSE;
+  a.grouped = group_shared;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int cur_max = (p.N - 1) / p.bs;
+  SeqLens seq;
+  seq.lens = seq_lens;
+  seq.rows_per_seq = group_shared ? p.Hkv : p.Hq;
+  seq.max_len = p.N;
+  cudaError_t e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode,
+                                p.log_tau, a.sel.idx, a.sel.cnt, a.sel.logg, nullptr, st, nullptr, nullptr, 0, seq);
+  if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/select");
+  const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1;
+  a.splits = num_splits;
+  if (a.splits == 0) {
+    e = decode_auto_splits(p, false, n_ent, &a.splits);
+    if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/splits");
+  }
+  if (a.splits > n_ent) a.splits = n_ent;
+  if (p.dtype == GBS_BF16)
+    e = p.d == 64 ? launch_decode4<__nv_bfloat16, 64>(a, st) : launch_decode4<__nv_bfloat16, 128>(a, st);
+  else
+    e = p.d == 64 ? launch_decode4<float, 64>(a, st) : launch_decode4<float, 128>(a, st);
+  return cuda_done(e, "gbs_kv4_decode");
+}

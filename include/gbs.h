@@ -279,6 +279,143 @@ GBS_API gbs_status gbs_decode_noalloc(const gbs_params* p, const void* q, const 
                                       const void* Vc, const float* S, void* O, float* LSE,
                                       int num_splits, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys with rotary positions, in one pass (no counterpart
+ * in the paper, which starts from Q, K and V: this is the step that makes them
+ * from a model's projections).
+ *
+ * One row is one token of one head, d channels x. With r = 1 / sqrt(mean x^2 +
+ * eps) and weights w, y = x r w (y = x without weights); the first `rot`
+ * channels are then rotated in pairs (a, b):
+ *   a' = a c - b s,  b' = b c + a s,  c = cos_tab[pos[axis[i]]][i], s alike,
+ * for pair i < rot / 2: channels (i, i + rot / 2), or (2 i, 2 i + 1) with
+ * `interleaved`. Channels from rot on pass through. Values are turned into the
+ * attention's head-major tensors on the way. All arithmetic is fp32, rounded
+ * once when a result is stored. */
+
+/* A [B, heads, N, d] tensor with any order and spacing of its batch, head and
+ * token dimensions; channels are contiguous. Strides are in elements, multiples
+ * of 16 bytes, not negative; ptr is 16-byte aligned. A dimension of one may have
+ * any stride that keeps this rule. */
+typedef struct gbs_heads {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_n;
+} gbs_heads;
+
+typedef struct gbs_rope_params {
+  int B, N;             /* batch, tokens (any length, one included)               */
+  int Hq, Hkv, d;       /* heads; d in {64, 128}; Hq need not divide by Hkv        */
+  int rot;              /* rotated channels: a multiple of 8, 0 <= rot <= d        */
+  int interleaved;      /* pairs of neighbours (1) or of halves (0)                */
+  int n_axes;           /* position axes, 1 .. 4                                   */
+  unsigned char axis[64]; /* axis[i] < n_axes of pair i, i < rot / 2               */
+  int max_pos;          /* rows of the cos / sin tables                            */
+  int dtype;            /* gbs_dtype of q, k, v, Q, K, V and their gradients       */
+  int w_dtype;          /* gbs_dtype of wq, wk                                     */
+  float eps;            /* finite, >= 0                                            */
+} gbs_rope_params;
+
+/* Bytes of workspace for gbs_qkv_rope_bwd (0 if the parameters are invalid),
+ * 256-byte aligned device memory. gbs_qkv_rope_fwd needs the first 256 bytes. */
+GBS_API size_t gbs_qkv_rope_workspace_bytes(const gbs_rope_params* p);
+
+/*   q, k, v   inputs [B, Hq | Hkv, N, d]; v and V both NULL leave values out.
+ *   wq, wk    [d] weights, both or neither (NULL: no norm).
+ *   cos_tab, sin_tab  [max_pos, rot / 2] fp32 (not read with rot = 0).
+ *   pos       [B, N, n_axes] int32; a position outside [0, max_pos) is clamped
+ *             and reported by gbs_check(ws) as GBS_ERR_INVALID_ARG.
+ *   Q, K, V   outputs, the same shapes; they must not overlap the inputs.
+ *   ws        NULL (nothing is reported) or device memory of >= 256 bytes. */
+GBS_API gbs_status gbs_qkv_rope_fwd(const gbs_rope_params* p, const gbs_heads* q,
+                                    const gbs_heads* k, const gbs_heads* v, const void* wq,
+                                    const void* wk, const float* cos_tab, const float* sin_tab,
+                                    const int32_t* pos, const gbs_heads* Q, const gbs_heads* K,
+                                    const gbs_heads* V, void* ws, void* stream);
+
+/* Gradients of gbs_qkv_rope_fwd: with g the rotation of dz by the negative
+ * angles, xh = x r and h = g w,
+ *   dx = r (h - xh mean(h xh)) (dx = g without weights),
+ *   dw = sum over batch, heads and tokens of g xh.
+ *   dQ, dK, dV  upstream gradients (what gbs_bwd returns); dV may be NULL.
+ *   dq, dk, dv  out; dv NULL exactly if dV is. They must not overlap the inputs.
+ *   dwq, dwk    [d] fp32 out, with weights only; sums in a fixed order, so equal
+ *               inputs give equal bits.
+ *   ws          gbs_qkv_rope_workspace_bytes(p) bytes. */
+GBS_API gbs_status gbs_qkv_rope_bwd(const gbs_rope_params* p, const gbs_heads* q,
+                                    const gbs_heads* k, const void* wq, const void* wk,
+                                    const float* cos_tab, const float* sin_tab,
+                                    const int32_t* pos, const gbs_heads* dQ,
+                                    const gbs_heads* dK, const gbs_heads* dV, const gbs_heads* dq,
+                                    const gbs_heads* dk, const gbs_heads* dv, float* dwq,
+                                    float* dwk, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Key/value cache held in 4 bits (no counterpart in the paper: a serving-side
+ * storage format of this library for the decode above).
+ *
+ * A row is one token of one head. Each 32 channels of it share an fp16 scale s
+ * and an fp16 minimum m, and a code n in 0..15 stands for m + s n:
+ *   lo, hi  smallest and largest of the 32 values, limited to +-60000
+ *   m = fp16(lo), s = fp16(fp32((hi - m) / 15))
+ *   n = (x - m) / s rounded to the nearest whole number (ties to even) and
+ *       limited to 0..15, as if computed in 64 bits; 0 where s = 0.
+ * A NaN among the 32 makes m and s NaN, so all 32 read back as NaN.
+ * Layout (d / 2 code bytes and d / 8 parameter bytes a row, 80 in all for d = 128
+ * against 256 in bf16): channel c has bits 4 (c % 4) .. + 3 of the row's
+ * little-endian 16-bit word (c % 32) / 4 * (d / 32) + c / 32, so that the words
+ * a tensor-core lane needs of every group lie side by side. Parameters are
+ * [d / 32][2] fp16: s then m of each group. */
+typedef struct gbs_kv4_cache {
+  void* kc;   /* key codes:   contiguous [B, Hkv, cap, d / 2] bytes, or pages     */
+              /*              [num_pages, Hkv, block, d / 2]                       */
+  void* kp;   /* key parameters, the same with [d / 32, 2] fp16                    */
+  void* vc;   /* value codes                                                       */
+  void* vp;   /* value parameters; all four 16-byte aligned                        */
+  const int32_t* block_table; /* NULL: contiguous; else as in gbs_kv_layout        */
+  int max_blocks, num_pages;  /* as in gbs_kv_layout (num_pages without its limit) */
+  int cap;    /* contiguous: rows of a head, a multiple of block, >= p->N          */
+} gbs_kv4_cache;
+
+/* Writes T tokens of every sequence into the cache: token t of sequence b goes
+ * to position start[b] + t.
+ *   p      B, Hkv, N (longest length a sequence may reach), d, block and dtype
+ *          are read.
+ *   K, V   [B, Hkv, T, d] in p->dtype.
+ *   start  [B] int32; count NULL or [B] int32: only tokens t < count[b] are
+ *          written (a padded batch); rows not written keep their contents.
+ *   A token whose position is outside [0, N) or whose page is outside the pool
+ *   is left out, and count[b] outside [0, T] is clamped; both are reported by
+ *   gbs_check(ws) as GBS_ERR_INVALID_ARG. Two tokens of one call must not go to
+ *   the same row (two sequences that share a page they both write).
+ *   ws     NULL (nothing is reported) or device memory of >= 256 bytes.
+ *   T = 0 does nothing. */
+GBS_API gbs_status gbs_kv4_append(const gbs_params* p, const gbs_kv4_cache* cache,
+                                  const gbs_heads* K, const gbs_heads* V, int T,
+                                  const int32_t* start, const int32_t* count, void* ws,
+                                  void* stream);
+
+/* The values that T tokens of every sequence stand for, into K and V [B, Hkv,
+ * T, d] of p->dtype: m + s n in fp32, rounded once. Arguments as in
+ * gbs_kv4_append; tokens left out (t >= count[b], or a bad position or page) read as
+ * zeros. */
+GBS_API gbs_status gbs_kv4_read(const gbs_params* p, const gbs_kv4_cache* cache,
+                                const gbs_heads* K, const gbs_heads* V, int T,
+                                const int32_t* start, const int32_t* count, void* ws, void* stream);
+
+/* Bytes of workspace for gbs_kv4_decode (0 if the parameters are invalid). */
+GBS_API size_t gbs_kv4_workspace_bytes(const gbs_params* p);
+
+/* gbs_decode_ex over a 4-bit cache: the same selection, gates and outputs, with
+ * the keys and values that the cache's codes stand for. q and O are p->dtype.
+ *   seq_lens, group_shared  as in gbs_kv_layout, except that a length of 0 (an
+ *          idle slot of a batch) is valid: its O is 0 and its LSE -infinity.
+ *   S, LSE, num_splits  as in gbs_decode_ex.
+ *   ws     gbs_kv4_workspace_bytes(p) bytes. */
+GBS_API gbs_status gbs_kv4_decode(const gbs_params* p, const gbs_kv4_cache* cache,
+                                  const int32_t* seq_lens, int group_shared, const void* q,
+                                  const float* S, void* O, float* LSE, int num_splits, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
