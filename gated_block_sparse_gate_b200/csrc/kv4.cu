@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "sm100.cuh"
 
 namespace gbs {
 namespace {
@@ -305,6 +306,367 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
   }
 }
 
+// ------------------------------------------------------------ tensor-core decode
+// bf16 queries. A CTA serves up to eight query heads of one selection row (one
+// head without a shared selection) over its share of the kept blocks. A block's
+// codes and parameters (10,240 bytes for d = 128) arrive by bulk copies into a
+// ring of stages; each of four warps takes 16 of its 64 keys.
+//
+//   z[head, key] = sum_g s_g sum_{i in g} q_i n_i + sum_g m_g sum_{i in g} q_i
+// The inner sums are m16n8k16 products of q (rows: heads) and whole-number codes
+// as fp16, both exact: q is scaled by a power of two for each head so that it
+// fits, scales are applied to the fp32 sums, and the minima's part is one more
+// product of the raw parameter words with the sums of q as two fp16 terms.
+//   O[head, :] = sum_key p v,  v = m + s n rounded to fp16 (2^-12 of the value,
+// against the 2^-9 of the bf16 result); p as two fp16 terms, the second in the
+// eight rows of the product that no head uses, so that it costs nothing.
+// The product's key and channel order is free, so lanes take whole words of codes:
+// a thread's word of four channels (or two of them joined by one byte permute)
+// becomes operand registers by masking each nibble into the mantissa of 1024 or
+// 64 and subtracting that.
+// Bytes bound it (5 bits a value; 10,240 bytes a block); the unpacking costs about
+// 1,400 warp instructions a block, which is why K needs no multiplications.
+
+template <int D>
+struct Kv4Tile {
+  static constexpr int NG = D / 32, RB = D / 2, PB = NG * 4;
+  static constexpr int kKp = kBS * RB, kV = kKp + kBS * PB, kVp = kV + kBS * RB;
+  static constexpr int kStage = kVp + kBS * PB;
+  static constexpr int kStages = D == 128 ? 6 : 8;
+  static constexpr int kBytes = kStages * kStage;
+  static_assert(kBytes >= 4 * 8 * D * 4, "the warps' sums are joined in the stages' memory");
+};
+constexpr int kMmaThreads = 160;  // four warps of arithmetic, one of copies
+constexpr uint64_t kWaitNs = 4000000000ull;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+__device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return as_word(__floats2half2_rn(lo, hi)); }
+
+// Nibbles i = 0..3 of both halves of w as pairs of fp16 whole numbers.
+__device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
+  const uint32_t h = w >> 8;
+  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);  // 1024, 64
+  n[0] = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), big);
+  n[1] = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), small);
+  n[2] = __hsub2(as_half2((h & 0x000f000fu) | 0x64006400u), big);
+  n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
+  using Tile = Kv4Tile<D>;
+  constexpr int NG = Tile::NG, S = Tile::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[S], empty[S];
+  __shared__ float s_bias[S], s_m[4][8], s_l[4][8];
+  __shared__ int s_rows[S], s_abort;
+  const Problem& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // the CTA's selection row and heads
+  int b, kvh, h0, nh, srow;
+  if (a.grouped) {
+    const int n_sub = (p.G + 7) / 8, sub = blockIdx.x % n_sub;
+    srow = blockIdx.x / n_sub;
+    b = srow / p.Hkv;
+    kvh = srow % p.Hkv;
+    h0 = kvh * p.G + sub * 8;
+    nh = min(8, p.G - sub * 8);
+  } else {
+    srow = blockIdx.x;
+    b = srow / p.Hq;
+    h0 = srow % p.Hq;
+    kvh = h0 / p.G;
+    nh = 1;
+  }
+  const int split = blockIdx.y;
+  const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
+  const int n_hist = L > 0 ? dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err) : 0;
+  const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
+  const int e0 = split * per, e1 = min(n_ent, e0 + per);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      sm100::mbar_init(&full[s], 1);
+      sm100::mbar_init(&empty[s], 4);
+    }
+    s_abort = 0;
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == 4) {
+    int issued = 0;
+    bool ok = true;
+    for (int base = e0; base < e1 && ok; base += 32) {
+      // 32 blocks' places at once, so that no copy waits for its lookup
+      const int e = base + lane;
+      long long row0 = -1;
+      float bias = 0.f;
+      int rows = 0;
+      if (e < e1) {
+        const bool is_cur = e == n_hist;
+        const int c = is_cur ? cur : dcheck(a.sel.idx[(size_t)srow * p.topk + e], 0, cur - 1, a.c.err);
+        bias = is_cur ? 0.f : a.sel.logg[(size_t)srow * p.topk + e] * GBS_LOG2E;
+        rows = is_cur ? L - cur * kBS : kBS;
+        row0 = block_row(a, b, kvh, c);
+      }
+      for (int i = 0; i < 32 && base + i < e1; ++i, ++issued) {
+        const long long at = __shfl_sync(0xffffffffu, row0, i);
+        const float bi = __shfl_sync(0xffffffffu, bias, i);
+        const int n = __shfl_sync(0xffffffffu, rows, i);
+        const int s = issued % S, turn = issued / S;
+        if (lane == 0) {
+          if (turn > 0) ok = sm100::mbar_wait(&empty[s], (turn - 1) & 1, &s_abort, a.c.err, kWaitNs);
+          if (ok) {
+            s_bias[s] = bi;
+            s_rows[s] = at < 0 ? 0 : n;
+            if (at < 0) {
+              sm100::mbar_arrive(&full[s]);
+            } else {
+              // an even number of rows: whole 16-byte units of the parameters too
+              const int m = (n + 1) & ~1;
+              uint8_t* st = smem + s * Tile::kStage;
+              sm100::mbar_arrive_expect_tx(&full[s], 2 * m * (Tile::RB + Tile::PB));
+              sm100::bulk_load(st, a.c.kc + at * Tile::RB, m * Tile::RB, &full[s]);
+              sm100::bulk_load(st + Tile::kKp, a.c.kp + at * NG, m * Tile::PB, &full[s]);
+              sm100::bulk_load(st + Tile::kV, a.c.vc + at * Tile::RB, m * Tile::RB, &full[s]);
+              sm100::bulk_load(st + Tile::kVp, a.c.vp + at * NG, m * Tile::PB, &full[s]);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        if (!ok) break;
+      }
+    }
+    if (!ok && lane == 0)  // given up: no copy may be in flight when the CTA ends
+      for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+        sm100::mbar_drain(&full[i % S], (i / S) & 1, 1000000ull);
+    __syncwarp();
+  } else {
+    const int g = lane >> 2, t = lane & 3;
+    // q of head g, channels 8 t .. 8 t + 7 of every group, as fp16 times a power of two
+    uint32_t qa[NG][2][2];
+    float qsum = 0.f, zscale = p.scale_log2;
+    {
+      float qv[NG][8], mx = 0.f;
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + g) * D + 8 * t;
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          qv[k][i] = g < nh ? __bfloat162float(q[32 * k + i]) : 0.f;
+          mx = fmaxf(mx, fabsf(qv[k][i]));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      int ex = (int)(__float_as_uint(mx) >> 23) - 127;  // 2^ex <= mx
+      if (ex == 128 || ex == -127) ex = 0;              // infinite, zero or subnormal: as it is
+      const float down = ldexpf(1.f, -ex);
+      zscale *= ldexpf(1.f, ex);
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          qv[k][i] = __half2float(__float2half_rn(qv[k][i] * down));
+          sum += qv[k][i];
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (k == t) qsum = sum;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          qa[k][u][0] = pack_half2(qv[k][2 * u], qv[k][2 * u + 4]);
+          qa[k][u][1] = pack_half2(qv[k][2 * u + 1], qv[k][2 * u + 5]);
+        }
+      }
+    }
+    // parameter word t is (s, m): its product takes 0 s + qsum m, qsum in two terms
+    const float qs_hi = __half2float(__float2half_rn(qsum));
+    const uint32_t qm0 = pack_half2(0.f, qs_hi), qm1 = pack_half2(0.f, qsum - qs_hi);
+
+    float o[NG * 4][4], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    // rows of the block: the operand's column n is key n ^ (n >> 1 & 1) of eight, an
+    // order in which neither kind of load meets a bank twice more than it must
+    const int row_k = 16 * warp + (g ^ (g >> 1 & 1));
+    int row_c[2];  // of the columns 2 t and 2 t + 1
+    row_c[0] = 16 * warp + (2 * t ^ (t & 1));
+    row_c[1] = 16 * warp + ((2 * t + 1) ^ (t & 1));
+
+    for (int e = e0; e < e1; ++e) {
+      const int s = (e - e0) % S;
+      if (!sm100::mbar_wait(&full[s], ((e - e0) / S) & 1, &s_abort, a.c.err, kWaitNs)) break;
+      const uint8_t* st = smem + s * Tile::kStage;
+      const int rows = s_rows[s];
+      if (rows > 16 * warp) {
+        const float bias = s_bias[s];
+        float z[2][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t kw[NG], kp[2][NG];
+          load_words<NG>(st + (row_k + 8 * x) * Tile::RB + t * (Tile::RB / 4), kw);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) load_words<NG>(st + Tile::kKp + (row_c[c] + 8 * x) * Tile::PB, kp[c]);
+          uint32_t km = 0u;
+          if (t < NG) km = *reinterpret_cast<const uint32_t*>(st + Tile::kKp + (row_k + 8 * x) * Tile::PB + 4 * t);
+          float c0[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(c0, qm0, 0u, qm1, 0u, km, km);
+          z[x][0] = c0[0];
+          z[x][1] = c0[1];
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            // the group's two words of four channels, from the lane's NG words
+            const uint32_t w = __byte_perm(kw[k / 2], kw[NG / 2 + k / 2], k & 1 ? 0x7632 : 0x5410);
+            __half2 n[4];
+            unpack4(w, n);
+            float c1[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(c1, qa[k][0][0], 0u, qa[k][0][1], 0u, as_word(n[0]), as_word(n[1]));
+            mma16816(c1, qa[k][1][0], 0u, qa[k][1][1], 0u, as_word(n[2]), as_word(n[3]));
+            z[x][0] = fmaf(low_half(kp[0][k]), c1[0], z[x][0]);
+            z[x][1] = fmaf(low_half(kp[1][k]), c1[1], z[x][1]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) z[x][c] = fmaf(z[x][c], zscale, bias);
+        const bool ends = rows < 16 * warp + 16;  // the sequence ends in these keys
+        if (ends) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (row_c[c] + 8 * x >= rows) z[x][c] = -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m)) {
+          const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < NG * 4; ++i) {
+            o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+          }
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float p0 = fast_exp2(z[x][0] - m), p1 = fast_exp2(z[x][1] - m);
+          l += p0 + p1;
+          const __half2 hi = __floats2half2_rn(p0, p1);
+          pa[2 * x] = as_word(hi);
+          pa[2 * x + 1] = pack_half2(p0 - __low2float(hi), p1 - __high2float(hi));
+        }
+        uint32_t vw[2][2][NG / 2], vp[2][2][NG];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            load_words<NG / 2>(st + Tile::kV + (row_c[c] + 8 * x) * Tile::RB + g * (Tile::RB / 8), vw[x][c]);
+            load_words<NG>(st + Tile::kVp + (row_c[c] + 8 * x) * Tile::PB, vp[x][c]);
+            if (ends && row_c[c] + 8 * x >= rows) {  // whatever is there, it has no weight
+#pragma unroll
+              for (int k = 0; k < NG; ++k) vp[x][c][k] = 0u;
+            }
+          }
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          __half2 v[2][4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t sel = k & 1 ? 0x7632 : 0x5410;
+            unpack4(__byte_perm(vw[x][0][k / 2], vw[x][1][k / 2], sel), v[x]);
+            const __half2 sc = as_half2(__byte_perm(vp[x][0][k], vp[x][1][k], 0x5410));
+            const __half2 mi = as_half2(__byte_perm(vp[x][0][k], vp[x][1][k], 0x7632));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[x][i] = __hfma2(v[x][i], sc, mi);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma16816(o[4 * k + i], pa[0], pa[1], pa[2], pa[3], as_word(v[0][i]), as_word(v[1][i]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&empty[s]);
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    // all stages are consumed once every warp is here: their memory takes the sums
+    sm100::named_bar_sync(1, 128);
+    float* sum = reinterpret_cast<float*>(smem) + (warp * 8 + g) * D;
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<float4*>(sum + 32 * k + 4 * (2 * t + c)) =
+            make_float4(o[4 * k][c] + o[4 * k][2 + c], o[4 * k + 1][c] + o[4 * k + 1][2 + c],
+                        o[4 * k + 2][c] + o[4 * k + 2][2 + c], o[4 * k + 3][c] + o[4 * k + 3][2 + c]);
+    if (t == 0) {
+      s_m[warp][g] = m;
+      s_l[warp][g] = l;
+    }
+  }
+  __syncthreads();
+  if (s_abort) return;  // reported in the error word; nothing is written
+  for (int i = threadIdx.x; i < nh * D; i += kMmaThreads) {
+    const int h = i / D, c = i % D;
+    float M = -INFINITY, l = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][h]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = s_m[w][h] == -INFINITY ? 1.f : fast_exp2(s_m[w][h] - M);
+      l += s_l[w][h] * f;
+      v += reinterpret_cast<const float*>(smem)[(w * 8 + h) * D + c] * f;
+    }
+    const size_t row = (size_t)b * p.Hq + h0 + h;
+    if (a.splits == 1) {
+      reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + c] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
+      if (c == 0) a.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
+    } else {
+      const size_t part = row * a.splits + split;
+      a.part_acc[part * D + c] = v;
+      if (c == 0) {
+        a.part_ml[part * 2] = M;
+        a.part_ml[part * 2 + 1] = l;
+      }
+    }
+  }
+}
+
 // Joins the splits of a row: one warp each. A row without a key (a length of 0)
 // gives 0 and -infinity.
 template <typename T, int D>
@@ -327,15 +689,33 @@ __global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant_
   if (lane == 0) a.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
 }
 
+// CTA rows of the tensor-core decode: selection rows, times slices of eight heads.
+int decode4_rows(const DecodeArgs& a) {
+  return a.grouped ? a.p.B * a.p.Hkv * ((a.p.G + 7) / 8) : a.p.B * a.p.Hq;
+}
+
 template <typename T, int D>
 cudaError_t launch_decode4(const DecodeArgs& a, cudaStream_t st) {
   const int rows = a.p.B * a.p.Hq;
-  timer_begin(GBS_OP_DECODE, st);
-  kv4_decode_simt_kernel<T, D><<<dim3(rows, a.splits), 128, 0, st>>>(a);
-  timer_end(GBS_OP_DECODE, st);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2) {
+    e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Kv4Tile<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    timer_begin(GBS_OP_DECODE, st);
+    kv4_decode_mma_kernel<D><<<dim3(decode4_rows(a), a.splits), kMmaThreads, Kv4Tile<D>::kBytes, st>>>(a);
+    timer_end(GBS_OP_DECODE, st);
+    note_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.splits == 1) return e;
+  } else {
+    timer_begin(GBS_OP_DECODE, st);
+    kv4_decode_simt_kernel<T, D><<<dim3(rows, a.splits), 128, 0, st>>>(a);
+    timer_end(GBS_OP_DECODE, st);
+    note_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   kv4_combine_kernel<T, D><<<(rows + 3) / 4, 128, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
