@@ -312,21 +312,17 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 // codes and parameters (10,240 bytes for d = 128) arrive by bulk copies into a
 // ring of stages; each of four warps takes 16 of its 64 keys.
 //
-//   z[head, key] = sum_g s_g sum_{i in g} q_i n_i + sum_g m_g sum_{i in g} q_i
-// The inner sums are m16n8k16 products of q (rows: heads) and whole-number codes
-// as fp16, both exact: q is scaled by a power of two for each head so that it
-// fits, scales are applied to the fp32 sums, and the minima's part is one more
-// product of the raw parameter words with the sums of q as two fp16 terms.
-//   O[head, :] = sum_key p v,  v = m + s n rounded to fp16 (2^-12 of the value,
-// against the 2^-9 of the bf16 result); p as two fp16 terms, the second in the
-// eight rows of the product that no head uses, so that it costs nothing.
-// The product's key and channel order is free, so lanes take whole words of codes:
-// a thread's word of four channels (or two of them joined by one byte permute)
-// becomes operand registers by masking each nibble into the mantissa of 1024 or
-// 64 and subtracting that.
-// Bytes bound it (5 bits a value; 10,240 bytes a block); the unpacking costs about
-// 1,400 warp instructions a block, which is why K needs no multiplications.
-
+//   z[key, head] = sum_g s_g sum_{i in g} n_i q_i + sum_g m_g sum_{i in g} q_i
+// The inner sums are m16n8k16 products of whole-number codes (rows: keys) and q
+// (columns: heads) as fp16, both exact: q is scaled by a power of two for each head
+// so that it fits, scales are applied to the fp32 sums, and the minima's part is one
+// more product, of the raw parameter words with the sums of q as two fp16 terms.
+//   O[channel, head] = sum_key v p,  v = m + s n and p rounded to fp16 (2^-11 of the
+// value, against the 2^-8 of the bf16 result), sums in fp32.
+// With channels and keys as the product's 16 rows, no part of it is padding but
+// unused heads. Its key and channel order is free, so lanes take whole words of codes:
+// a thread's two words of four channels, joined by a byte permute, become operand
+// registers by masking each nibble into the mantissa of 1024 or 64 and subtracting that.
 template <int D>
 struct Kv4Tile {
   static constexpr int NG = D / 32, RB = D / 2, PB = NG * 4;
@@ -338,9 +334,20 @@ struct Kv4Tile {
 };
 constexpr int kMmaThreads = 160;  // four warps of arithmetic, one of copies
 constexpr uint64_t kWaitNs = 4000000000ull;
+// Weights are 2^(z - m) with m at most kLift below the largest z when it was set and
+// kRoom below any: fp16 holds 2^kRoom, and steps of small weights end at 2^(-24 - kLift)
+// of the largest.
+constexpr float kLift = 8.f, kRoom = 14.f;
 
+// c = a b, and c += a b
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma16816_add(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -350,14 +357,34 @@ __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return as_word(__floats2half2_rn(lo, hi)); }
 
+// The transpose of an 8 x 8 matrix of fp16: a lane's word is row lane / 4, columns 2 (lane % 4) and the next.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// (w & MASK) | magic in one instruction (which takes one constant; the other has to
+// be a register that the compiler cannot see through).
+template <uint32_t MASK>
+__device__ __forceinline__ __half2 mask_or(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return as_half2(r);
+}
+struct Magic {
+  uint32_t big = 0x64006400u, small = 0x54005400u;  // 1024 and 64, whose lowest bits weigh 1 at bits 0 and 4
+  __device__ __forceinline__ Magic() { asm volatile("" : "+r"(big), "+r"(small)); }
+};
+
 // Nibbles i = 0..3 of both halves of w as pairs of fp16 whole numbers.
-__device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
+__device__ __forceinline__ void unpack4(uint32_t w, const Magic& k, __half2 (&n)[4]) {
   const uint32_t h = w >> 8;
-  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);  // 1024, 64
-  n[0] = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), big);
-  n[1] = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), small);
-  n[2] = __hsub2(as_half2((h & 0x000f000fu) | 0x64006400u), big);
-  n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
+  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);
+  n[0] = __hsub2(mask_or<0x000f000fu>(w, k.big), big);
+  n[1] = __hsub2(mask_or<0x00f000f0u>(w, k.small), small);
+  n[2] = __hsub2(mask_or<0x000f000fu>(h, k.big), big);
+  n[3] = __hsub2(mask_or<0x00f000f0u>(h, k.small), small);
 }
 
 template <int N>
@@ -473,8 +500,8 @@ __global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __
   } else {
     const int g = lane >> 2, t = lane & 3;
     // q of head g, channels 8 t .. 8 t + 7 of every group, as fp16 times a power of two
-    uint32_t qa[NG][2][2];
-    float qsum = 0.f, zscale = p.scale_log2;
+    uint32_t qb[NG][2][2];
+    float qsum = 0.f, zs[2];
     {
       float qv[NG][8], mx = 0.f;
       const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + g) * D + 8 * t;
@@ -489,8 +516,9 @@ __global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       int ex = (int)(__float_as_uint(mx) >> 23) - 127;  // 2^ex <= mx
       if (ex == 128 || ex == -127) ex = 0;              // infinite, zero or subnormal: as it is
-      const float down = ldexpf(1.f, -ex);
-      zscale *= ldexpf(1.f, ex);
+      const float down = ldexpf(1.f, -ex), zscale = p.scale_log2 * ldexpf(1.f, ex);
+      zs[0] = __shfl_sync(0xffffffffu, zscale, 8 * t);  // of the heads 2 t and 2 t + 1
+      zs[1] = __shfl_sync(0xffffffffu, zscale, 8 * t + 4);
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
         float sum = 0.f;
@@ -504,8 +532,8 @@ __global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __
         if (k == t) qsum = sum;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          qa[k][u][0] = pack_half2(qv[k][2 * u], qv[k][2 * u + 4]);
-          qa[k][u][1] = pack_half2(qv[k][2 * u + 1], qv[k][2 * u + 5]);
+          qb[k][u][0] = pack_half2(qv[k][2 * u], qv[k][2 * u + 4]);
+          qb[k][u][1] = pack_half2(qv[k][2 * u + 1], qv[k][2 * u + 5]);
         }
       }
     }
@@ -513,131 +541,153 @@ __global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __
     const float qs_hi = __half2float(__float2half_rn(qsum));
     const uint32_t qm0 = pack_half2(0.f, qs_hi), qm1 = pack_half2(0.f, qsum - qs_hi);
 
-    float o[NG * 4][4], m = -INFINITY, l = 0.f;
+    // sums of heads 2 t and 2 t + 1; a head that is not there never raises its maximum
+    float o[NG * 2][4], m[2], l[2] = {0.f, 0.f};
+    m[0] = 2 * t < nh ? -INFINITY : INFINITY;
+    m[1] = 2 * t + 1 < nh ? -INFINITY : INFINITY;
 #pragma unroll
-    for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    // rows of the block: the operand's column n is key n ^ (n >> 1 & 1) of eight, an
-    // order in which neither kind of load meets a bank twice more than it must
+    // the product's row n is key n ^ (n >> 1 & 1) of eight, an order in which neither
+    // kind of load meets a bank twice more than it must
     const int row_k = 16 * warp + (g ^ (g >> 1 & 1));
-    int row_c[2];  // of the columns 2 t and 2 t + 1
-    row_c[0] = 16 * warp + (2 * t ^ (t & 1));
-    row_c[1] = 16 * warp + ((2 * t + 1) ^ (t & 1));
+    const int row_v0 = 16 * warp + (2 * t ^ (t & 1)), row_v1 = 16 * warp + ((2 * t + 1) ^ (t & 1));
+    const int at_k = row_k * Tile::RB + t * (Tile::RB / 4), at_kp = Tile::kKp + row_k * Tile::PB;
+    const int at_v0 = Tile::kV + row_v0 * Tile::RB + g * (Tile::RB / 8);
+    const int at_v1 = Tile::kV + row_v1 * Tile::RB + g * (Tile::RB / 8);
+    const int at_vp0 = Tile::kVp + row_v0 * Tile::PB, at_vp1 = Tile::kVp + row_v1 * Tile::PB;
 
+    const Magic magic;
+    int s = 0;
+    uint32_t parity = 0;
     for (int e = e0; e < e1; ++e) {
-      const int s = (e - e0) % S;
-      if (!sm100::mbar_wait(&full[s], ((e - e0) / S) & 1, &s_abort, a.c.err, kWaitNs)) break;
+      if (!sm100::mbar_wait(&full[s], parity, &s_abort, a.c.err, kWaitNs)) break;
       const uint8_t* st = smem + s * Tile::kStage;
-      const int rows = s_rows[s];
-      if (rows > 16 * warp) {
+      const int rows = s_rows[s] - 16 * warp;  // of this warp's keys
+      if (rows > 0) {
         const float bias = s_bias[s];
-        float z[2][2];
+        // z of keys row_k (z[0], z[1]: heads 2 t, 2 t + 1) and row_k + 8
+        float z[4];
+        {
+          uint32_t kw[2][NG], kp[2][NG], km[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t kw[NG], kp[2][NG];
-          load_words<NG>(st + (row_k + 8 * x) * Tile::RB + t * (Tile::RB / 4), kw);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) load_words<NG>(st + Tile::kKp + (row_c[c] + 8 * x) * Tile::PB, kp[c]);
-          uint32_t km = 0u;
-          if (t < NG) km = *reinterpret_cast<const uint32_t*>(st + Tile::kKp + (row_k + 8 * x) * Tile::PB + 4 * t);
-          float c0[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(c0, qm0, 0u, qm1, 0u, km, km);
-          z[x][0] = c0[0];
-          z[x][1] = c0[1];
+          for (int x = 0; x < 2; ++x) {
+            load_words<NG>(st + at_k + 8 * x * Tile::RB, kw[x]);
+            load_words<NG>(st + at_kp + 8 * x * Tile::PB, kp[x]);
+            km[x] = t < NG ? *reinterpret_cast<const uint32_t*>(st + at_kp + 8 * x * Tile::PB + 4 * t) : 0u;
+          }
+          mma16816(z, km[0], km[1], km[0], km[1], qm0, qm1);
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
+            __half2 n[2][4];
             // the group's two words of four channels, from the lane's NG words
-            const uint32_t w = __byte_perm(kw[k / 2], kw[NG / 2 + k / 2], k & 1 ? 0x7632 : 0x5410);
-            __half2 n[4];
-            unpack4(w, n);
-            float c1[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(c1, qa[k][0][0], 0u, qa[k][0][1], 0u, as_word(n[0]), as_word(n[1]));
-            mma16816(c1, qa[k][1][0], 0u, qa[k][1][1], 0u, as_word(n[2]), as_word(n[3]));
-            z[x][0] = fmaf(low_half(kp[0][k]), c1[0], z[x][0]);
-            z[x][1] = fmaf(low_half(kp[1][k]), c1[1], z[x][1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              unpack4(__byte_perm(kw[x][k / 2], kw[x][NG / 2 + k / 2], k & 1 ? 0x7632 : 0x5410), magic, n[x]);
+            float c[4];
+            mma16816(c, as_word(n[0][0]), as_word(n[1][0]), as_word(n[0][1]), as_word(n[1][1]), qb[k][0][0], qb[k][0][1]);
+            mma16816_add(c, as_word(n[0][2]), as_word(n[1][2]), as_word(n[0][3]), as_word(n[1][3]), qb[k][1][0],
+                         qb[k][1][1]);
+            const float s0 = low_half(kp[0][k]), s1 = low_half(kp[1][k]);
+            z[0] = fmaf(s0, c[0], z[0]);
+            z[1] = fmaf(s0, c[1], z[1]);
+            z[2] = fmaf(s1, c[2], z[2]);
+            z[3] = fmaf(s1, c[3], z[3]);
           }
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) z[x][c] = fmaf(z[x][c], zscale, bias);
-        const bool ends = rows < 16 * warp + 16;  // the sequence ends in these keys
+        for (int i = 0; i < 4; ++i) z[i] = fmaf(z[i], zs[i & 1], bias);
+        const bool ends = rows < 16;  // the sequence ends in these keys
         if (ends) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if (row_c[c] + 8 * x >= rows) z[x][c] = -INFINITY;
+          if (row_k - 16 * warp >= rows) z[0] = z[1] = -INFINITY;
+          if (row_k - 16 * warp + 8 >= rows) z[2] = z[3] = -INFINITY;
         }
-        float mx = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (__any_sync(0xffffffffu, mx > m)) {
-          const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
-          m = mn;
-          l *= f;
+        // m is raised only where a weight would pass 2^kRoom, so the exchange between
+        // lanes that a maximum takes is seldom needed
+        const bool high = fmaxf(z[0], z[2]) - kRoom > m[0] || fmaxf(z[1], z[3]) - kRoom > m[1];
+        if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
-          for (int i = 0; i < NG * 4; ++i) {
-            o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(z[c], z[2 + c]);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(m[c], mx - kLift), f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
+            m[c] = mn;
+            l[c] *= f;
+#pragma unroll
+            for (int i = 0; i < NG * 2; ++i) {
+              o[i][c] *= f;
+              o[i][2 + c] *= f;
+            }
           }
         }
-        uint32_t pa[4];
+        uint32_t pb[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float p0 = fast_exp2(z[x][0] - m), p1 = fast_exp2(z[x][1] - m);
-          l += p0 + p1;
-          const __half2 hi = __floats2half2_rn(p0, p1);
-          pa[2 * x] = as_word(hi);
-          pa[2 * x + 1] = pack_half2(p0 - __low2float(hi), p1 - __high2float(hi));
+          const float p0 = fast_exp2(z[2 * x] - m[0]), p1 = fast_exp2(z[2 * x + 1] - m[1]);
+          l[0] += p0;
+          l[1] += p1;
+          pb[x] = transpose8x8(pack_half2(p0, p1));  // head g, keys of the columns 2 t and 2 t + 1
         }
         uint32_t vw[2][2][NG / 2], vp[2][2][NG];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+          load_words<NG / 2>(st + at_v0 + 8 * x * Tile::RB, vw[x][0]);
+          load_words<NG / 2>(st + at_v1 + 8 * x * Tile::RB, vw[x][1]);
+          load_words<NG>(st + at_vp0 + 8 * x * Tile::PB, vp[x][0]);
+          load_words<NG>(st + at_vp1 + 8 * x * Tile::PB, vp[x][1]);
+        }
+        if (ends) {  // whatever lies behind the sequence, it has no weight
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            load_words<NG / 2>(st + Tile::kV + (row_c[c] + 8 * x) * Tile::RB + g * (Tile::RB / 8), vw[x][c]);
-            load_words<NG>(st + Tile::kVp + (row_c[c] + 8 * x) * Tile::PB, vp[x][c]);
-            if (ends && row_c[c] + 8 * x >= rows) {  // whatever is there, it has no weight
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int k = 0; k < NG; ++k) vp[x][c][k] = 0u;
+            for (int k = 0; k < NG; ++k) {
+              if (row_v0 - 16 * warp + 8 * x >= rows) vp[x][0][k] = 0u;
+              if (row_v1 - 16 * warp + 8 * x >= rows) vp[x][1][k] = 0u;
             }
-          }
+        }
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
           __half2 v[2][4];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t sel = k & 1 ? 0x7632 : 0x5410;
-            unpack4(__byte_perm(vw[x][0][k / 2], vw[x][1][k / 2], sel), v[x]);
+            unpack4(__byte_perm(vw[x][0][k / 2], vw[x][1][k / 2], k & 1 ? 0x7632 : 0x5410), magic, v[x]);
             const __half2 sc = as_half2(__byte_perm(vp[x][0][k], vp[x][1][k], 0x5410));
             const __half2 mi = as_half2(__byte_perm(vp[x][0][k], vp[x][1][k], 0x7632));
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[x][i] = __hfma2(v[x][i], sc, mi);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma16816(o[4 * k + i], pa[0], pa[1], pa[2], pa[3], as_word(v[0][i]), as_word(v[1][i]));
+          mma16816_add(o[2 * k], as_word(v[0][0]), as_word(v[0][1]), as_word(v[1][0]), as_word(v[1][1]), pb[0], pb[1]);
+          mma16816_add(o[2 * k + 1], as_word(v[0][2]), as_word(v[0][3]), as_word(v[1][2]), as_word(v[1][3]), pb[0], pb[1]);
         }
       }
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&empty[s]);
+      if (++s == S) {
+        s = 0;
+        parity ^= 1u;
+      }
     }
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
+    }
     // all stages are consumed once every warp is here: their memory takes the sums
     sm100::named_bar_sync(1, 128);
-    float* sum = reinterpret_cast<float*>(smem) + (warp * 8 + g) * D;
 #pragma unroll
-    for (int k = 0; k < NG; ++k)
+    for (int c = 0; c < 2; ++c)
+      if (2 * t + c < nh) {
+        float* sum = reinterpret_cast<float*>(smem) + (warp * 8 + 2 * t + c) * D + 4 * g;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<float4*>(sum + 32 * k + 4 * (2 * t + c)) =
-            make_float4(o[4 * k][c] + o[4 * k][2 + c], o[4 * k + 1][c] + o[4 * k + 1][2 + c],
-                        o[4 * k + 2][c] + o[4 * k + 2][2 + c], o[4 * k + 3][c] + o[4 * k + 3][2 + c]);
-    if (t == 0) {
-      s_m[warp][g] = m;
-      s_l[warp][g] = l;
-    }
+        for (int k = 0; k < NG; ++k)
+          *reinterpret_cast<float4*>(sum + 32 * k) =
+              make_float4(o[2 * k][c], o[2 * k][2 + c], o[2 * k + 1][c], o[2 * k + 1][2 + c]);
+        if (g == 0) {
+          s_m[warp][2 * t + c] = m[c];
+          s_l[warp][2 * t + c] = l[c];
+        }
+      }
   }
   __syncthreads();
   if (s_abort) return;  // reported in the error word; nothing is written

@@ -8,10 +8,11 @@ Decode, for one query over the kept keys (p the weights, v the values):
        scale sum |q k| (a tensor core may cut instead of round: one step, not half),
        and the sums of exponentials and the logarithm by 2^-18 in all.
   O    the weights inherit the logits' error e (twice, in numerator and sum):
-       2 e sum p |v|; values are rounded to fp16 (2^-11 of |v|) and weights to two
-       fp16 terms; sums of fp32 as above with at most 2^-16: (2 e + 2^-11 + 2^-16)
-       sum p |v|, and half a step of the output's type. With fp32 queries values and
-       weights stay in fp32: the 2^-11 falls away.
+       2 e sum p |v|; values are rounded to fp16 (2^-11 of |v|) and so are weights
+       (2^-11, or 2^-33 of the largest for the smallest of them); sums of fp32 as
+       above with at most 2^-16: (2 e + 2^-10 + 2^-16) sum p |v|, and half a step of
+       the output's type. With fp32 queries values and weights stay in fp32: the 2^-10
+       falls away.
 """
 import math
 
@@ -247,7 +248,7 @@ def _check(x, L, k, shared, tau=None, splits=0, scale=0.0):
     assert np.array_equal(np.isfinite(LSE), live) and bool((LSE[~live] == -np.inf).all())
     off = np.abs(LSE - Lr)[live] - e[live] - 2.0 ** -23 * np.abs(Lr[live])
     assert (off <= 0).all(), off.max()
-    value = 2.0 ** -16 + (2.0 ** -11 if x["q"].dtype == BF else 0)
+    value = 2.0 ** -16 + (2.0 ** -10 if x["q"].dtype == BF else 0)
     _within(O, Or, (2 * e[..., None] + value) * A)
 
 
