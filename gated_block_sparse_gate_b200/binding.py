@@ -7,6 +7,7 @@ There is no fallback: if the library or a CUDA device is missing, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -137,6 +138,7 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
 _F16 = (torch.float16,)
+_WEIGHTS = (torch.float32, torch.bfloat16)
 
 
 def _invalid(where, detail):
@@ -147,14 +149,18 @@ def _device(where, name, t):
     """The device of the call's anchor tensor, which must be a CUDA tensor."""
     if not isinstance(t, torch.Tensor):
         raise _invalid(where, f"{name} must be a torch.Tensor")
-    if t.device.type not in _DEVICE_TYPES:
-        raise _invalid(where, f"{name} is on {t.device}; the kernels need CUDA memory")
-    return t.device
+    device = t.device
+    if device.type not in _DEVICE_TYPES:
+        raise _invalid(where, f"{name} is on {device}; the kernels need CUDA memory")
+    return device
 
 
 def _need(where, name, t, shape, dtypes, device):
     """t is a contiguous tensor on ``device`` with one of ``dtypes`` and, unless
     ``shape`` is None, exactly that shape: the layout the C ABI reads."""
+    if (type(t) is torch.Tensor and t.device == device and t.dtype in dtypes
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise _invalid(where, f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -431,52 +437,67 @@ def decode_noalloc(q, Kc, Vc, S, L=None, block=64, topk=32, scale=0.0, num_split
 # ------------------------------------------- projections to attention, 4-bit cache
 
 
-def _on(device, stream):
-    """The context of a call's own allocations and launches: ``device`` current
-    and, if given, ``stream`` too, so that temporaries belong to the stream that
-    uses them. None where both are current already."""
+def _elsewhere(device, stream):
+    """What a call has to enter before it allocates and launches: ``stream``, so that
+    temporaries belong to the stream that uses them, or the tensors' device. None
+    where both are current already."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
     return None
 
 
-def _called(device, stream, fn):
-    ctx = _on(device, stream)
-    if ctx is None:
-        return fn(_stream())
-    with ctx:
-        return fn(_stream())
+def _current(device):
+    """The handle of ``device``'s current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _heads(where, name, t, shape, dtypes, device, n_dim=1, out=False):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _heads(where, name, t, shape, dtype, device, n_dim=1, out=False):
     """A [B, *, *, d] tensor with contiguous channels as gbs_heads; ``n_dim`` is
     its token dimension (1: [B, N, H, d], 2: [B, H, N, d])."""
-    if not isinstance(t, torch.Tensor):
-        raise _invalid(where, f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise _invalid(where, f"{name} is on {t.device}; expected {device}")
-    if t.dtype not in dtypes:
-        raise _invalid(where, f"{name} has dtype {t.dtype}; expected {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != shape:
-        raise _invalid(where, f"{name} has shape {tuple(t.shape)}; expected {shape}")
-    s = t.stride()
-    if s[3] != 1:
+    if not (type(t) is torch.Tensor and t.device == device and t.dtype is dtype and t.shape == shape):
+        if not isinstance(t, torch.Tensor):
+            raise _invalid(where, f"{name} must be a torch.Tensor")
+        if t.device != device:
+            raise _invalid(where, f"{name} is on {t.device}; expected {device}")
+        if t.dtype is not dtype:
+            raise _invalid(where, f"{name} has dtype {t.dtype}; expected {dtype}")
+        if tuple(t.shape) != shape:
+            raise _invalid(where, f"{name} has shape {tuple(t.shape)}; expected {shape}")
+    b, x, y, c = t.stride()
+    if c != 1:
         raise _invalid(where, f"{name} must have contiguous channels")
     # the stride of a dimension of one is never followed
-    st = [s[i] if shape[i] > 1 else 0 for i in range(3)]
-    if out:
+    if shape[0] == 1:
+        b = 0
+    if shape[1] == 1:
+        x = 0
+    if shape[2] == 1:
+        y = 0
+    if out and not t.is_contiguous():
         need = shape[3]
-        for step, n in sorted((st[i], shape[i]) for i in range(3) if shape[i] > 1):
+        for step, n in sorted(p for p in zip((b, x, y), shape) if p[1] > 1):
             if step < need:
                 raise _invalid(where, f"{name} is written and has elements that share memory")
             need = step * n
-    return Heads(t.data_ptr(), st[0], st[3 - n_dim], st[n_dim])
+    return Heads(t.data_ptr(), b, y, x) if n_dim == 1 else Heads(t.data_ptr(), b, x, y)
 
 
 def _opt(h):
     return None if h is None else ctypes.byref(h)
+
+
+def _check_ws(where, ws, device):
+    """An optional workspace whose error word is all that is used."""
+    if ws is not None:
+        _need(where, "ws", ws, None, _U8, device)
+        if ws.numel() < 256:
+            raise GbsError(5, where, "ws must have at least 256 bytes")
 
 
 def rope_tables(max_pos, rot, base=10000.0, device="cuda"):
@@ -493,49 +514,58 @@ def rope_axes(sections, interleaved=False):
     (all of axis 0, then axis 1, ...), or dealt out in turn while an axis has
     pairs left."""
     if not interleaved:
-        return [a for a, n in enumerate(sections) for _ in range(n)]
+        return tuple(a for a, n in enumerate(sections) for _ in range(n))
     left, out = list(sections), []
     while any(left):
         for a in range(len(left)):
             if left[a]:
                 left[a] -= 1
                 out.append(a)
-    return out
+    return tuple(out)
 
 
-def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved):
-    """(params, device) of a qkv_rope call, its small tensors checked."""
-    dev = _device(where, "q", q)
+_AxisArray = ctypes.c_ubyte * 64
+
+
+@functools.lru_cache(maxsize=64)
+def _axis_array(axes, half, n_axes):
+    """The axes of ``half`` pairs as the C array, or the reason why they are refused."""
+    if len(axes) != half:
+        return f"axes has {len(axes)} entries; expected one of each of the {half} pairs"
+    if not all(0 <= a < n_axes for a in axes):
+        return f"an axis is outside [0, {n_axes})"
+    return _AxisArray(*axes)
+
+
+def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev):
+    """The parameters of a qkv_rope call, its small tensors checked."""
     if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise _invalid(where, "q and k must be 4-D: [B, N, H, d]")
     B, N, Hq, d = q.shape
     _act_dtype(where, "q", q)
     if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
         raise _invalid(where, "cos must be [max_pos, rot / 2]")
-    max_pos, half = cos.shape
-    for name, t in (("cos", cos), ("sin", sin)):
-        _need(where, name, t, (max_pos, half), _F32, dev)
+    table = max_pos, half = cos.shape
+    _need(where, "cos", cos, table, _F32, dev)
+    _need(where, "sin", sin, table, _F32, dev)
     if not isinstance(pos, torch.Tensor) or pos.dim() not in (2, 3):
         raise _invalid(where, "pos must be [B, N] or [B, N, axes]")
     n_axes = 1 if pos.dim() == 2 else pos.shape[2]
     _need(where, "pos", pos, (B, N) if pos.dim() == 2 else (B, N, n_axes), _I32, dev)
     if half > 64:
         raise _invalid(where, f"cos has {half} columns; at most d / 2 = {d // 2} pairs are rotated")
-    axes = [0] * half if axes is None else axes
-    if len(axes) != half:
-        raise _invalid(where, f"axes has {len(axes)} entries; expected one of each of the {half} pairs")
-    if not all(0 <= a < n_axes for a in axes):
-        raise _invalid(where, f"an axis is outside [0, {n_axes})")
+    axis = _axis_array((0,) * half if axes is None else tuple(axes), half, n_axes)
+    if type(axis) is str:
+        raise _invalid(where, axis)
     if (wq is None) != (wk is None):
         raise _invalid(where, "give both weights or neither")
-    w_dtype = torch.float32
+    w_dtype = 1
     if wq is not None:
-        _need(where, "wq", wq, (d,), (torch.float32, torch.bfloat16), dev)
+        _need(where, "wq", wq, (d,), _WEIGHTS, dev)
         _need(where, "wk", wk, (d,), (wq.dtype,), dev)
-        w_dtype = wq.dtype
-    p = RopeParams(B, N, Hq, k.shape[2], d, 2 * half, int(bool(interleaved)), n_axes,
-                   (ctypes.c_ubyte * 64)(*axes), max_pos, DTYPES[q.dtype], DTYPES[w_dtype], float(eps))
-    return p, dev
+        w_dtype = DTYPES[wq.dtype]
+    return RopeParams(B, N, Hq, k.shape[2], d, 2 * half, 1 if interleaved else 0, n_axes, axis, max_pos,
+                      DTYPES[q.dtype], w_dtype, eps)
 
 
 def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, interleaved=False, out=None,
@@ -551,32 +581,30 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
     (``rope_axes``). ``out``: (Q, K, V) to write to, strided too. Returns (Q, K, V)."""
     where = "gbs_qkv_rope_fwd"
     lib = load_library()
-    p, dev = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved)
-    B, N, Hq, d, Hkv, act = p.B, p.N, p.Hq, p.d, p.Hkv, (q.dtype,)
+    dev = _device(where, "q", q)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return qkv_rope(q, k, v, cos, sin, pos, wq, wk, eps, axes, interleaved, out, ws)
+    p = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
+    B, N, Hq, d = q.shape
+    Hkv, act = p.Hkv, q.dtype
     hq = _heads(where, "q", q, (B, N, Hq, d), act, dev)
     hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev)
     hv = None if v is None else _heads(where, "v", v, (B, N, Hkv, d), act, dev)
     if out is not None and (len(out) != 3 or (out[2] is None) != (v is None)):
         raise _invalid(where, "out must be (Q, K, V), V None exactly if v is")
-    if ws is not None:
-        _need(where, "ws", ws, None, _U8, dev)
-        if ws.numel() < 256:
-            raise GbsError(5, where, "ws must have at least 256 bytes")
-
-    def go(st):
-        Q, K, V = out if out is not None else (
-            torch.empty(B, Hq, N, d, dtype=q.dtype, device=dev),
-            torch.empty(B, Hkv, N, d, dtype=q.dtype, device=dev),
-            None if v is None else torch.empty(B, Hkv, N, d, dtype=q.dtype, device=dev))
-        oq = _heads(where, "Q", Q, (B, Hq, N, d), act, dev, 2, True)
-        ok = _heads(where, "K", K, (B, Hkv, N, d), act, dev, 2, True)
-        ov = None if v is None else _heads(where, "V", V, (B, Hkv, N, d), act, dev, 2, True)
-        _check(lib.gbs_qkv_rope_fwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _opt(hv), _ptr(wq),
-                                    _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos), ctypes.byref(oq),
-                                    ctypes.byref(ok), _opt(ov), _ptr(ws), st), where)
-        return Q, K, V
-
-    return _called(dev, stream, go)
+    _check_ws(where, ws, dev)
+    Q, K, V = out if out is not None else (
+        torch.empty(B, Hq, N, d, dtype=act, device=dev), torch.empty(B, Hkv, N, d, dtype=act, device=dev),
+        None if v is None else torch.empty(B, Hkv, N, d, dtype=act, device=dev))
+    oq = _heads(where, "Q", Q, (B, Hq, N, d), act, dev, 2, True)
+    ok = _heads(where, "K", K, (B, Hkv, N, d), act, dev, 2, True)
+    ov = None if v is None else _heads(where, "V", V, (B, Hkv, N, d), act, dev, 2, True)
+    _check(lib.gbs_qkv_rope_fwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _opt(hv), _addr(wq),
+                                _addr(wk), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), ctypes.byref(oq),
+                                ctypes.byref(ok), _opt(ov), _addr(ws), _current(dev)), where)
+    return Q, K, V
 
 
 def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, eps=1e-6, axes=None,
@@ -588,8 +616,14 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
     such as parts of one packed tensor."""
     where = "gbs_qkv_rope_bwd"
     lib = load_library()
-    p, dev = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved)
-    B, N, Hq, d, Hkv, act = p.B, p.N, p.Hq, p.d, p.Hkv, (q.dtype,)
+    dev = _device(where, "q", q)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV, wq, wk, eps, axes, interleaved, grads, ws)
+    p = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
+    B, N, Hq, d = q.shape
+    Hkv, act = p.Hkv, q.dtype
     hq = _heads(where, "q", q, (B, N, Hq, d), act, dev)
     hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev)
     zq = _heads(where, "dQ", dQ, (B, Hq, N, d), act, dev, 2)
@@ -599,33 +633,26 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
         raise _invalid(where, "grads must be (dq, dk, dv), dv None exactly if dV is")
     if ws is not None:
         _need(where, "ws", ws, None, _U8, dev)
-
-    def go(st):
-        dq, dk, dv = grads if grads is not None else (
-            torch.empty(B, N, Hq, d, dtype=q.dtype, device=dev),
-            torch.empty(B, N, Hkv, d, dtype=q.dtype, device=dev),
-            None if dV is None else torch.empty(B, N, Hkv, d, dtype=q.dtype, device=dev))
-        oq = _heads(where, "dq", dq, (B, N, Hq, d), act, dev, 1, True)
-        ok = _heads(where, "dk", dk, (B, N, Hkv, d), act, dev, 1, True)
-        ov = None if dV is None else _heads(where, "dv", dv, (B, N, Hkv, d), act, dev, 1, True)
-        dwq, dwk = (None, None) if wq is None else torch.empty(2, d, dtype=torch.float32, device=dev).unbind()
-        scratch = ws
-        if scratch is None:
-            scratch = torch.empty(lib.gbs_qkv_rope_workspace_bytes(ctypes.byref(p)) or 256, dtype=torch.uint8,
-                                  device=dev)
-        _check(lib.gbs_qkv_rope_bwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _ptr(wq), _ptr(wk),
-                                    _ptr(cos), _ptr(sin), _ptr(pos), ctypes.byref(zq), ctypes.byref(zk),
-                                    _opt(zv), ctypes.byref(oq), ctypes.byref(ok), _opt(ov), _ptr(dwq),
-                                    _ptr(dwk), _ptr(scratch), scratch.numel(), st), where)
-        return dq, dk, dv, dwq, dwk
-
-    return _called(dev, stream, go)
+    dq, dk, dv = grads if grads is not None else (
+        torch.empty(B, N, Hq, d, dtype=act, device=dev), torch.empty(B, N, Hkv, d, dtype=act, device=dev),
+        None if dV is None else torch.empty(B, N, Hkv, d, dtype=act, device=dev))
+    oq = _heads(where, "dq", dq, (B, N, Hq, d), act, dev, 1, True)
+    ok = _heads(where, "dk", dk, (B, N, Hkv, d), act, dev, 1, True)
+    ov = None if dV is None else _heads(where, "dv", dv, (B, N, Hkv, d), act, dev, 1, True)
+    dwq, dwk = (None, None) if wq is None else torch.empty(2, d, dtype=torch.float32, device=dev).unbind()
+    if ws is None:
+        ws = torch.empty(lib.gbs_qkv_rope_workspace_bytes(ctypes.byref(p)) or 256, dtype=torch.uint8, device=dev)
+    _check(lib.gbs_qkv_rope_bwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _addr(wq), _addr(wk),
+                                cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), ctypes.byref(zq),
+                                ctypes.byref(zk), _opt(zv), ctypes.byref(oq), ctypes.byref(ok), _opt(ov),
+                                _addr(dwq), _addr(dwk), ws.data_ptr(), ws.numel(), _current(dev)), where)
+    return dq, dk, dv, dwq, dwk
 
 
 def qkv_rope_workspace_bytes(q, k, rot):
     """Bytes of ``ws`` for ``qkv_rope_backward`` (``qkv_rope`` takes the same one)."""
     B, N, Hq, d = q.shape
-    p = RopeParams(B, N, Hq, k.shape[2], d, rot, 0, 1, (ctypes.c_ubyte * 64)(), 1, DTYPES[q.dtype], 1, 0.0)
+    p = RopeParams(B, N, Hq, k.shape[2], d, rot, 0, 1, _AxisArray(), 1, DTYPES[q.dtype], 1, 0.0)
     n = int(load_library().gbs_qkv_rope_workspace_bytes(ctypes.byref(p)))
     if n == 0:
         raise GbsError(1, "gbs_qkv_rope_workspace_bytes", load_library().gbs_last_error().decode())
@@ -651,7 +678,7 @@ def _check_kv4(where, cache, B, d, device, block, block_table):
     fp16 of keys and of values, or pages [num_pages, Hkv, block, ...]."""
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise _invalid(where, "cache must be (key codes, key parameters, value codes, value parameters)")
-    kc = cache[0]
+    kc, kp, vc, vp = cache
     if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
         raise _invalid(where, "key codes must be 4-D")
     first, Hkv, rows, _ = kc.shape
@@ -661,43 +688,42 @@ def _check_kv4(where, cache, B, d, device, block, block_table):
                                   f"{block}, {d // 2})")
     elif rows != block:
         raise _invalid(where, f"a page of the key codes has {rows} rows; expected {block}")
-    for i, name in enumerate(("key codes", "key parameters", "value codes", "value parameters")):
-        if i % 2:
-            _need(where, name, cache[i], (first, Hkv, rows, d // 32, 2), _F16, device)
-        else:
-            _need(where, name, cache[i], (first, Hkv, rows, d // 2), _U8, device)
-    table = None
-    if block_table is not None:
-        _need(where, "block_table", block_table, None, _I32, device)
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise _invalid(where, f"block_table must be [B={B}, max_blocks]")
-        table = block_table.data_ptr()
-    desc = Kv4CacheDesc(*(t.data_ptr() for t in cache), table, 0 if table is None else block_table.shape[1],
-                        0 if table is None else first, rows)
-    return desc, Hkv, rows if block_table is None else block_table.shape[1] * block
+    codes, params = (first, Hkv, rows, d // 2), (first, Hkv, rows, d // 32, 2)
+    _need(where, "key codes", kc, codes, _U8, device)
+    _need(where, "key parameters", kp, params, _F16, device)
+    _need(where, "value codes", vc, codes, _U8, device)
+    _need(where, "value parameters", vp, params, _F16, device)
+    if block_table is None:
+        desc = Kv4CacheDesc(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), None, 0, 0, rows)
+        return desc, Hkv, rows
+    _need(where, "block_table", block_table, None, _I32, device)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise _invalid(where, f"block_table must be [B={B}, max_blocks]")
+    max_blocks = block_table.shape[1]
+    desc = Kv4CacheDesc(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), block_table.data_ptr(),
+                        max_blocks, first, rows)
+    return desc, Hkv, max_blocks * block
 
 
-def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out):
-    dev = _device(where, "K", K)
+def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out, dev):
+    """The checks and the call that ``kv4_append`` and ``kv4_read`` share."""
     if K.dim() != 4:
         raise _invalid(where, "K must be [B, Hkv, T, d]")
     B, _, T, d = K.shape
+    act = K.dtype
     _act_dtype(where, "K", K)
     desc, Hkv, L = _check_kv4(where, cache, B, d, dev, block, block_table)
-    hk = _heads(where, "K", K, (B, Hkv, T, d), (K.dtype,), dev, 2, out)
-    hv = _heads(where, "V", V, (B, Hkv, T, d), (K.dtype,), dev, 2, out)
+    hk = _heads(where, "K", K, (B, Hkv, T, d), act, dev, 2, out)
+    hv = _heads(where, "V", V, (B, Hkv, T, d), act, dev, 2, out)
     _need(where, "start", start, (B,), _I32, dev)
     if count is not None:
         _need(where, "count", count, (B,), _I32, dev)
-    if ws is not None:
-        _need(where, "ws", ws, None, _U8, dev)
-        if ws.numel() < 256:
-            raise GbsError(5, where, "ws must have at least 256 bytes")
+    _check_ws(where, ws, dev)
     if T == 0:
-        return lambda st: None
-    p = make_params(B, Hkv, Hkv, L, d, block, dtype=K.dtype)
-    return lambda st: _check(fn(ctypes.byref(p), ctypes.byref(desc), ctypes.byref(hk), ctypes.byref(hv), T,
-                                _ptr(start), _ptr(count), _ptr(ws), st), where)
+        return
+    p = Params(B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[act], 0.0, 0.0)
+    _check(fn(ctypes.byref(p), ctypes.byref(desc), ctypes.byref(hk), ctypes.byref(hv), T, start.data_ptr(),
+              _addr(count), _addr(ws), _current(dev)), where)
 
 
 def kv4_append(K, V, cache, start, block_table=None, count=None, block=64, ws=None, stream=None):
@@ -705,9 +731,14 @@ def kv4_append(K, V, cache, start, block_table=None, count=None, block=64, ws=No
     4-bit cache (``kv4_cache``), token t of sequence b at position start[b] + t
     (``start`` int32 [B]); with ``count`` (int32 [B]) only its first count[b]
     tokens. ``block_table`` (int32 [B, max_blocks]) makes the cache page pools."""
+    where = "gbs_kv4_append"
     fn = load_library().gbs_kv4_append
-    _called(_device("gbs_kv4_append", "K", K), stream,
-            _kv4_rows("gbs_kv4_append", fn, K, V, cache, start, block_table, count, ws, block, False))
+    dev = _device(where, "K", K)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_append(K, V, cache, start, block_table, count, block, ws)
+    _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, False, dev)
 
 
 def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16, block=64, out=None, ws=None,
@@ -718,6 +749,10 @@ def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16
     where = "gbs_kv4_read"
     fn = load_library().gbs_kv4_read
     dev = _device(where, "start", start)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_read(cache, start, T, block_table, count, dtype, block, out, ws)
     if not isinstance(cache, (tuple, list)) or len(cache) != 4 or not isinstance(cache[0], torch.Tensor) \
             or cache[0].dim() != 4:
         raise _invalid(where, "cache must be (key codes, key parameters, value codes, value parameters)")
@@ -725,14 +760,16 @@ def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16
         raise _invalid(where, f"dtype {dtype}; expected torch.bfloat16 or torch.float32")
     if T < 0:
         raise _invalid(where, "T must not be negative")
-
-    def go(st):
+    if out is None:
         shape = (start.shape[0], cache[0].shape[1], T, 2 * cache[0].shape[3])
-        K, V = out if out is not None else (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
-        _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, True)(st)
-        return K, V
-
-    return _called(dev, stream, go)
+        K, V = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        K, V = out
+        _device(where, "K", K)
+        if K.dim() != 4 or K.shape[2] != T:
+            raise _invalid(where, f"out must be (K, V) [B, Hkv, T={T}, d]")
+    _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, True, dev)
+    return K, V
 
 
 def kv4_workspace_bytes(params: Params) -> int:
@@ -748,6 +785,11 @@ def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block
     where = "gbs_kv4_decode"
     lib = load_library()
     dev = _device(where, "q", q)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_decode(q, cache, S, L, block, topk, scale, num_splits, block_table, seq_lens, group_shared,
+                              out, lse, ws, tau)
     if q.dim() != 3:
         raise _invalid(where, "q must be [B, Hq, d]")
     B, Hq, d = q.shape
@@ -759,24 +801,21 @@ def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block
     _need(where, "S", S, (B, Hkv if group_shared else Hq, -(-L // block)), _F32, dev)
     if seq_lens is not None:
         _need(where, "seq_lens", seq_lens, (B,), _I32, dev)
-    if out is not None:
-        _need(where, "O", out, (B, Hq, d), act, dev)
-    if lse is not None:
-        _need(where, "LSE", lse, (B, Hq), _F32, dev)
     if ws is not None:
         _need(where, "ws", ws, None, _U8, dev)
-    p = make_params(B, Hq, Hkv, L, d, block, topk, "sparse" if tau is None else "threshold", q.dtype, scale,
-                    0.0 if tau is None else tau)
-
-    def go(st):
-        O = out if out is not None else torch.empty_like(q)
-        LSE = lse if lse is not None else torch.empty(B, Hq, dtype=torch.float32, device=dev)
-        scratch = ws
-        if scratch is None:
-            scratch = torch.empty(kv4_workspace_bytes(p) or 256, dtype=torch.uint8, device=dev)
-        _check(lib.gbs_kv4_decode(ctypes.byref(p), ctypes.byref(desc), _ptr(seq_lens), 1 if group_shared else 0,
-                                  _ptr(q), _ptr(S), _ptr(O), _ptr(LSE), num_splits, _ptr(scratch),
-                                  scratch.numel(), st), where)
-        return O, LSE
-
-    return _called(dev, stream, go)
+    p = Params(B, Hq, Hkv, L, d, block, topk, 1 if tau is None else 2, DTYPES[q.dtype], scale,
+               0.0 if tau is None else tau)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(where, "O", out, (B, Hq, d), act, dev)
+    if lse is None:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+    else:
+        _need(where, "LSE", lse, (B, Hq), _F32, dev)
+    if ws is None:
+        ws = torch.empty(lib.gbs_kv4_workspace_bytes(ctypes.byref(p)) or 256, dtype=torch.uint8, device=dev)
+    _check(lib.gbs_kv4_decode(ctypes.byref(p), ctypes.byref(desc), _addr(seq_lens), 1 if group_shared else 0,
+                              q.data_ptr(), S.data_ptr(), out.data_ptr(), lse.data_ptr(), num_splits,
+                              ws.data_ptr(), ws.numel(), _current(dev)), where)
+    return out, lse

@@ -308,36 +308,44 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 
 // ------------------------------------------------------------ tensor-core decode
 // bf16 queries. A CTA serves up to eight query heads of one selection row (one
-// head without a shared selection) over its share of the kept blocks. A block's
-// codes and parameters (10,240 bytes for d = 128) arrive by bulk copies into a
-// ring of stages; each of four warps takes 16 of its 64 keys.
+// head without a shared selection) over its share of the kept blocks. Each of its
+// four warps works alone until the end, on every fourth half block: 32 keys, whose
+// codes and parameters (5,120 bytes for d = 128) arrive by bulk copies into the warp's
+// own ring of stages, issued by its first lane when a stage has been read.
 //
 //   z[key, head] = sum_g s_g sum_{i in g} n_i q_i + sum_g m_g sum_{i in g} q_i
-// The inner sums are m16n8k16 products of whole-number codes (rows: keys) and q
-// (columns: heads) as fp16, both exact: q is scaled by a power of two for each head
-// so that it fits, scales are applied to the fp32 sums, and the minima's part is one
-// more product, of the raw parameter words with the sums of q as two fp16 terms.
-//   O[channel, head] = sum_key v p,  v = m + s n and p rounded to fp16 (2^-11 of the
-// value, against the 2^-8 of the bf16 result), sums in fp32.
-// With channels and keys as the product's 16 rows, no part of it is padding but
-// unused heads. Its key and channel order is free, so lanes take whole words of codes:
-// a thread's two words of four channels, joined by a byte permute, become operand
-// registers by masking each nibble into the mantissa of 1024 or 64 and subtracting that.
+// The inner sums are m16n8k16 products of codes (rows: keys) and q (columns: heads) as
+// fp16, both exact: q is scaled by a power of two for each head so that it fits, scales
+// are applied to the fp32 sums, and the minima's part is one more product, of the raw
+// parameter words with the sums of q as two fp16 terms.
+//   O[channel, head] = sum_key n (s p) + sum_key m p
+// with codes as rows again, p and s p rounded to fp16 (2^-11 each, against the 2^-8 of
+// the bf16 result) and sums in fp32; where a scale is too small or large for that, values
+// m + s n are made first and rounded instead.
+// With channels and keys as the product's 16 rows, no part of it is padding but unused
+// heads. Its key and channel order is free, so lanes take whole words of codes: two words
+// of four channels, joined by a byte permute, become operand registers by masks alone.
+constexpr int kUnit = 32;  // keys of a warp's turn
 template <int D>
 struct Kv4Tile {
   static constexpr int NG = D / 32, RB = D / 2, PB = NG * 4;
-  static constexpr int kKp = kBS * RB, kV = kKp + kBS * PB, kVp = kV + kBS * RB;
-  static constexpr int kStage = kVp + kBS * PB;
-  static constexpr int kStages = D == 128 ? 6 : 8;
-  static constexpr int kBytes = kStages * kStage;
-  static_assert(kBytes >= 4 * 8 * D * 4, "the warps' sums are joined in the stages' memory");
+  static constexpr int kKp = kUnit * RB, kV = kKp + kUnit * PB, kVp = kV + kKp;
+  static constexpr int kStage = kVp + kUnit * PB;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kWarp = kStages * kStage, kBytes = 4 * kWarp;
+  static_assert(kWarp >= 8 * D * 4, "a warp's sums are joined in its stages' memory");
 };
-constexpr int kMmaThreads = 160;  // four warps of arithmetic, one of copies
+constexpr int kMmaThreads = 128;
 constexpr uint64_t kWaitNs = 4000000000ull;
-// Weights are 2^(z - m) with m at most kLift below the largest z when it was set and
-// kRoom below any: fp16 holds 2^kRoom, and steps of small weights end at 2^(-24 - kLift)
-// of the largest.
-constexpr float kLift = 8.f, kRoom = 14.f;
+// Weights are 2^(z - m), at most 2^kRoom, with m kLift below the largest z when it was
+// set. Products of weights with scales from 2^-9 to below 2^10 then stay inside fp16, and
+// what its steps of 2^-24 cut off is small against the largest of them.
+constexpr float kLift = 2.f, kRoom = 5.f;
+#define kLeastScale __ushort_as_half(0x1800)  // 2^-9
+#define kMostScale __ushort_as_half(0x6400)   // 2^10
+// A nibble alone is the fp16 of its code times 2^-24 (low in its byte) or 2^-20 (high):
+// products take it as it is, exactly, and the power of two goes into what it meets.
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 // c = a b, and c += a b
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -364,27 +372,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
   return r;
 }
 
-// (w & MASK) | magic in one instruction (which takes one constant; the other has to
-// be a register that the compiler cannot see through).
-template <uint32_t MASK>
-__device__ __forceinline__ __half2 mask_or(uint32_t w, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
-  return as_half2(r);
-}
-struct Magic {
-  uint32_t big = 0x64006400u, small = 0x54005400u;  // 1024 and 64, whose lowest bits weigh 1 at bits 0 and 4
-  __device__ __forceinline__ Magic() { asm volatile("" : "+r"(big), "+r"(small)); }
-};
-
 // Nibbles i = 0..3 of both halves of w as pairs of fp16 whole numbers.
-__device__ __forceinline__ void unpack4(uint32_t w, const Magic& k, __half2 (&n)[4]) {
+__device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
   const uint32_t h = w >> 8;
-  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);
-  n[0] = __hsub2(mask_or<0x000f000fu>(w, k.big), big);
-  n[1] = __hsub2(mask_or<0x00f000f0u>(w, k.small), small);
-  n[2] = __hsub2(mask_or<0x000f000fu>(h, k.big), big);
-  n[3] = __hsub2(mask_or<0x00f000f0u>(h, k.small), small);
+  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);  // 1024, 64: steps of 1 at bits 0 and 4
+  n[0] = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), big);
+  n[1] = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), small);
+  n[2] = __hsub2(as_half2((h & 0x000f000fu) | 0x64006400u), big);
+  n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
 }
 
 template <int N>
@@ -407,15 +402,21 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
   using Tile = Kv4Tile<D>;
   constexpr int NG = Tile::NG, S = Tile::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[S], empty[S];
-  __shared__ float s_bias[S], s_m[4][8], s_l[4][8];
-  __shared__ int s_rows[S], s_abort;
+  __shared__ uint64_t full_all[4][S];
+  __shared__ float bias_all[4][S], s_m[4][8], s_l[4][8];
+  __shared__ int rows_all[4][S], s_abort;
+  __shared__ uint4 s_q[NG][32];
+  __shared__ float s_qsum[8][NG];
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* full = full_all[warp];
+  float* s_bias = bias_all[warp];
+  int* s_rows = rows_all[warp];
+  uint8_t* ring = smem + warp * Tile::kWarp;
 
   // the CTA's selection row and heads
   int b, kvh, h0, nh, srow;
@@ -438,257 +439,321 @@ __global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __
   const int n_hist = L > 0 ? dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err) : 0;
   const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
   const int e0 = split * per, e1 = min(n_ent, e0 + per);
+  // this warp's blocks are first, first + 2, ...; it takes their keys half .. half + 31
+  const int first = e0 + (warp >> 1), half = (warp & 1) * kUnit;
+  const int turns = first < e1 ? (e1 - first + 1) / 2 : 0;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], 4);
-    }
-    s_abort = 0;
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) sm100::mbar_init(&full[s], 1);
     sm100::fence_barrier_init();
   }
-  __syncthreads();
+  __syncwarp();
 
-  if (warp == 4) {
-    int issued = 0;
-    bool ok = true;
-    for (int base = e0; base < e1 && ok; base += 32) {
-      // 32 blocks' places at once, so that no copy waits for its lookup
-      const int e = base + lane;
-      long long row0 = -1;
-      float bias = 0.f;
-      int rows = 0;
-      if (e < e1) {
-        const bool is_cur = e == n_hist;
-        const int c = is_cur ? cur : dcheck(a.sel.idx[(size_t)srow * p.topk + e], 0, cur - 1, a.c.err);
-        bias = is_cur ? 0.f : a.sel.logg[(size_t)srow * p.topk + e] * GBS_LOG2E;
-        rows = is_cur ? L - cur * kBS : kBS;
-        row0 = block_row(a, b, kvh, c);
-      }
-      for (int i = 0; i < 32 && base + i < e1; ++i, ++issued) {
-        const long long at = __shfl_sync(0xffffffffu, row0, i);
-        const float bi = __shfl_sync(0xffffffffu, bias, i);
-        const int n = __shfl_sync(0xffffffffu, rows, i);
-        const int s = issued % S, turn = issued / S;
-        if (lane == 0) {
-          if (turn > 0) ok = sm100::mbar_wait(&empty[s], (turn - 1) & 1, &s_abort, a.c.err, kWaitNs);
-          if (ok) {
-            s_bias[s] = bi;
-            s_rows[s] = at < 0 ? 0 : n;
-            if (at < 0) {
-              sm100::mbar_arrive(&full[s]);
-            } else {
-              // an even number of rows: whole 16-byte units of the parameters too
-              const int m = (n + 1) & ~1;
-              uint8_t* st = smem + s * Tile::kStage;
-              sm100::mbar_arrive_expect_tx(&full[s], 2 * m * (Tile::RB + Tile::PB));
-              sm100::bulk_load(st, a.c.kc + at * Tile::RB, m * Tile::RB, &full[s]);
-              sm100::bulk_load(st + Tile::kKp, a.c.kp + at * NG, m * Tile::PB, &full[s]);
-              sm100::bulk_load(st + Tile::kV, a.c.vc + at * Tile::RB, m * Tile::RB, &full[s]);
-              sm100::bulk_load(st + Tile::kVp, a.c.vp + at * NG, m * Tile::PB, &full[s]);
-            }
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-        if (!ok) break;
-      }
+  // places of 32 of the warp's turns at once, a lane each, so that no copy waits for its
+  // lookup: the half block's index among all of the cache's
+  int my_unit = 0, my_rows = 0;
+  float my_bias = 0.f;
+  const uint8_t* copy_from = lane < 2 ? (lane ? (const uint8_t*)a.c.kp : a.c.kc) : (lane & 1 ? (const uint8_t*)a.c.vp : a.c.vc);
+  const uint32_t copy_row = lane & 1 ? Tile::PB : Tile::RB;
+  const uint32_t copy_to = (lane & 2 ? Tile::kV : 0) + (lane & 1 ? Tile::kKp : 0);
+  auto look_up = [&](int turn) {
+    const int e = first + 2 * turn;
+    my_rows = 0;
+    if (turn < turns) {
+      const bool is_cur = e == n_hist;
+      const int c = is_cur ? cur : dcheck(a.sel.idx[(size_t)srow * p.topk + e], 0, cur - 1, a.c.err);
+      my_bias = is_cur ? 0.f : a.sel.logg[(size_t)srow * p.topk + e] * GBS_LOG2E;
+      const long long row = block_row(a, b, kvh, c);
+      my_unit = (int)(row / kUnit) + (warp & 1);
+      my_rows = row < 0 ? 0 : min(kUnit, is_cur ? L - cur * kBS - half : kUnit);
     }
-    if (!ok && lane == 0)  // given up: no copy may be in flight when the CTA ends
-      for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-        sm100::mbar_drain(&full[i % S], (i / S) & 1, 1000000ull);
+  };
+  auto issue = [&](int turn, int s) {
+    if (turn > 0 && (turn & 31) == 0) look_up(turn + lane);
+    const int unit = __shfl_sync(0xffffffffu, my_unit, turn & 31);
+    const float bias = __shfl_sync(0xffffffffu, my_bias, turn & 31);
+    const int n = __shfl_sync(0xffffffffu, my_rows, turn & 31);
+    const uint32_t m = n > 0 ? (n + 1) & ~1 : 0;  // whole 16-byte units of the parameters too
+    if (lane == 0) {
+      s_bias[s] = bias;
+      s_rows[s] = n;
+      sm100::mbar_arrive_expect_tx(&full[s], 2 * m * (Tile::RB + Tile::PB));
+    }
     __syncwarp();
-  } else {
-    const int g = lane >> 2, t = lane & 3;
-    // q of head g, channels 8 t .. 8 t + 7 of every group, as fp16 times a power of two
-    uint32_t qb[NG][2][2];
-    float qsum = 0.f, zs[2];
-    {
-      float qv[NG][8], mx = 0.f;
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + g) * D + 8 * t;
+    if (lane < 4 && m > 0)  // one of the four tensors each
+      sm100::bulk_load(ring + s * Tile::kStage + copy_to, copy_from + (size_t)unit * (kUnit * copy_row), m * copy_row, &full[s]);
+  };
+  look_up(lane);
+  for (int s = 0; s < S && s < turns; ++s) issue(s, s);
+
+  const int g = lane >> 2, t = lane & 3;
+  // q of head g, channels 8 t .. 8 t + 7 of every group, as fp16 times a power of two;
+  // each group is converted by one warp
+  float zs[2];
+  {
+    const uint4* q = reinterpret_cast<const uint4*>(
+        reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + g) * D + 8 * t);
+    uint4 mine = make_uint4(0u, 0u, 0u, 0u);
+    __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < NG; ++k)
+    for (int k = 0; k < NG; ++k) {
+      const uint4 u = g < nh ? __ldg(q + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
+      if (k == warp) mine = u;
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          qv[k][i] = g < nh ? __bfloat162float(q[32 * k + i]) : 0.f;
-          mx = fmaxf(mx, fabsf(qv[k][i]));
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      int ex = (int)(__float_as_uint(mx) >> 23) - 127;  // 2^ex <= mx
-      if (ex == 128 || ex == -127) ex = 0;              // infinite, zero or subnormal: as it is
-      const float down = ldexpf(1.f, -ex), zscale = p.scale_log2 * ldexpf(1.f, ex);
-      zs[0] = __shfl_sync(0xffffffffu, zscale, 8 * t);  // of the heads 2 t and 2 t + 1
-      zs[1] = __shfl_sync(0xffffffffu, zscale, 8 * t + 4);
-#pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          qv[k][i] = __half2float(__float2half_rn(qv[k][i] * down));
-          sum += qv[k][i];
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (k == t) qsum = sum;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          qb[k][u][0] = pack_half2(qv[k][2 * u], qv[k][2 * u + 4]);
-          qb[k][u][1] = pack_half2(qv[k][2 * u + 1], qv[k][2 * u + 5]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
     }
-    // parameter word t is (s, m): its product takes 0 s + qsum m, qsum in two terms
-    const float qs_hi = __half2float(__float2half_rn(qsum));
-    const uint32_t qm0 = pack_half2(0.f, qs_hi), qm1 = pack_half2(0.f, qsum - qs_hi);
+    float mx = fmaxf(__low2float(most), __high2float(most));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 8;  // 2^(ex + 8) <= mx < 2^(ex + 9)
+    if (ex == 120 || ex == -135) ex = 0;                  // infinite, zero or subnormal: as it is
+    // the codes' products are 2^-24 of what they stand for, the scales' and minima's not
+    const float down = ldexpf(1.f, -ex), zscale = p.scale_log2 * ldexpf(1.f, ex) * 0x1p24f;
+    zs[0] = __shfl_sync(0xffffffffu, zscale, 8 * t);  // of the heads 2 t and 2 t + 1
+    zs[1] = __shfl_sync(0xffffffffu, zscale, 8 * t + 4);
+    if (warp < NG) {
+      const uint32_t w[4] = {mine.x, mine.y, mine.z, mine.w};
+      float v[8], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = __half2float(__float2half_rn(__uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * down));
+        sum += v[i];
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (t == 0) s_qsum[g][warp] = sum;
+      // high nibbles count 16 times; of q, that rounds only what is below 2^-15 of its largest
+      s_q[warp][lane] = make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1] * 0x1p-4f, v[5] * 0x1p-4f),
+                                   pack_half2(v[2], v[6]), pack_half2(v[3] * 0x1p-4f, v[7] * 0x1p-4f));
+    }
+  }
+  __syncthreads();
+  const float qsum = t < NG ? s_qsum[g][t] : 0.f;
+  // parameter word t is (s, m): its product takes 0 s + qsum m, qsum in two terms
+  const float qs_hi = __half2float(__float2half_rn(qsum));
+  const uint32_t qm0 = pack_half2(0.f, qs_hi), qm1 = pack_half2(0.f, qsum - qs_hi);
 
-    // sums of heads 2 t and 2 t + 1; a head that is not there never raises its maximum
-    float o[NG * 2][4], m[2], l[2] = {0.f, 0.f};
-    m[0] = 2 * t < nh ? -INFINITY : INFINITY;
-    m[1] = 2 * t + 1 < nh ? -INFINITY : INFINITY;
+  // sums of heads 2 t and 2 t + 1; a head that is not there never raises its maximum
+  // (o in units of 2^-24 and 2^-20 of low and high nibbles; om: the minima's part, groups g)
+  float o[NG * 2][4], om[4] = {0.f, 0.f, 0.f, 0.f}, m[2], l[2] = {0.f, 0.f};
+  m[0] = 2 * t < nh ? -INFINITY : INFINITY;
+  m[1] = 2 * t + 1 < nh ? -INFINITY : INFINITY;
 #pragma unroll
-    for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    // the product's row n is key n ^ (n >> 1 & 1) of eight, an order in which neither
-    // kind of load meets a bank twice more than it must
-    const int row_k = 16 * warp + (g ^ (g >> 1 & 1));
-    const int row_v0 = 16 * warp + (2 * t ^ (t & 1)), row_v1 = 16 * warp + ((2 * t + 1) ^ (t & 1));
-    const int at_k = row_k * Tile::RB + t * (Tile::RB / 4), at_kp = Tile::kKp + row_k * Tile::PB;
-    const int at_v0 = Tile::kV + row_v0 * Tile::RB + g * (Tile::RB / 8);
-    const int at_v1 = Tile::kV + row_v1 * Tile::RB + g * (Tile::RB / 8);
-    const int at_vp0 = Tile::kVp + row_v0 * Tile::PB, at_vp1 = Tile::kVp + row_v1 * Tile::PB;
+  // the product's row n is key n ^ (n >> 1 & 1) of eight, an order in which neither
+  // kind of load meets a bank twice more than it must
+  const int row_k = g ^ (g >> 1 & 1), row_v0 = 2 * t ^ (t & 1), row_v1 = (2 * t + 1) ^ (t & 1);
+  const int at_k = row_k * Tile::RB + t * (Tile::RB / 4), at_kp = Tile::kKp + row_k * Tile::PB;
+  const int at_v0 = Tile::kV + row_v0 * Tile::RB + g * (Tile::RB / 8);
+  const int at_v1 = Tile::kV + row_v1 * Tile::RB + g * (Tile::RB / 8);
+  const int at_vp0 = Tile::kVp + row_v0 * Tile::PB, at_vp1 = Tile::kVp + row_v1 * Tile::PB;
 
-    const Magic magic;
-    int s = 0;
-    uint32_t parity = 0;
-    for (int e = e0; e < e1; ++e) {
-      if (!sm100::mbar_wait(&full[s], parity, &s_abort, a.c.err, kWaitNs)) break;
-      const uint8_t* st = smem + s * Tile::kStage;
-      const int rows = s_rows[s] - 16 * warp;  // of this warp's keys
-      if (rows > 0) {
-        const float bias = s_bias[s];
-        // z of keys row_k (z[0], z[1]: heads 2 t, 2 t + 1) and row_k + 8
-        float z[4];
-        {
-          uint32_t kw[2][NG], kp[2][NG], km[2];
+  int s = 0;
+  uint32_t parity = 0;
+  for (int turn = 0; turn < turns; ++turn) {
+    if (!sm100::mbar_wait(&full[s], parity, &s_abort, a.c.err, kWaitNs)) {
+      // given up: no copy may be in flight when the CTA ends
+      if (lane == 0)
+        for (int i = turn; i < turns && i < turn + S; ++i) sm100::mbar_drain(&full[i % S], (i / S) & 1, 1000000ull);
+      __syncwarp();
+      break;
+    }
+    uint8_t* st = ring + s * Tile::kStage;
+    const int rows = s_rows[s];
+    if (rows > 0) {
+      const bool ends = rows < kUnit;  // the sequence ends in these keys
+      if (ends) {
+        __syncwarp();  // (a branch of its own: it is seldom taken)
+        if (lane >= rows)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            load_words<NG>(st + at_k + 8 * x * Tile::RB, kw[x]);
-            load_words<NG>(st + at_kp + 8 * x * Tile::PB, kp[x]);
-            km[x] = t < NG ? *reinterpret_cast<const uint32_t*>(st + at_kp + 8 * x * Tile::PB + 4 * t) : 0u;
+          for (int k = 0; k < NG; ++k) {  // whatever lies behind the sequence stands for zeros
+            reinterpret_cast<uint32_t*>(st + Tile::kKp + lane * Tile::PB)[k] = 0u;
+            reinterpret_cast<uint32_t*>(st + Tile::kVp + lane * Tile::PB)[k] = 0u;
           }
-          mma16816(z, km[0], km[1], km[0], km[1], qm0, qm1);
+        __syncwarp();
+      }
+      // of 16 keys y: z of keys row_k (z[y][0], z[y][1]: heads 2 t, 2 t + 1) and row_k + 8
+      float z[2][4];
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            __half2 n[2][4];
-            // the group's two words of four channels, from the lane's NG words
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              unpack4(__byte_perm(kw[x][k / 2], kw[x][NG / 2 + k / 2], k & 1 ? 0x7632 : 0x5410), magic, n[x]);
-            float c[4];
-            mma16816(c, as_word(n[0][0]), as_word(n[1][0]), as_word(n[0][1]), as_word(n[1][1]), qb[k][0][0], qb[k][0][1]);
-            mma16816_add(c, as_word(n[0][2]), as_word(n[1][2]), as_word(n[0][3]), as_word(n[1][3]), qb[k][1][0],
-                         qb[k][1][1]);
-            const float s0 = low_half(kp[0][k]), s1 = low_half(kp[1][k]);
-            z[0] = fmaf(s0, c[0], z[0]);
-            z[1] = fmaf(s0, c[1], z[1]);
-            z[2] = fmaf(s1, c[2], z[2]);
-            z[3] = fmaf(s1, c[3], z[3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = fmaf(z[i], zs[i & 1], bias);
-        const bool ends = rows < 16;  // the sequence ends in these keys
-        if (ends) {
-          if (row_k - 16 * warp >= rows) z[0] = z[1] = -INFINITY;
-          if (row_k - 16 * warp + 8 >= rows) z[2] = z[3] = -INFINITY;
-        }
-        // m is raised only where a weight would pass 2^kRoom, so the exchange between
-        // lanes that a maximum takes is seldom needed
-        const bool high = fmaxf(z[0], z[2]) - kRoom > m[0] || fmaxf(z[1], z[3]) - kRoom > m[1];
-        if (__any_sync(0xffffffffu, high)) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(z[c], z[2 + c]);
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            const float mn = fmaxf(m[c], mx - kLift), f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
-            m[c] = mn;
-            l[c] *= f;
-#pragma unroll
-            for (int i = 0; i < NG * 2; ++i) {
-              o[i][c] *= f;
-              o[i][2 + c] *= f;
-            }
-          }
-        }
-        uint32_t pb[2];
+      for (int y = 0; y < 2; ++y) {
+        uint32_t kw[2][NG], kp[2][NG], km[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float p0 = fast_exp2(z[2 * x] - m[0]), p1 = fast_exp2(z[2 * x + 1] - m[1]);
+          const int r = 16 * y + 8 * x;
+          load_words<NG>(st + at_k + r * Tile::RB, kw[x]);
+          load_words<NG>(st + at_kp + r * Tile::PB, kp[x]);
+          km[x] = t < NG ? *reinterpret_cast<const uint32_t*>(st + at_kp + r * Tile::PB + 4 * t) : 0u;
+        }
+        mma16816(z[y], km[0], km[1], km[0], km[1], qm0, qm1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[y][i] *= 0x1p-24f;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          uint32_t w[2], h[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            // the group's two words of four channels, from the lane's NG words
+            w[x] = __byte_perm(kw[x][k / 2], kw[x][NG / 2 + k / 2], k & 1 ? 0x7632 : 0x5410);
+            h[x] = w[x] >> 8;
+          }
+          const uint4 qk = s_q[k][lane];
+          float c[4];
+          mma16816(c, w[0] & kLow, w[1] & kLow, w[0] & kHigh, w[1] & kHigh, qk.x, qk.y);
+          mma16816_add(c, h[0] & kLow, h[1] & kLow, h[0] & kHigh, h[1] & kHigh, qk.z, qk.w);
+          const float s0 = low_half(kp[0][k]), s1 = low_half(kp[1][k]);
+          z[y][0] = fmaf(s0, c[0], z[y][0]);
+          z[y][1] = fmaf(s0, c[1], z[y][1]);
+          z[y][2] = fmaf(s1, c[2], z[y][2]);
+          z[y][3] = fmaf(s1, c[3], z[y][3]);
+        }
+      }
+      if (ends) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // scales of the heads are not negative
+          if (row_k + 8 * (i >> 1) >= rows) z[i >> 2][i & 3] = -INFINITY;
+      }
+      // logarithms of the weights; m is raised only where one would pass kRoom, so the
+      // exchange between lanes that a maximum takes is seldom needed
+      const float bias = s_bias[s];
+      float x[2][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = fmaf(z[i >> 2][i & 3], zs[i & 1], bias - m[i & 1]);
+      float mx[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(x[0][c], x[0][2 + c]), fmaxf(x[1][c], x[1][2 + c]));
+      if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > kRoom)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mx[c] = fmaxf(fmaxf(z[0][c], z[0][2 + c]), fmaxf(z[1][c], z[1][2 + c]));
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], w));
+          const float mn = fmaxf(m[c], fmaf(mx[c], zs[c], bias) - kLift), f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
+          m[c] = mn;
+          l[c] *= f;
+          om[c] *= f;
+#pragma unroll
+          for (int i = 0; i < NG * 2; ++i) {
+            o[i][c] *= f;
+            o[i][2 + c] *= f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = fmaf(z[i >> 2][i & 3], zs[i & 1], bias - m[i & 1]);
+      }
+      // a lane looks at one row's value scales: do they all suit fp16 products with weights?
+      bool plain;
+      {
+        uint32_t sc[NG];
+        load_words<NG>(st + Tile::kVp + lane * Tile::PB, sc);
+        __half2 lo = as_half2(sc[0]), hi = as_half2(sc[0]);
+#pragma unroll
+        for (int k = 1; k < NG; ++k) {
+          lo = __hmin2_nan(lo, as_half2(sc[k]));
+          hi = __hmax2_nan(hi, as_half2(sc[k]));
+        }
+        plain = __all_sync(0xffffffffu, __low2half(lo) >= kLeastScale && __low2half(hi) < kMostScale);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t pb[2];  // head g, keys of the columns 2 t and 2 t + 1
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const float p0 = fast_exp2(x[y][2 * v]), p1 = fast_exp2(x[y][2 * v + 1]);
           l[0] += p0;
           l[1] += p1;
-          pb[x] = transpose8x8(pack_half2(p0, p1));  // head g, keys of the columns 2 t and 2 t + 1
+          pb[v] = transpose8x8(pack_half2(p0, p1));
         }
         uint32_t vw[2][2][NG / 2], vp[2][2][NG];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          load_words<NG / 2>(st + at_v0 + 8 * x * Tile::RB, vw[x][0]);
-          load_words<NG / 2>(st + at_v1 + 8 * x * Tile::RB, vw[x][1]);
-          load_words<NG>(st + at_vp0 + 8 * x * Tile::PB, vp[x][0]);
-          load_words<NG>(st + at_vp1 + 8 * x * Tile::PB, vp[x][1]);
+        for (int v = 0; v < 2; ++v) {
+          const int r = 16 * y + 8 * v;
+          load_words<NG / 2>(st + at_v0 + r * Tile::RB, vw[v][0]);
+          load_words<NG / 2>(st + at_v1 + r * Tile::RB, vw[v][1]);
+          load_words<NG>(st + at_vp0 + r * Tile::PB, vp[v][0]);
+          load_words<NG>(st + at_vp1 + r * Tile::PB, vp[v][1]);
         }
-        if (ends) {  // whatever lies behind the sequence, it has no weight
+        if (plain) {
+          uint32_t mi[2] = {0u, 0u};
+          if (g < NG)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
-              if (row_v0 - 16 * warp + 8 * x >= rows) vp[x][0][k] = 0u;
-              if (row_v1 - 16 * warp + 8 * x >= rows) vp[x][1][k] = 0u;
+            for (int v = 0; v < 2; ++v) {
+              const int r = 16 * y + 8 * v;
+              mi[v] = __byte_perm(*reinterpret_cast<const uint32_t*>(st + at_vp0 + r * Tile::PB + 4 * g),
+                                  *reinterpret_cast<const uint32_t*>(st + at_vp1 + r * Tile::PB + 4 * g), 0x7632);
             }
-        }
+          mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          __half2 v[2][4];
+          for (int k = 0; k < NG; ++k) {
+            uint32_t w[2], h[2], ps[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            unpack4(__byte_perm(vw[x][0][k / 2], vw[x][1][k / 2], k & 1 ? 0x7632 : 0x5410), magic, v[x]);
-            const __half2 sc = as_half2(__byte_perm(vp[x][0][k], vp[x][1][k], 0x5410));
-            const __half2 mi = as_half2(__byte_perm(vp[x][0][k], vp[x][1][k], 0x7632));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[x][i] = __hfma2(v[x][i], sc, mi);
+            for (int v = 0; v < 2; ++v) {
+              w[v] = __byte_perm(vw[v][0][k / 2], vw[v][1][k / 2], k & 1 ? 0x7632 : 0x5410);
+              h[v] = w[v] >> 8;
+              ps[v] = as_word(__hmul2(as_half2(pb[v]), as_half2(__byte_perm(vp[v][0][k], vp[v][1][k], 0x5410))));
+            }
+            mma16816_add(o[2 * k], w[0] & kLow, w[0] & kHigh, w[1] & kLow, w[1] & kHigh, ps[0], ps[1]);
+            mma16816_add(o[2 * k + 1], h[0] & kLow, h[0] & kHigh, h[1] & kLow, h[1] & kHigh, ps[0], ps[1]);
           }
-          mma16816_add(o[2 * k], as_word(v[0][0]), as_word(v[0][1]), as_word(v[1][0]), as_word(v[1][1]), pb[0], pb[1]);
-          mma16816_add(o[2 * k + 1], as_word(v[0][2]), as_word(v[0][3]), as_word(v[1][2]), as_word(v[1][3]), pb[0], pb[1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            __half2 n[2][4];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              unpack4(__byte_perm(vw[v][0][k / 2], vw[v][1][k / 2], k & 1 ? 0x7632 : 0x5410), n[v]);
+              const __half2 sc = as_half2(__byte_perm(vp[v][0][k], vp[v][1][k], 0x5410));
+              const __half2 mn = as_half2(__byte_perm(vp[v][0][k], vp[v][1][k], 0x7632));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) n[v][i] = __hfma2(n[v][i], sc, mn);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float c[4];
+              mma16816(c, as_word(n[0][2 * u]), as_word(n[0][2 * u + 1]), as_word(n[1][2 * u]),
+                       as_word(n[1][2 * u + 1]), pb[0], pb[1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[2 * k + u][i] = fmaf(c[i], i < 2 ? 0x1p-24f : 0x1p-20f, o[2 * k + u][i]);
+            }
+          }
         }
       }
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&empty[s]);
-      if (++s == S) {
-        s = 0;
-        parity ^= 1u;
-      }
     }
-#pragma unroll
-    for (int w = 4; w < 32; w <<= 1) {
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
-      l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
+    __syncwarp();
+    if (turn + S < turns) issue(turn + S, s);
+    if (++s == S) {
+      s = 0;
+      parity ^= 1u;
     }
-    // all stages are consumed once every warp is here: their memory takes the sums
-    sm100::named_bar_sync(1, 128);
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (2 * t + c < nh) {
-        float* sum = reinterpret_cast<float*>(smem) + (warp * 8 + 2 * t + c) * D + 4 * g;
-#pragma unroll
-        for (int k = 0; k < NG; ++k)
-          *reinterpret_cast<float4*>(sum + 32 * k) =
-              make_float4(o[2 * k][c], o[2 * k][2 + c], o[2 * k + 1][c], o[2 * k + 1][2 + c]);
-        if (g == 0) {
-          s_m[warp][2 * t + c] = m[c];
-          s_l[warp][2 * t + c] = l[c];
-        }
-      }
   }
+#pragma unroll
+  for (int w = 4; w < 32; w <<= 1) {
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
+    l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
+  }
+  float least[NG][2];
+#pragma unroll
+  for (int k = 0; k < NG; ++k)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) least[k][c] = __shfl_sync(0xffffffffu, om[c], 4 * k + t);
+  // the warp's stages are all read: their memory takes its sums
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (2 * t + c < nh) {
+      float* sum = reinterpret_cast<float*>(ring) + (2 * t + c) * D + 4 * g;
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+        *reinterpret_cast<float4*>(sum + 32 * k) =
+            make_float4(fmaf(o[2 * k][c], 0x1p24f, least[k][c]), fmaf(o[2 * k][2 + c], 0x1p20f, least[k][c]),
+                        fmaf(o[2 * k + 1][c], 0x1p24f, least[k][c]), fmaf(o[2 * k + 1][2 + c], 0x1p20f, least[k][c]));
+      if (g == 0) {
+        s_m[warp][2 * t + c] = m[c];
+        s_l[warp][2 * t + c] = l[c];
+      }
+    }
   __syncthreads();
   if (s_abort) return;  // reported in the error word; nothing is written
   for (int i = threadIdx.x; i < nh * D; i += kMmaThreads) {
@@ -700,7 +765,7 @@ __global__ void __launch_bounds__(kMmaThreads, 3) kv4_decode_mma_kernel(const __
     for (int w = 0; w < 4; ++w) {
       const float f = s_m[w][h] == -INFINITY ? 1.f : fast_exp2(s_m[w][h] - M);
       l += s_l[w][h] * f;
-      v += reinterpret_cast<const float*>(smem)[(w * 8 + h) * D + c] * f;
+      v += reinterpret_cast<const float*>(smem + w * Tile::kWarp)[h * D + c] * f;
     }
     const size_t row = (size_t)b * p.Hq + h0 + h;
     if (a.splits == 1) {
@@ -785,10 +850,14 @@ gbs_status resolve_cache(const Problem& p, const gbs_kv4_cache* in, Kv4* out) {
     if (in->max_blocks < p.Nb)
       return fail_status(GBS_ERR_INVALID_ARG, "max_blocks (%d) is below ceil(N / block) = %d", in->max_blocks, p.Nb);
     if (in->num_pages <= 0) return fail_status(GBS_ERR_INVALID_ARG, "num_pages must be positive");
+    if ((long long)in->num_pages * p.Hkv > INT32_MAX / 2)  // half blocks are counted in 32 bits
+      return fail_status(GBS_ERR_INVALID_ARG, "num_pages * Hkv must be below 2^30");
     if ((uintptr_t)in->block_table & 3u)
       return fail_status(GBS_ERR_INVALID_ARG, "block_table is not 4-byte aligned");
   } else if (in->cap < p.N || in->cap % p.bs) {
     return fail_status(GBS_ERR_INVALID_ARG, "cap (%d) must be a multiple of block and at least N = %d", in->cap, p.N);
+  } else if ((long long)p.B * p.Hkv * (in->cap / p.bs) > INT32_MAX / 2) {
+    return fail_status(GBS_ERR_INVALID_ARG, "B * Hkv * cap / block must be below 2^30");
   }
   out->kc = static_cast<uint8_t*>(in->kc);
   out->kp = static_cast<uint32_t*>(in->kp);

@@ -372,7 +372,7 @@ typedef struct gbs_kv4_cache {
   void* vc;   /* value codes                                                       */
   void* vp;   /* value parameters; all four 16-byte aligned                        */
   const int32_t* block_table; /* NULL: contiguous; else as in gbs_kv_layout        */
-  int max_blocks, num_pages;  /* as in gbs_kv_layout (num_pages without its limit) */
+  int max_blocks, num_pages;  /* as in gbs_kv_layout (num_pages * Hkv < 2^30)  */
   int cap;    /* contiguous: rows of a head, a multiple of block, >= p->N          */
 } gbs_kv4_cache;
 

@@ -8,11 +8,13 @@ Decode, for one query over the kept keys (p the weights, v the values):
        scale sum |q k| (a tensor core may cut instead of round: one step, not half),
        and the sums of exponentials and the logarithm by 2^-18 in all.
   O    the weights inherit the logits' error e (twice, in numerator and sum):
-       2 e sum p |v|; values are rounded to fp16 (2^-11 of |v|) and so are weights
-       (2^-11, or 2^-33 of the largest for the smallest of them); sums of fp32 as
-       above with at most 2^-16: (2 e + 2^-10 + 2^-16) sum p |v|, and half a step of
-       the output's type. With fp32 queries values and weights stay in fp32: the 2^-10
-       falls away.
+       2 e sum p |v|; sums of fp32 as above with at most 2^-16 of the same. With bf16
+       queries weights p are rounded to fp16 (2^-11 of |v|), then products s p (2^-11 of
+       s n <= |v| + |m|, with |m| <= 6 spread in the caches below) or values (2^-11 of
+       |v|); a product below fp16's normal range is cut to steps of 2^-24, off by 2^-25
+       times a code of at most 15, against a sum of weights of at least 4: 2^-23 a key.
+       In all (2 e + 2^-16) sum p |v|, with bf16 queries 2^-10 sum p |v| + 2^-11 6 spread
+       + 2^-23 keys more, and half a step of the output's type.
 """
 import math
 
@@ -238,7 +240,7 @@ def _run(x, L, k, shared, tau=None, splits=0, scale=0.0, **kw):
                          seq_lens=on["lens"], group_shared=shared, tau=tau, num_splits=splits, scale=scale, **kw)
 
 
-def _check(x, L, k, shared, tau=None, splits=0, scale=0.0):
+def _check(x, L, k, shared, tau=None, splits=0, scale=0.0, spread=1.0):
     O, LSE = _run(x, L, k, shared, tau, splits, scale)
     Or, Lr, A, Z = _reference(x, L, k, shared, tau, scale or None)
     d = x["q"].shape[2]
@@ -248,8 +250,10 @@ def _check(x, L, k, shared, tau=None, splits=0, scale=0.0):
     assert np.array_equal(np.isfinite(LSE), live) and bool((LSE[~live] == -np.inf).all())
     off = np.abs(LSE - Lr)[live] - e[live] - 2.0 ** -23 * np.abs(Lr[live])
     assert (off <= 0).all(), off.max()
-    value = 2.0 ** -16 + (2.0 ** -10 if x["q"].dtype == BF else 0)
-    _within(O, Or, (2 * e[..., None] + value) * A)
+    slack = (2 * e[..., None] + 2.0 ** -16) * A
+    if x["q"].dtype == BF:
+        slack += 2.0 ** -10 * A + 2.0 ** -11 * 6 * spread + 2.0 ** -23 * min(L, 64 * (k + 1))
+    _within(O, Or, slack)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -306,9 +310,9 @@ def test_idle_slots(dtype):
     _check(_decode_case(6, 1, 4, 2, 64, 300, [0], False, dtype), 300, 3, False)
 
 
-@pytest.mark.parametrize("spread", [1e-3, 30.0])
+@pytest.mark.parametrize("spread", [1e-3, 30.0, 6000.0])
 def test_decode_small_and_large_values(spread):
-    _check(_decode_case(7, 2, 4, 2, 128, 700, None, True, spread=spread), 700, 6, True, scale=0.02)
+    _check(_decode_case(7, 2, 4, 2, 128, 700, None, True, spread=spread), 700, 6, True, scale=0.02, spread=spread)
 
 
 def test_rows_behind_the_sequence_may_hold_anything():

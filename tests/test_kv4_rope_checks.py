@@ -24,9 +24,14 @@ def lib():
 
 @pytest.fixture
 def on_meta(monkeypatch):
-    """The checks run on meta tensors and stop before the library."""
+    """The calls run on meta tensors, with a library that returns success for everything."""
+    class Library:
+        def __getattr__(self, name):
+            return (lambda *a: 256) if name.endswith("_bytes") else lambda *a: 0
+
     monkeypatch.setattr(gb, "_DEVICE_TYPES", ("meta",))
-    monkeypatch.setattr(gb, "_called", lambda device, stream, fn: "called")
+    monkeypatch.setattr(gb, "load_library", Library)
+    monkeypatch.setattr(gb, "_current", lambda device: 0)
 
 
 def rejected(fn, *args, status=1, **kw):
@@ -171,10 +176,10 @@ def rope_args(B=2, N=9, Hq=4, Hkv=2, d=64, rot=64, axes=None, **kw):
 
 
 def test_rope_layouts(on_meta):
-    assert gb.qkv_rope(**rope_args()) == "called"
-    assert gb.qkv_rope(**rope_args(pos=meta(2, 9, 3, dtype=I32)), axes=[i % 3 for i in range(32)]) == "called"
+    assert [t.shape for t in gb.qkv_rope(**rope_args())] == [(2, 4, 9, 64), (2, 2, 9, 64), (2, 2, 9, 64)]
+    gb.qkv_rope(**rope_args(pos=meta(2, 9, 3, dtype=I32)), axes=[i % 3 for i in range(32)])
     w = dict(wq=meta(64, dtype=F32), wk=meta(64, dtype=F32))
-    assert gb.qkv_rope(**rope_args(), **w) == "called"
+    gb.qkv_rope(**rope_args(), **w)
     for kw, text in ((dict(k=meta(2, 9, 2, 64, dtype=F32)), "k has dtype"), (dict(v=meta(2, 9, 3, 64)), "v has shape"),
                      (dict(q=meta(2, 9, 64, 4).transpose(2, 3)), "contiguous channels"),
                      (dict(pos=meta(2, 9, dtype=torch.int64)), "pos has dtype"), (dict(pos=meta(2, 8, dtype=I32)), "pos"),
@@ -189,7 +194,7 @@ def test_rope_layouts(on_meta):
 
 def test_outputs_whose_elements_share_memory(on_meta):
     dev = torch.device("meta")
-    h = lambda t, out: gb._heads("t", "X", t, tuple(t.shape), (BF,), dev, 2, out)  # noqa: E731
+    h = lambda t, out: gb._heads("t", "X", t, tuple(t.shape), BF, dev, 2, out)  # noqa: E731
     shared = meta(2, 1, 9, 64).expand(2, 4, 9, 64)
     assert h(shared, False).stride_h == 0
     assert "share memory" in rejected(h, shared, True)
@@ -219,8 +224,11 @@ def test_kv4_layouts(on_meta):
         with pytest.raises(gb.GbsError, match=text):
             gb.kv4_append(*args, **kw)
     q, S = meta(B, 4, d), meta(B, 4, 4, dtype=F32)
-    assert gb.kv4_decode(q, flat, S, L) == "called"
-    assert gb.kv4_decode(q, pages, S, L, block_table=table, seq_lens=start) == "called"
+    assert [t.shape for t in gb.kv4_decode(q, flat, S, L)] == [(B, 4, d), (B, 4)]
+    gb.kv4_decode(q, pages, S, L, block_table=table, seq_lens=start)
+    assert [t.shape for t in gb.kv4_read(flat, start, 5)] == [(B, Hkv, 5, d)] * 2
+    with pytest.raises(gb.GbsError, match="out must be"):
+        gb.kv4_read(flat, start, 5, out=(K[:, :, :4], K[:, :, :4]))
     for kw, text in ((dict(L=257), "outside"), (dict(L=0), "outside"), (dict(S=meta(B, 2, 4, dtype=F32)), "S has"),
                      (dict(group_shared=True), "S has"), (dict(seq_lens=start[:1]), "seq_lens"),
                      (dict(out=meta(B, 4, d, dtype=F32)), "O has dtype"), (dict(q=q.half()), "float16")):
@@ -231,8 +239,8 @@ def test_kv4_layouts(on_meta):
 
 
 def test_axes_and_tables():
-    assert gb.rope_axes((2, 1, 1)) == [0, 0, 1, 2]
-    assert gb.rope_axes((3, 1, 2), interleaved=True) == [0, 1, 2, 0, 2, 0]
+    assert gb.rope_axes((2, 1, 1)) == (0, 0, 1, 2)
+    assert gb.rope_axes((3, 1, 2), interleaved=True) == (0, 1, 2, 0, 2, 0)
     cos, sin = gb.rope_tables(200001, 8, 10000.0, "cpu")
     angle = torch.tensor(200000.0, dtype=torch.float64) * 10000.0 ** -0.25
     assert cos.dtype == F32 and abs(float(cos[200000, 1]) - float(angle.cos())) < 2 ** -24
