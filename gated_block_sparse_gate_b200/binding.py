@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -83,7 +84,6 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(Params)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    H, C4 = ctypes.POINTER(Heads), ctypes.POINTER(Kv4CacheDesc)
     sigs = {
         "gbs_version": (i32, []),
         "gbs_status_string": (ctypes.c_char_p, [i32]),
@@ -99,14 +99,14 @@ def load_library(path: str = LIB_PATH):
                                 vp]),
         "gbs_set_timer": (i32, [i32, vp, vp]),
         "gbs_launch_count": (ctypes.c_uint64, []),
-        "gbs_qkv_rope_workspace_bytes": (sz, [ctypes.POINTER(RopeParams)]),
-        "gbs_qkv_rope_fwd": (i32, [ctypes.POINTER(RopeParams)] + [H] * 3 + [vp] * 5 + [H] * 3 + [vp] * 2),
-        "gbs_qkv_rope_bwd": (i32, [ctypes.POINTER(RopeParams)] + [H] * 2 + [vp] * 5 + [H] * 6
-                             + [vp] * 3 + [sz, vp]),
-        "gbs_kv4_append": (i32, [P, C4, H, H, i32, vp, vp, vp, vp]),
-        "gbs_kv4_read": (i32, [P, C4, H, H, i32, vp, vp, vp, vp]),
-        "gbs_kv4_workspace_bytes": (sz, [P]),
-        "gbs_kv4_decode": (i32, [P, C4, vp, i32, vp, vp, vp, vp, i32, vp, sz, vp]),
+        # structures go as bytes (struct.pack) or byref: both are addresses
+        "gbs_qkv_rope_workspace_bytes": (sz, [vp]),
+        "gbs_qkv_rope_fwd": (i32, [vp] * 14),
+        "gbs_qkv_rope_bwd": (i32, [vp] * 17 + [sz, vp]),
+        "gbs_kv4_append": (i32, [vp] * 4 + [i32] + [vp] * 4),
+        "gbs_kv4_read": (i32, [vp] * 4 + [i32] + [vp] * 4),
+        "gbs_kv4_workspace_bytes": (sz, [vp]),
+        "gbs_kv4_decode": (i32, [vp] * 3 + [i32] + [vp] * 4 + [i32, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -147,7 +147,7 @@ def _invalid(where, detail):
 
 def _device(where, name, t):
     """The device of the call's anchor tensor, which must be a CUDA tensor."""
-    if not isinstance(t, torch.Tensor):
+    if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
         raise _invalid(where, f"{name} must be a torch.Tensor")
     device = t.device
     if device.type not in _DEVICE_TYPES:
@@ -158,7 +158,7 @@ def _device(where, name, t):
 def _need(where, name, t, shape, dtypes, device):
     """t is a contiguous tensor on ``device`` with one of ``dtypes`` and, unless
     ``shape`` is None, exactly that shape: the layout the C ABI reads."""
-    if (type(t) is torch.Tensor and t.device == device and t.dtype in dtypes
+    if (type(t) is torch.Tensor and t.get_device() == device.index and t.dtype in dtypes
             and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor):
@@ -457,10 +457,20 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _heads(where, name, t, shape, dtype, device, n_dim=1, out=False):
-    """A [B, *, *, d] tensor with contiguous channels as gbs_heads; ``n_dim`` is
-    its token dimension (1: [B, N, H, d], 2: [B, H, N, d])."""
-    if not (type(t) is torch.Tensor and t.device == device and t.dtype is dtype and t.shape == shape):
+# The structures of include/gbs.h that the calls below pass, in C layout.
+_PARAMS = struct.Struct("9i2f").pack
+_HEADS = struct.Struct("P3q").pack
+_KV4 = struct.Struct("5P3i4x").pack
+_ROPE = struct.Struct("8i64s3if").pack
+assert struct.calcsize("9i2f") == ctypes.sizeof(Params) and struct.calcsize("P3q") == ctypes.sizeof(Heads)
+assert struct.calcsize("5P3i4x") == ctypes.sizeof(Kv4CacheDesc)
+assert struct.calcsize("8i64s3if") == ctypes.sizeof(RopeParams)
+
+
+def _heads(where, name, t, shape, dtype, device, token_major=False, out=False):
+    """A [B, H, N, d] tensor (``token_major``: [B, N, H, d]) with contiguous
+    channels as gbs_heads."""
+    if not (type(t) is torch.Tensor and t.get_device() == device.index and t.dtype is dtype and t.shape == shape):
         if not isinstance(t, torch.Tensor):
             raise _invalid(where, f"{name} must be a torch.Tensor")
         if t.device != device:
@@ -472,24 +482,19 @@ def _heads(where, name, t, shape, dtype, device, n_dim=1, out=False):
     b, x, y, c = t.stride()
     if c != 1:
         raise _invalid(where, f"{name} must have contiguous channels")
-    # the stride of a dimension of one is never followed
-    if shape[0] == 1:
-        b = 0
-    if shape[1] == 1:
-        x = 0
-    if shape[2] == 1:
-        y = 0
+    if 1 in shape:  # the stride of a dimension of one is never followed
+        b, x, y = (0 if n == 1 else step for n, step in zip(shape, (b, x, y)))
     if out and not t.is_contiguous():
         need = shape[3]
         for step, n in sorted(p for p in zip((b, x, y), shape) if p[1] > 1):
             if step < need:
                 raise _invalid(where, f"{name} is written and has elements that share memory")
             need = step * n
-    return Heads(t.data_ptr(), b, y, x) if n_dim == 1 else Heads(t.data_ptr(), b, x, y)
-
-
-def _opt(h):
-    return None if h is None else ctypes.byref(h)
+    if token_major:
+        x, y = y, x
+    if b < 0 or x < 0 or y < 0:  # (torch has none; pack would take them)
+        raise _invalid(where, f"{name} has a negative stride")
+    return _HEADS(t.data_ptr(), b, x, y)
 
 
 def _check_ws(where, ws, device):
@@ -524,24 +529,25 @@ def rope_axes(sections, interleaved=False):
     return tuple(out)
 
 
-_AxisArray = ctypes.c_ubyte * 64
+_ONE_AXIS = (0,) * 64
 
 
 @functools.lru_cache(maxsize=64)
-def _axis_array(axes, half, n_axes):
-    """The axes of ``half`` pairs as the C array, or the reason why they are refused."""
+def _axis_bytes(axes, half, n_axes):
+    """The axes of ``half`` pairs as bytes, or the text why they are refused."""
     if len(axes) != half:
         return f"axes has {len(axes)} entries; expected one of each of the {half} pairs"
     if not all(0 <= a < n_axes for a in axes):
         return f"an axis is outside [0, {n_axes})"
-    return _AxisArray(*axes)
+    return bytes(axes)
 
 
 def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev):
-    """The parameters of a qkv_rope call, its small tensors checked."""
+    """The parameters of a qkv_rope call and (B, N, Hq, Hkv, d), its small tensors checked."""
     if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise _invalid(where, "q and k must be 4-D: [B, N, H, d]")
     B, N, Hq, d = q.shape
+    Hkv = k.shape[2]
     _act_dtype(where, "q", q)
     if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
         raise _invalid(where, "cos must be [max_pos, rot / 2]")
@@ -554,7 +560,7 @@ def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev):
     _need(where, "pos", pos, (B, N) if pos.dim() == 2 else (B, N, n_axes), _I32, dev)
     if half > 64:
         raise _invalid(where, f"cos has {half} columns; at most d / 2 = {d // 2} pairs are rotated")
-    axis = _axis_array((0,) * half if axes is None else tuple(axes), half, n_axes)
+    axis = _axis_bytes(_ONE_AXIS[:half] if axes is None else tuple(axes), half, n_axes)
     if type(axis) is str:
         raise _invalid(where, axis)
     if (wq is None) != (wk is None):
@@ -564,8 +570,8 @@ def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev):
         _need(where, "wq", wq, (d,), _WEIGHTS, dev)
         _need(where, "wk", wk, (d,), (wq.dtype,), dev)
         w_dtype = DTYPES[wq.dtype]
-    return RopeParams(B, N, Hq, k.shape[2], d, 2 * half, 1 if interleaved else 0, n_axes, axis, max_pos,
-                      DTYPES[q.dtype], w_dtype, eps)
+    return _ROPE(B, N, Hq, Hkv, d, 2 * half, 1 if interleaved else 0, n_axes, axis, max_pos, DTYPES[q.dtype],
+                 w_dtype, eps), (B, N, Hq, Hkv, d)
 
 
 def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, interleaved=False, out=None,
@@ -586,24 +592,23 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
     if ctx is not None:
         with ctx:
             return qkv_rope(q, k, v, cos, sin, pos, wq, wk, eps, axes, interleaved, out, ws)
-    p = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
-    B, N, Hq, d = q.shape
-    Hkv, act = p.Hkv, q.dtype
-    hq = _heads(where, "q", q, (B, N, Hq, d), act, dev)
-    hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev)
-    hv = None if v is None else _heads(where, "v", v, (B, N, Hkv, d), act, dev)
+    p, (B, N, Hq, Hkv, d) = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
+    act = q.dtype
+    hq = _heads(where, "q", q, (B, N, Hq, d), act, dev, True)
+    hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev, True)
+    hv = None if v is None else _heads(where, "v", v, (B, N, Hkv, d), act, dev, True)
     if out is not None and (len(out) != 3 or (out[2] is None) != (v is None)):
         raise _invalid(where, "out must be (Q, K, V), V None exactly if v is")
     _check_ws(where, ws, dev)
     Q, K, V = out if out is not None else (
-        torch.empty(B, Hq, N, d, dtype=act, device=dev), torch.empty(B, Hkv, N, d, dtype=act, device=dev),
-        None if v is None else torch.empty(B, Hkv, N, d, dtype=act, device=dev))
-    oq = _heads(where, "Q", Q, (B, Hq, N, d), act, dev, 2, True)
-    ok = _heads(where, "K", K, (B, Hkv, N, d), act, dev, 2, True)
-    ov = None if v is None else _heads(where, "V", V, (B, Hkv, N, d), act, dev, 2, True)
-    _check(lib.gbs_qkv_rope_fwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _opt(hv), _addr(wq),
-                                _addr(wk), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), ctypes.byref(oq),
-                                ctypes.byref(ok), _opt(ov), _addr(ws), _current(dev)), where)
+        q.new_empty((B, Hq, N, d)), q.new_empty((B, Hkv, N, d)), None if v is None else q.new_empty((B, Hkv, N, d)))
+    oq = _heads(where, "Q", Q, (B, Hq, N, d), act, dev, out=True)
+    ok = _heads(where, "K", K, (B, Hkv, N, d), act, dev, out=True)
+    ov = None if v is None else _heads(where, "V", V, (B, Hkv, N, d), act, dev, out=True)
+    s = lib.gbs_qkv_rope_fwd(p, hq, hk, hv, _addr(wq), _addr(wk), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(),
+                             oq, ok, ov, _addr(ws), _current(dev))
+    if s:
+        _check(s, where)
     return Q, K, V
 
 
@@ -621,39 +626,37 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
     if ctx is not None:
         with ctx:
             return qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV, wq, wk, eps, axes, interleaved, grads, ws)
-    p = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
-    B, N, Hq, d = q.shape
-    Hkv, act = p.Hkv, q.dtype
-    hq = _heads(where, "q", q, (B, N, Hq, d), act, dev)
-    hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev)
-    zq = _heads(where, "dQ", dQ, (B, Hq, N, d), act, dev, 2)
-    zk = _heads(where, "dK", dK, (B, Hkv, N, d), act, dev, 2)
-    zv = None if dV is None else _heads(where, "dV", dV, (B, Hkv, N, d), act, dev, 2)
+    p, (B, N, Hq, Hkv, d) = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
+    act = q.dtype
+    hq = _heads(where, "q", q, (B, N, Hq, d), act, dev, True)
+    hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev, True)
+    zq = _heads(where, "dQ", dQ, (B, Hq, N, d), act, dev)
+    zk = _heads(where, "dK", dK, (B, Hkv, N, d), act, dev)
+    zv = None if dV is None else _heads(where, "dV", dV, (B, Hkv, N, d), act, dev)
     if grads is not None and (len(grads) != 3 or (grads[2] is None) != (dV is None)):
         raise _invalid(where, "grads must be (dq, dk, dv), dv None exactly if dV is")
     if ws is not None:
         _need(where, "ws", ws, None, _U8, dev)
     dq, dk, dv = grads if grads is not None else (
-        torch.empty(B, N, Hq, d, dtype=act, device=dev), torch.empty(B, N, Hkv, d, dtype=act, device=dev),
-        None if dV is None else torch.empty(B, N, Hkv, d, dtype=act, device=dev))
-    oq = _heads(where, "dq", dq, (B, N, Hq, d), act, dev, 1, True)
-    ok = _heads(where, "dk", dk, (B, N, Hkv, d), act, dev, 1, True)
-    ov = None if dV is None else _heads(where, "dv", dv, (B, N, Hkv, d), act, dev, 1, True)
-    dwq, dwk = (None, None) if wq is None else torch.empty(2, d, dtype=torch.float32, device=dev).unbind()
+        q.new_empty((B, N, Hq, d)), q.new_empty((B, N, Hkv, d)), None if dV is None else q.new_empty((B, N, Hkv, d)))
+    oq = _heads(where, "dq", dq, (B, N, Hq, d), act, dev, True, True)
+    ok = _heads(where, "dk", dk, (B, N, Hkv, d), act, dev, True, True)
+    ov = None if dV is None else _heads(where, "dv", dv, (B, N, Hkv, d), act, dev, True, True)
+    dwq, dwk = (None, None) if wq is None else q.new_empty((2, d), dtype=torch.float32).unbind()
     if ws is None:
-        ws = torch.empty(lib.gbs_qkv_rope_workspace_bytes(ctypes.byref(p)) or 256, dtype=torch.uint8, device=dev)
-    _check(lib.gbs_qkv_rope_bwd(ctypes.byref(p), ctypes.byref(hq), ctypes.byref(hk), _addr(wq), _addr(wk),
-                                cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), ctypes.byref(zq),
-                                ctypes.byref(zk), _opt(zv), ctypes.byref(oq), ctypes.byref(ok), _opt(ov),
-                                _addr(dwq), _addr(dwk), ws.data_ptr(), ws.numel(), _current(dev)), where)
+        ws = q.new_empty(lib.gbs_qkv_rope_workspace_bytes(p) or 256, dtype=torch.uint8)
+    s = lib.gbs_qkv_rope_bwd(p, hq, hk, _addr(wq), _addr(wk), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), zq, zk,
+                             zv, oq, ok, ov, _addr(dwq), _addr(dwk), ws.data_ptr(), ws.numel(), _current(dev))
+    if s:
+        _check(s, where)
     return dq, dk, dv, dwq, dwk
 
 
 def qkv_rope_workspace_bytes(q, k, rot):
     """Bytes of ``ws`` for ``qkv_rope_backward`` (``qkv_rope`` takes the same one)."""
     B, N, Hq, d = q.shape
-    p = RopeParams(B, N, Hq, k.shape[2], d, rot, 0, 1, _AxisArray(), 1, DTYPES[q.dtype], 1, 0.0)
-    n = int(load_library().gbs_qkv_rope_workspace_bytes(ctypes.byref(p)))
+    p = _ROPE(B, N, Hq, k.shape[2], d, rot, 0, 1, b"", 1, DTYPES[q.dtype], 1, 0.0)
+    n = int(load_library().gbs_qkv_rope_workspace_bytes(p))
     if n == 0:
         raise GbsError(1, "gbs_qkv_rope_workspace_bytes", load_library().gbs_last_error().decode())
     return n
@@ -694,14 +697,14 @@ def _check_kv4(where, cache, B, d, device, block, block_table):
     _need(where, "value codes", vc, codes, _U8, device)
     _need(where, "value parameters", vp, params, _F16, device)
     if block_table is None:
-        desc = Kv4CacheDesc(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), None, 0, 0, rows)
+        desc = _KV4(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), 0, 0, 0, rows)
         return desc, Hkv, rows
     _need(where, "block_table", block_table, None, _I32, device)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise _invalid(where, f"block_table must be [B={B}, max_blocks]")
     max_blocks = block_table.shape[1]
-    desc = Kv4CacheDesc(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), block_table.data_ptr(),
-                        max_blocks, first, rows)
+    desc = _KV4(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), block_table.data_ptr(), max_blocks, first,
+                rows)
     return desc, Hkv, max_blocks * block
 
 
@@ -713,17 +716,18 @@ def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out,
     act = K.dtype
     _act_dtype(where, "K", K)
     desc, Hkv, L = _check_kv4(where, cache, B, d, dev, block, block_table)
-    hk = _heads(where, "K", K, (B, Hkv, T, d), act, dev, 2, out)
-    hv = _heads(where, "V", V, (B, Hkv, T, d), act, dev, 2, out)
+    hk = _heads(where, "K", K, (B, Hkv, T, d), act, dev, False, out)
+    hv = _heads(where, "V", V, (B, Hkv, T, d), act, dev, False, out)
     _need(where, "start", start, (B,), _I32, dev)
     if count is not None:
         _need(where, "count", count, (B,), _I32, dev)
     _check_ws(where, ws, dev)
     if T == 0:
         return
-    p = Params(B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[act], 0.0, 0.0)
-    _check(fn(ctypes.byref(p), ctypes.byref(desc), ctypes.byref(hk), ctypes.byref(hv), T, start.data_ptr(),
-              _addr(count), _addr(ws), _current(dev)), where)
+    s = fn(_PARAMS(B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[act], 0.0, 0.0), desc, hk, hv, T, start.data_ptr(),
+           _addr(count), _addr(ws), _current(dev))
+    if s:
+        _check(s, where)
 
 
 def kv4_append(K, V, cache, start, block_table=None, count=None, block=64, ws=None, stream=None):
@@ -762,7 +766,7 @@ def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16
         raise _invalid(where, "T must not be negative")
     if out is None:
         shape = (start.shape[0], cache[0].shape[1], T, 2 * cache[0].shape[3])
-        K, V = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+        K, V = start.new_empty(shape, dtype=dtype), start.new_empty(shape, dtype=dtype)
     else:
         K, V = out
         _device(where, "K", K)
@@ -803,19 +807,20 @@ def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block
         _need(where, "seq_lens", seq_lens, (B,), _I32, dev)
     if ws is not None:
         _need(where, "ws", ws, None, _U8, dev)
-    p = Params(B, Hq, Hkv, L, d, block, topk, 1 if tau is None else 2, DTYPES[q.dtype], scale,
-               0.0 if tau is None else tau)
+    p = _PARAMS(B, Hq, Hkv, L, d, block, topk, 1 if tau is None else 2, DTYPES[q.dtype], scale,
+                0.0 if tau is None else tau)
     if out is None:
         out = torch.empty_like(q)
     else:
         _need(where, "O", out, (B, Hq, d), act, dev)
     if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
     else:
         _need(where, "LSE", lse, (B, Hq), _F32, dev)
     if ws is None:
-        ws = torch.empty(lib.gbs_kv4_workspace_bytes(ctypes.byref(p)) or 256, dtype=torch.uint8, device=dev)
-    _check(lib.gbs_kv4_decode(ctypes.byref(p), ctypes.byref(desc), _addr(seq_lens), 1 if group_shared else 0,
-                              q.data_ptr(), S.data_ptr(), out.data_ptr(), lse.data_ptr(), num_splits,
-                              ws.data_ptr(), ws.numel(), _current(dev)), where)
+        ws = q.new_empty(lib.gbs_kv4_workspace_bytes(p) or 256, dtype=torch.uint8)
+    s = lib.gbs_kv4_decode(p, desc, _addr(seq_lens), 1 if group_shared else 0, q.data_ptr(), S.data_ptr(),
+                           out.data_ptr(), lse.data_ptr(), num_splits, ws.data_ptr(), ws.numel(), _current(dev))
+    if s:
+        _check(s, where)
     return out, lse

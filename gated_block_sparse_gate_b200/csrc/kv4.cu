@@ -4,6 +4,7 @@
 // A group of 32 channels of one token and head is stored as fp16 (scale s,
 // minimum m) and codes n in 0..15; a code stands for m + s n. Channel c has
 // nibble c % 4 of the row's 16-bit word (c % 32) / 4 * (d / 32) + c / 32.
+#include <atomic>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -809,14 +810,45 @@ int decode4_rows(const DecodeArgs& a) {
   return a.grouped ? a.p.B * a.p.Hkv * ((a.p.G + 7) / 8) : a.p.B * a.p.Hq;
 }
 
+// Splits of every CTA row's n_ent blocks. A CTA costs its share and about two blocks'
+// worth of beginning and end; while all CTAs fit on the GPU at once the largest share
+// is what counts, beyond that their number (64 x 131072, K = 32, 2048 rows: 1 split
+// 160 us, 2 splits 166, 4 splits 184; 102 rows of 49 blocks: 1 split 30 us, 4 splits 16).
+int decode4_splits(int rows, int n_ent, int slots) {
+  int best = 1;
+  float least = 0.f;
+  for (int s = 1; s <= n_ent && s <= kMaxDecodeSplits; ++s) {
+    const float load = (float)rows * s / slots;
+    const float cost = (load <= 1.f ? 1.f : load + 0.5f) * ((n_ent + s - 1) / s + 2);
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+// SMs of a device, asked for once.
+cudaError_t sm_count(int device, int* sms) {
+  static std::atomic<int> known[64];
+  if (device < 64 && (*sms = known[device].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  const cudaError_t e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device);
+  if (e == cudaSuccess && device < 64) known[device].store(*sms, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename T, int D>
-cudaError_t launch_decode4(const DecodeArgs& a, cudaStream_t st) {
+cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
   const int rows = a.p.B * a.p.Hq;
   cudaError_t e;
   if constexpr (sizeof(T) == 2) {
-    e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Kv4Tile<D>::kBytes);
-    if (e != cudaSuccess) return e;
+    static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use this much shared memory
+    if (device >= 64 || !(ready.load(std::memory_order_acquire) >> device & 1)) {
+      e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Kv4Tile<D>::kBytes);
+      if (e != cudaSuccess) return e;
+      if (device < 64) ready.fetch_or(1ull << device, std::memory_order_release);
+    }
     timer_begin(GBS_OP_DECODE, st);
     kv4_decode_mma_kernel<D><<<dim3(decode4_rows(a), a.splits), kMmaThreads, Kv4Tile<D>::kBytes, st>>>(a);
     timer_end(GBS_OP_DECODE, st);
@@ -995,19 +1027,21 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   seq.lens = seq_lens;
   seq.rows_per_seq = group_shared ? p.Hkv : p.Hq;
   seq.max_len = p.N;
-  cudaError_t e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode,
+  int device = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = sm_count(device, &sms);
+  if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/device");
+  e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode,
                                 p.log_tau, a.sel.idx, a.sel.cnt, a.sel.logg, nullptr, st, nullptr, nullptr, 0, seq);
   if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/select");
   const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1;
   a.splits = num_splits;
-  if (a.splits == 0) {
-    e = decode_auto_splits(p, false, n_ent, &a.splits);
-    if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/splits");
-  }
+  if (a.splits == 0)
+    a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms);
   if (a.splits > n_ent) a.splits = n_ent;
   if (p.dtype == GBS_BF16)
-    e = p.d == 64 ? launch_decode4<__nv_bfloat16, 64>(a, st) : launch_decode4<__nv_bfloat16, 128>(a, st);
+    e = p.d == 64 ? launch_decode4<__nv_bfloat16, 64>(a, device, st) : launch_decode4<__nv_bfloat16, 128>(a, device, st);
   else
-    e = p.d == 64 ? launch_decode4<float, 64>(a, st) : launch_decode4<float, 128>(a, st);
+    e = p.d == 64 ? launch_decode4<float, 64>(a, device, st) : launch_decode4<float, 128>(a, device, st);
   return cuda_done(e, "gbs_kv4_decode");
 }

@@ -6,50 +6,112 @@
 // (halves: channels 4 l .. 4 l + 3 and rot / 2 + 4 l ..; neighbours, and channels
 // that are not rotated: 8 l .. 8 l + 7). The norm's sums go over the row's lanes
 // by shuffles. A row is read once and written once, and the cos and sin of a
-// token stay in registers for all of its heads, so the pass is bound by memory.
+// token stay in registers for all of its heads, so the pass is bound by memory. A
+// CTA works on one tensor: its 16 lane groups (d = 128) walk along the heads of 16
+// adjacent tokens, which is 8 KB in a row in the projection for each group (32 heads)
+// and 4 KB in a row in every head's plane for all of them; with four groups to a token
+// the forward took 342 us instead of 305.
 #include <math.h>
 #include <string.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "sm100.cuh"
 
 namespace gbs {
 namespace {
 
+using namespace sm100;  // f32x2
+
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows whose loads are in flight before any arithmetic
+// Rows whose loads a lane group has in flight before any arithmetic. Two, with the
+// registers held to four (backward: three) CTAs an SM, measured best: forward of 65536
+// tokens (32 + 16 heads, d = 128, bf16) 297 us against 305 with four rows and three CTAs
+// and 342 with eight rows and two.
+constexpr int kRows = 2;
 
 struct RopeArgs {
   int B, N, Hq, Hkv, half, interleaved, n_axes, max_pos, norm, w_bf16;
-  int per_token;  // lane groups that share a token's heads
+  int per_token[2];  // lane groups that share a token's heads: of q; of k and v
+  int ctas[3];       // CTAs of q, k, v, in this order
   float eps;
   const void *wq, *wk;
   const float *cos_tab, *sin_tab;
   const int32_t* pos;
   Heads in[3], out[3];  // q, k, v and what becomes of them (backward: dQ, dK, dV -> dq, dk, dv)
   Heads x[2];           // backward: q, k
-  float* part;          // backward: [CTAs][2][d] partial sums of dwq, dwk
+  float* part;          // backward: [CTAs of q and k][d] partial sums of dwq, dwk
   unsigned int* err;
-  unsigned char axis[64];
+  alignas(4) unsigned char axis[64];
+};
+
+// Eight channels of a lane as two vectors of first (p) and second (r) members of four
+// pairs, in packed fp32 pairs (two lanes of arithmetic an instruction).
+struct Pairs {
+  f32x2 p[2], r[2];
 };
 
 template <typename T> struct Quad;  // four channels as one load
 template <> struct Quad<float> { using type = float4; };
 template <> struct Quad<__nv_bfloat16> { using type = uint2; };
 
-__device__ __forceinline__ void widen(const float4& u, float* v) {
-  v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+__device__ __forceinline__ f32x2 make2(uint32_t lo, uint32_t hi) {
+  return f2_make(__uint_as_float(lo), __uint_as_float(hi));
 }
-__device__ __forceinline__ void widen(const uint2& u, float* v) {
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+// INTER: pairs are neighbours; else pair i is (a[i], b[i]).
+template <bool INTER>
+__device__ __forceinline__ Pairs widen(const float4& a, const float4& b) {
+  if (INTER) return {{f2_make(a.x, a.z), f2_make(b.x, b.z)}, {f2_make(a.y, a.w), f2_make(b.y, b.w)}};
+  return {{f2_make(a.x, a.y), f2_make(a.z, a.w)}, {f2_make(b.x, b.y), f2_make(b.z, b.w)}};
 }
-__device__ __forceinline__ void narrow(const float* v, float4* u) {
-  *u = make_float4(v[0], v[1], v[2], v[3]);
+template <bool INTER>
+__device__ __forceinline__ Pairs widen(const uint2& a, const uint2& b) {
+  constexpr uint32_t H = 0xffff0000u;
+  if (INTER)
+    return {{make2(a.x << 16, a.y << 16), make2(b.x << 16, b.y << 16)}, {make2(a.x & H, a.y & H), make2(b.x & H, b.y & H)}};
+  return {{make2(a.x << 16, a.x & H), make2(a.y << 16, a.y & H)}, {make2(b.x << 16, b.x & H), make2(b.y << 16, b.y & H)}};
 }
-__device__ __forceinline__ void narrow(const float* v, uint2* u) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  *u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool INTER>
+__device__ __forceinline__ void narrow(const Pairs& v, float4* a, float4* b) {
+  float p[4], r[4];
+  f2_split(v.p[0], p[0], p[1]); f2_split(v.p[1], p[2], p[3]);
+  f2_split(v.r[0], r[0], r[1]); f2_split(v.r[1], r[2], r[3]);
+  *a = INTER ? make_float4(p[0], r[0], p[1], r[1]) : make_float4(p[0], p[1], p[2], p[3]);
+  *b = INTER ? make_float4(p[2], r[2], p[3], r[3]) : make_float4(r[0], r[1], r[2], r[3]);
+}
+template <bool INTER>
+__device__ __forceinline__ void narrow(const Pairs& v, uint2* a, uint2* b) {
+  float4 x, y;
+  narrow<INTER>(v, &x, &y);
+  *a = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+  *b = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+}
+// sum of the products of all channels
+__device__ __forceinline__ float dot(const Pairs& x, const Pairs& y) {
+  const f32x2 s = f2_fma(x.r[1], y.r[1], f2_fma(x.r[0], y.r[0], f2_fma(x.p[1], y.p[1], f2_mul(x.p[0], y.p[0]))));
+  float lo, hi;
+  f2_split(s, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ Pairs times(const Pairs& x, const Pairs& y) {
+  return {{f2_mul(x.p[0], y.p[0]), f2_mul(x.p[1], y.p[1])}, {f2_mul(x.r[0], y.r[0]), f2_mul(x.r[1], y.r[1])}};
+}
+__device__ __forceinline__ Pairs times(const Pairs& x, float f) {
+  const f32x2 y = f2_make(f, f);
+  return {{f2_mul(x.p[0], y), f2_mul(x.p[1], y)}, {f2_mul(x.r[0], y), f2_mul(x.r[1], y)}};
+}
+// x y + z and f x + z
+__device__ __forceinline__ Pairs fma(const Pairs& x, const Pairs& y, const Pairs& z) {
+  return {{f2_fma(x.p[0], y.p[0], z.p[0]), f2_fma(x.p[1], y.p[1], z.p[1])},
+          {f2_fma(x.r[0], y.r[0], z.r[0]), f2_fma(x.r[1], y.r[1], z.r[1])}};
+}
+__device__ __forceinline__ Pairs fma(float f, const Pairs& x, const Pairs& z) {
+  const f32x2 y = f2_make(f, f);
+  return {{f2_fma(x.p[0], y, z.p[0]), f2_fma(x.p[1], y, z.p[1])}, {f2_fma(x.r[0], y, z.r[0]), f2_fma(x.r[1], y, z.r[1])}};
 }
 
 template <int LANES>
@@ -59,65 +121,70 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// What a lane keeps of its token: the angles of its four pairs.
+// What a lane keeps of its token: the angles of its four pairs, sin with either sign.
 struct Angles {
-  float c[4], s[4];
-  int mode;  // 0: not rotated, 1: pairs (v[i], v[4 + i]), 2: pairs (v[2 i], v[2 i + 1])
+  f32x2 c[2], s[2], minus_s[2];
 };
 
-__device__ __forceinline__ Angles load_angles(const RopeArgs& a, long long token, int lane, bool valid) {
-  Angles r;
-  const int i0 = 4 * lane;
-  r.mode = i0 < a.half ? (a.interleaved ? 2 : 1) : 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.c[i] = 1.f, r.s[i] = 0.f;
-  if (r.mode && valid) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int p = __ldg(a.pos + token * a.n_axes + a.axis[i0 + i]);
-      if (p < 0 || p >= a.max_pos) {
-        set_error(a.err, GBS_ERR_INVALID_ARG);
-        p = p < 0 ? 0 : a.max_pos - 1;
-      }
-      r.c[i] = __ldg(a.cos_tab + (size_t)p * a.half + i0 + i);
-      r.s[i] = __ldg(a.sin_tab + (size_t)p * a.half + i0 + i);
-    }
+__device__ __forceinline__ int table_row(const RopeArgs& a, long long token, int axis) {
+  int p = __ldg(a.pos + token * a.n_axes + axis);
+  if (p < 0 || p >= a.max_pos) {
+    set_error(a.err, GBS_ERR_INVALID_ARG);
+    p = p < 0 ? 0 : a.max_pos - 1;
   }
-  return r;
+  return p;
 }
 
-// Rotates eight channels by the angles (SIGN = -1: by their negatives).
-template <int SIGN>
-__device__ __forceinline__ void rotate(float (&v)[8], const Angles& r) {
-  if (r.mode == 1) {
+// axes: the axes of the lane's four pairs, a byte each. Called for lanes that rotate.
+__device__ __forceinline__ Angles load_angles(const RopeArgs& a, long long token, int lane, uint32_t axes) {
+  float4 c, s;
+  const int i0 = 4 * lane;
+  if (axes == (axes & 0xffu) * 0x01010101u) {
+    const size_t at = (size_t)table_row(a, token, axes & 0xffu) * a.half + i0;
+    c = __ldg(reinterpret_cast<const float4*>(a.cos_tab + at));
+    s = __ldg(reinterpret_cast<const float4*>(a.sin_tab + at));
+  } else {
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = v[i], y = v[4 + i], s = SIGN * r.s[i];
-      v[i] = x * r.c[i] - y * s;
-      v[4 + i] = y * r.c[i] + x * s;
+      const size_t at = (size_t)table_row(a, token, axes >> (8 * i) & 0xffu) * a.half + i0 + i;
+      v[i] = __ldg(a.cos_tab + at);
+      v[4 + i] = __ldg(a.sin_tab + at);
     }
-  } else if (r.mode == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = v[2 * i], y = v[2 * i + 1], s = SIGN * r.s[i];
-      v[2 * i] = x * r.c[i] - y * s;
-      v[2 * i + 1] = y * r.c[i] + x * s;
-    }
+    c = make_float4(v[0], v[1], v[2], v[3]);
+    s = make_float4(v[4], v[5], v[6], v[7]);
   }
+  return {{f2_make(c.x, c.y), f2_make(c.z, c.w)}, {f2_make(s.x, s.y), f2_make(s.z, s.w)},
+          {f2_make(-s.x, -s.y), f2_make(-s.z, -s.w)}};
+}
+
+// Rotates by the angles (BACK: by their negatives).
+template <bool BACK>
+__device__ __forceinline__ void rotate(Pairs& v, const Angles& t) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x2 p = v.p[i], r = v.r[i];
+    v.p[i] = f2_fma(r, BACK ? t.s[i] : t.minus_s[i], f2_mul(p, t.c[i]));
+    v.r[i] = f2_fma(p, BACK ? t.minus_s[i] : t.s[i], f2_mul(r, t.c[i]));
+  }
+}
+
+__device__ __forceinline__ bool lane_rotates(const RopeArgs& a, int lane) { return 4 * lane < a.half; }
+__device__ __forceinline__ uint32_t lane_axes(const RopeArgs& a, int lane) {
+  return lane_rotates(a, lane) ? *reinterpret_cast<const uint32_t*>(a.axis + 4 * lane) : 0u;
 }
 
 // First channels of a lane's two quads.
+template <bool INTER>
 __device__ __forceinline__ void quad_offsets(const RopeArgs& a, int lane, int* off) {
-  if (!a.interleaved && 4 * lane < a.half) {
-    off[0] = 4 * lane;
-    off[1] = a.half + 4 * lane;
-  } else {
-    off[0] = 8 * lane;
-    off[1] = 8 * lane + 4;
-  }
+  const bool apart = !INTER && lane_rotates(a, lane);
+  off[0] = apart ? 4 * lane : 8 * lane;
+  off[1] = apart ? a.half + 4 * lane : 8 * lane + 4;
 }
 
-__device__ __forceinline__ void load_weights(const RopeArgs& a, const void* w, const int* off, float (&v)[8]) {
+template <bool INTER>
+__device__ __forceinline__ Pairs load_weights(const RopeArgs& a, const void* w, const int* off) {
+  float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = off[i >> 2] + (i & 3);
@@ -125,200 +192,191 @@ __device__ __forceinline__ void load_weights(const RopeArgs& a, const void* w, c
               : (a.w_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[c])
                           : reinterpret_cast<const float*>(w)[c]);
   }
+  return widen<INTER>(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]));
 }
 
-template <typename T>
-__device__ __forceinline__ T* row_ptr(const Heads& t, int b, int h, int n) {
-  return reinterpret_cast<T*>(t.ptr) + b * t.sb + h * t.sh + n * t.sn;
+// Which of the three tensors a CTA works on, its place among that tensor's CTAs, and their number.
+struct Role {
+  int which, index, count, per_token;
+};
+__device__ __forceinline__ Role cta_role(const RopeArgs& a) {
+  int x = blockIdx.x;
+  if (x < a.ctas[0]) return {0, x, a.ctas[0], a.per_token[0]};
+  x -= a.ctas[0];
+  if (x < a.ctas[1]) return {1, x, a.ctas[1], a.per_token[1]};
+  return {2, x - a.ctas[1], a.ctas[2], a.per_token[1]};
 }
 
 // One of the three tensors of a token: heads h = sub, sub + per_token, ...
 // WHICH: 0 = q, 1 = k (norm and rotation), 2 = v (moved).
-template <typename T, int D, int WHICH>
-__device__ __forceinline__ void forward_heads(const RopeArgs& a, int b, int n, int sub, bool valid,
-                                              const Angles& ang, const int* off) {
+template <typename T, int D, int WHICH, bool INTER>
+__device__ __forceinline__ void forward_tensor(const RopeArgs& a, const Role& role) {
   using Q4 = typename Quad<T>::type;
-  const int H = WHICH == 0 ? a.Hq : a.Hkv;
-  float w[8];
-  if (WHICH < 2) load_weights(a, WHICH == 0 ? a.wq : a.wk, off, w);
-  const int rounds = (H + a.per_token * kUnroll - 1) / (a.per_token * kUnroll);
-  for (int it = 0; it < rounds; ++it) {
-    Q4 raw[kUnroll][2];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = sub + (it * kUnroll + u) * a.per_token;
-      if (valid && h < H) {
-        const T* src = row_ptr<T>(a.in[WHICH], b, h, n);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) raw[u][j] = __ldg(reinterpret_cast<const Q4*>(src + off[j]));
-      } else {
-        raw[u][0] = raw[u][1] = Q4{};
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = sub + (it * kUnroll + u) * a.per_token;
-      if (WHICH < 2) {
-        float v[8];
-        widen(raw[u][0], v);
-        widen(raw[u][1], v + 4);
-        if (a.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-          const float r = rsqrtf(row_sum<D / 8>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= r * w[i];
-        }
-        rotate<1>(v, ang);
-        narrow(v, &raw[u][0]);
-        narrow(v + 4, &raw[u][1]);
-      }
-      if (valid && h < H) {
-        T* dst = row_ptr<T>(a.out[WHICH], b, h, n);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) *reinterpret_cast<Q4*>(dst + off[j]) = raw[u][j];
-      }
-    }
-  }
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const int tokens_per_cta = GROUPS / a.per_token;
-  const long long tokens = (long long)a.B * a.N;
-  const long long token = (long long)blockIdx.x * tokens_per_cta + group / a.per_token;
-  const int sub = group % a.per_token;
-  const bool valid = token < tokens;
-  const int b = valid ? (int)(token / a.N) : 0, n = valid ? (int)(token - (long long)b * a.N) : 0;
-  const Angles ang = load_angles(a, token, lane, valid);
-  int off[2];
-  quad_offsets(a, lane, off);
-  forward_heads<T, D, 0>(a, b, n, sub, valid, ang, off);
-  forward_heads<T, D, 1>(a, b, n, sub, valid, ang, off);
-  if (a.in[2].ptr) {
-    int straight[2] = {8 * lane, 8 * lane + 4};
-    forward_heads<T, D, 2>(a, b, n, sub, valid, ang, straight);
-  }
-}
-
-// Backward of q (WHICH 0), k (1): dx from x and dz, and this lane's share of dw.
-template <typename T, int D, int WHICH>
-__device__ __forceinline__ void backward_heads(const RopeArgs& a, int b, int n, int sub, bool valid,
-                                               const Angles& ang, const int* off, const float (&w)[8],
-                                               float (&dw)[8]) {
-  using Q4 = typename Quad<T>::type;
-  constexpr int kRows = 2;  // two rows of x and dz in flight
-  const int H = WHICH == 0 ? a.Hq : a.Hkv;
-  const int rounds = (H + a.per_token * kRows - 1) / (a.per_token * kRows);
-  for (int it = 0; it < rounds; ++it) {
-    Q4 rz[kRows][2], rx[kRows][2];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, sub = group % role.per_token;
+  const long long token = (long long)role.index * (GROUPS / role.per_token) + group / role.per_token;
+  const bool valid = token < (long long)a.B * a.N;
+  const int b = valid ? (int)token / a.N : 0, n = valid ? (int)token - b * a.N : 0;
+  int off[2] = {8 * lane, 8 * lane + 4};
+  if (WHICH < 2) quad_offsets<INTER>(a, lane, off);
+  const int H = valid ? (WHICH == 0 ? a.Hq : a.Hkv) : 0;
+  const long long in_step = role.per_token * a.in[WHICH].sh, out_step = role.per_token * a.out[WHICH].sh;
+  const T* src = reinterpret_cast<const T*>(a.in[WHICH].ptr) + b * a.in[WHICH].sb + n * a.in[WHICH].sn + sub * a.in[WHICH].sh;
+  T* dst = reinterpret_cast<T*>(a.out[WHICH].ptr) + b * a.out[WHICH].sb + n * a.out[WHICH].sn + sub * a.out[WHICH].sh;
+  const int rounds = ((WHICH == 0 ? a.Hq : a.Hkv) + role.per_token * kRows - 1) / (role.per_token * kRows);
+  const bool rotates = WHICH < 2 && lane_rotates(a, lane);
+  Angles ang;
+  Pairs w;
+  for (int it = 0, h = sub; it < rounds; ++it) {
+    Q4 raw[kRows][2];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int h = sub + (it * kRows + u) * a.per_token;
-      rz[u][0] = rz[u][1] = rx[u][0] = rx[u][1] = Q4{};
-      if (valid && h < H) {
-        const T* dz = row_ptr<T>(a.in[WHICH], b, h, n);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) rz[u][j] = __ldg(reinterpret_cast<const Q4*>(dz + off[j]));
-        if (WHICH < 2 && a.norm) {
-          const T* x = row_ptr<T>(a.x[WHICH], b, h, n);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) rx[u][j] = __ldg(reinterpret_cast<const Q4*>(x + off[j]));
-        }
+      raw[u][0] = raw[u][1] = Q4{};
+      if (h + u * role.per_token < H) {
+        raw[u][0] = __ldg(reinterpret_cast<const Q4*>(src + off[0]));
+        raw[u][1] = __ldg(reinterpret_cast<const Q4*>(src + off[1]));
       }
+      src += in_step;
+    }
+    if (WHICH < 2 && it == 0) {  // behind the rows' loads, which need not wait for the position
+      if (rotates) ang = load_angles(a, valid ? token : 0, lane, lane_axes(a, lane));
+      w = load_weights<INTER>(a, WHICH == 0 ? a.wq : a.wk, off);
     }
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int h = sub + (it * kRows + u) * a.per_token;
+    for (int u = 0; u < kRows; ++u, h += role.per_token) {
       if (WHICH < 2) {
-        float g[8];
-        widen(rz[u][0], g);
-        widen(rz[u][1], g + 4);
-        rotate<-1>(g, ang);
-        if (a.norm) {
-          float x[8], ss = 0.f, hx = 0.f;
-          widen(rx[u][0], x);
-          widen(rx[u][1], x + 4);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss = fmaf(x[i], x[i], ss);
-            hx = fmaf(g[i] * w[i], x[i], hx);
-          }
-          const float r = rsqrtf(row_sum<D / 8>(ss) * (1.f / D) + a.eps);
-          // mean(h xh) xh = x r^2 mean(h x)
-          const float back = row_sum<D / 8>(hx) * (1.f / D) * r * r;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dw[i] = fmaf(g[i] * r, x[i], dw[i]);  // rows left out have g = x = 0
-            g[i] = r * (g[i] * w[i] - x[i] * back);
-          }
-        }
-        narrow(g, &rz[u][0]);
-        narrow(g + 4, &rz[u][1]);
+        Pairs v = widen<INTER>(raw[u][0], raw[u][1]);
+        if (a.norm) v = times(v, times(w, rsqrtf(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps)));
+        if (rotates) rotate<false>(v, ang);
+        narrow<INTER>(v, &raw[u][0], &raw[u][1]);
       }
-      if (valid && h < H) {
-        T* dx = row_ptr<T>(a.out[WHICH], b, h, n);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) *reinterpret_cast<Q4*>(dx + off[j]) = rz[u][j];
+      if (h < H) {
+        *reinterpret_cast<Q4*>(dst + off[0]) = raw[u][0];
+        *reinterpret_cast<Q4*>(dst + off[1]) = raw[u][1];
       }
+      dst += out_step;
     }
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
+  const Role r = cta_role(a);
+  if (r.which == 0) forward_tensor<T, D, 0, INTER>(a, r);
+  else if (r.which == 1) forward_tensor<T, D, 1, INTER>(a, r);
+  else forward_tensor<T, D, 2, INTER>(a, r);
+}
+
+// dx from x and dz, and this lane's share of dw.
+template <typename T, int D, int WHICH, bool INTER>
+__device__ __forceinline__ void backward_tensor(const RopeArgs& a, const Role& role) {
+  using Q4 = typename Quad<T>::type;
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
-  __shared__ float sums[GROUPS][D];
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const int tokens_per_cta = GROUPS / a.per_token;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, sub = group % role.per_token;
+  const int tokens_per_cta = GROUPS / role.per_token;
   const long long tokens = (long long)a.B * a.N;
-  const int sub = group % a.per_token;
-  int off[2], straight[2] = {8 * lane, 8 * lane + 4};
-  quad_offsets(a, lane, off);
-  float wq[8], wk[8], dwq[8] = {}, dwk[8] = {};
-  load_weights(a, a.wq, off, wq);
-  load_weights(a, a.wk, off, wk);
-  // a CTA takes every gridDim.x-th run of tokens, so that few partial sums of dw are left
-  for (long long first = (long long)blockIdx.x * tokens_per_cta; first < tokens;
-       first += (long long)gridDim.x * tokens_per_cta) {
-    const long long token = first + group / a.per_token;
+  int off[2] = {8 * lane, 8 * lane + 4};
+  const f32x2 zero = f2_make(0.f, 0.f);
+  Pairs w, dw = {{zero, zero}, {zero, zero}};
+  const uint32_t axes = lane_axes(a, lane);
+  const bool rotates = WHICH < 2 && lane_rotates(a, lane);
+  if (WHICH < 2) {
+    quad_offsets<INTER>(a, lane, off);
+    w = load_weights<INTER>(a, WHICH == 0 ? a.wq : a.wk, off);
+  }
+  const Heads& tx = a.x[WHICH < 2 ? WHICH : 0];
+  const long long in_step = role.per_token * a.in[WHICH].sh, out_step = role.per_token * a.out[WHICH].sh;
+  const long long x_step = role.per_token * tx.sh;
+  const int rounds = ((WHICH == 0 ? a.Hq : a.Hkv) + role.per_token * kRows - 1) / (role.per_token * kRows);
+  // a CTA takes every count-th run of tokens, so that few partial sums of dw are left
+  for (long long first = (long long)role.index * tokens_per_cta; first < tokens; first += (long long)role.count * tokens_per_cta) {
+    const long long token = first + group / role.per_token;
     const bool valid = token < tokens;
-    const int b = valid ? (int)(token / a.N) : 0, n = valid ? (int)(token - (long long)b * a.N) : 0;
-    const Angles ang = load_angles(a, token, lane, valid);
-    backward_heads<T, D, 0>(a, b, n, sub, valid, ang, off, wq, dwq);
-    backward_heads<T, D, 1>(a, b, n, sub, valid, ang, off, wk, dwk);
-    if (a.in[2].ptr) backward_heads<T, D, 2>(a, b, n, sub, valid, ang, straight, wk, dwk);
-  }
-  if (!a.norm) return;
-  for (int t = 0; t < 2; ++t) {
-    __syncthreads();
+    const int b = valid ? (int)token / a.N : 0, n = valid ? (int)token - b * a.N : 0;
+    const int H = valid ? (WHICH == 0 ? a.Hq : a.Hkv) : 0;
+    const T* dz = reinterpret_cast<const T*>(a.in[WHICH].ptr) + b * a.in[WHICH].sb + n * a.in[WHICH].sn + sub * a.in[WHICH].sh;
+    const T* x = reinterpret_cast<const T*>(tx.ptr) + b * tx.sb + n * tx.sn + sub * tx.sh;
+    T* dx = reinterpret_cast<T*>(a.out[WHICH].ptr) + b * a.out[WHICH].sb + n * a.out[WHICH].sn + sub * a.out[WHICH].sh;
+    Angles ang;
+    for (int it = 0, h = sub; it < rounds; ++it) {
+      Q4 rz[kRows][2], rx[kRows][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[group][off[i >> 2] + (i & 3)] = t ? dwk[i] : dwq[i];
+      for (int u = 0; u < kRows; ++u) {
+        rz[u][0] = rz[u][1] = rx[u][0] = rx[u][1] = Q4{};
+        if (h + u * role.per_token < H) {
+          rz[u][0] = __ldg(reinterpret_cast<const Q4*>(dz + off[0]));
+          rz[u][1] = __ldg(reinterpret_cast<const Q4*>(dz + off[1]));
+          if (WHICH < 2 && a.norm) {
+            rx[u][0] = __ldg(reinterpret_cast<const Q4*>(x + off[0]));
+            rx[u][1] = __ldg(reinterpret_cast<const Q4*>(x + off[1]));
+          }
+        }
+        dz += in_step;
+        x += x_step;
+      }
+      // (a token that is not there counts as zeros: its angles only have to be finite)
+      if (it == 0 && rotates) ang = load_angles(a, valid ? token : 0, lane, axes);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u, h += role.per_token) {
+        if (WHICH < 2) {
+          Pairs g = widen<INTER>(rz[u][0], rz[u][1]);
+          if (rotates) rotate<true>(g, ang);
+          if (a.norm) {
+            const Pairs v = widen<INTER>(rx[u][0], rx[u][1]), hw = times(g, w);
+            const float r = rsqrtf(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps);
+            // mean(h xh) xh = x r^2 mean(h x)
+            const float back = row_sum<LANES>(dot(hw, v)) * (1.f / D) * r * r;
+            dw = fma(times(g, r), v, dw);  // rows left out have g = x = 0
+            g = times(fma(-back, v, hw), r);
+          }
+          narrow<INTER>(g, &rz[u][0], &rz[u][1]);
+        }
+        if (h < H) {
+          *reinterpret_cast<Q4*>(dx + off[0]) = rz[u][0];
+          *reinterpret_cast<Q4*>(dx + off[1]) = rz[u][1];
+        }
+        dx += out_step;
+      }
+    }
+  }
+  if constexpr (WHICH < 2) {
+    if (!a.norm) return;
+    __shared__ float sums[GROUPS][D];
+    float4 lo, hi;
+    narrow<INTER>(dw, &lo, &hi);
+    *reinterpret_cast<float4*>(&sums[group][off[0]]) = lo;
+    *reinterpret_cast<float4*>(&sums[group][off[1]]) = hi;
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kThreads) {
       float s = 0.f;
       for (int g = 0; g < GROUPS; ++g) s += sums[g][c];
-      a.part[((size_t)blockIdx.x * 2 + t) * D + c] = s;
+      a.part[(size_t)blockIdx.x * D + c] = s;
     }
   }
 }
 
-// dw[t][c] = sum of the CTAs' partial sums, in a fixed order.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+  const Role r = cta_role(a);
+  if (r.which == 0) backward_tensor<T, D, 0, INTER>(a, r);
+  else if (r.which == 1) backward_tensor<T, D, 1, INTER>(a, r);
+  else backward_tensor<T, D, 2, INTER>(a, r);
+}
+
+// dw[c] = sum of the CTAs' partial sums, in a fixed order: blockIdx.y 0 for q, 1 for k.
 __global__ void __launch_bounds__(256)
-rope_dw_kernel(const float* __restrict__ part, int n, int d, float* __restrict__ dwq, float* __restrict__ dwk) {
+rope_dw_kernel(const float* __restrict__ part, int n_q, int n_k, int d, float* __restrict__ dwq, float* __restrict__ dwk) {
   __shared__ float s_sum[8][33];
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), row0 = threadIdx.x >> 5;
+  const int begin = blockIdx.y ? n_q : 0, end = blockIdx.y ? n_q + n_k : n_q;
   float s = 0.f;
-  for (int r = row0; r < n; r += 8) s += part[(size_t)r * 2 * d + col];
+  for (int r = begin + row0; r < end; r += 8) s += part[(size_t)r * d + col];
   s_sum[row0][threadIdx.x & 31] = s;
   __syncthreads();
   if (row0 == 0) {
     float v = 0.f;
     for (int r = 0; r < 8; ++r) v += s_sum[r][threadIdx.x];
-    (col < d ? dwq[col] : dwk[col - d]) = v;
+    (blockIdx.y ? dwk : dwq)[col] = v;
   }
 }
 
@@ -341,8 +399,8 @@ gbs_status resolve_rope(const gbs_rope_params* in, RopeArgs* a) {
   for (int i = 0; i < p.rot / 2; ++i)
     if (p.axis[i] >= p.n_axes)
       return fail_status(GBS_ERR_INVALID_ARG, "axis[%d] = %d is not below n_axes = %d", i, (int)p.axis[i], p.n_axes);
-  if ((long long)p.B * p.N > INT32_MAX || (long long)p.B * p.N * ((long long)p.Hq + p.Hkv) > ((long long)1 << 40))
-    return fail_status(GBS_ERR_INVALID_ARG, "problem too large: B * N must be below 2^31");
+  if ((long long)p.B * p.N > INT32_MAX / 4 || p.Hq > 65536 || p.Hkv > 65536)
+    return fail_status(GBS_ERR_INVALID_ARG, "problem too large: B * N must be below 2^29 and heads at most 65536");
   *a = RopeArgs{};
   a->B = p.B; a->N = p.N; a->Hq = p.Hq; a->Hkv = p.Hkv;
   a->half = p.rot / 2; a->interleaved = p.interleaved; a->n_axes = p.n_axes;
@@ -357,47 +415,49 @@ gbs_status check_side(const RopeArgs& a, const void* wq, const void* wk, const f
   if (((uintptr_t)wq | (uintptr_t)wk) & 3u) return fail_status(GBS_ERR_INVALID_ARG, "a weight is not 4-byte aligned");
   if (a.half && (!cos_tab || !sin_tab || !pos))
     return fail_status(GBS_ERR_INVALID_ARG, "cos_tab, sin_tab or pos is NULL");
-  if (((uintptr_t)cos_tab | (uintptr_t)sin_tab | (uintptr_t)pos) & 3u)
-    return fail_status(GBS_ERR_INVALID_ARG, "cos_tab, sin_tab or pos is not 4-byte aligned");
+  if (((uintptr_t)cos_tab | (uintptr_t)sin_tab) & 15u)
+    return fail_status(GBS_ERR_INVALID_ARG, "cos_tab or sin_tab is not 16-byte aligned");
+  if ((uintptr_t)pos & 3u) return fail_status(GBS_ERR_INVALID_ARG, "pos is not 4-byte aligned");
   return GBS_OK;
 }
 
-// Lane groups that share a token's heads: as many as a CTA has while there are
-// too few tokens to fill the GPU, and one when there are many.
-int groups_per_token(const RopeArgs& a, int groups, int want_ctas) {
-  const long long tokens = (long long)a.B * a.N;
+constexpr int kSms = 148;
+constexpr int kMaxBwdCtas = 3 * kSms;  // one wave: 78 us for 8192 tokens against 84 with 8 x 148
+
+// Lane groups that share a token's heads (a power of two): one while there are tokens
+// enough to fill the GPU, so that a group walks along a token's heads and the groups of
+// a CTA meet in adjacent rows of every head.
+int groups_per_token(long long tokens, int heads, int groups) {
   int g = 1;
-  while (g < groups && tokens * g / groups < want_ctas) g *= 2;
+  while (g < groups && g < heads && tokens * g / groups < kSms) g *= 2;
   return g;
-}
-
-constexpr int kMaxBwdCtas = 148 * 4;
-
-int bwd_ctas(const RopeArgs& a, int d, int per_token) {
-  const int tokens_per_cta = kThreads / (d / 8) / per_token;
-  const long long n = ((long long)a.B * a.N + tokens_per_cta - 1) / tokens_per_cta;
-  return (int)(n < kMaxBwdCtas ? n : kMaxBwdCtas);
 }
 
 template <typename T>
 cudaError_t launch_rope(RopeArgs& a, int d, bool backward, float* dwq, float* dwk, cudaStream_t st) {
   const int groups = kThreads / (d / 8);
-  a.per_token = groups_per_token(a, groups, kMaxBwdCtas);
-  const int tokens_per_cta = groups / a.per_token;
-  if (!backward) {
-    const unsigned grid = (unsigned)(((long long)a.B * a.N + tokens_per_cta - 1) / tokens_per_cta);
-    if (d == 64) rope_fwd_kernel<T, 64><<<grid, kThreads, 0, st>>>(a);
-    else rope_fwd_kernel<T, 128><<<grid, kThreads, 0, st>>>(a);
-    note_launch();
-    return cudaGetLastError();
+  const long long tokens = (long long)a.B * a.N;
+  const int heads[3] = {a.Hq, a.Hkv, a.in[2].ptr ? a.Hkv : 0};
+  for (int i = 0; i < 2; ++i) a.per_token[i] = groups_per_token(tokens, heads[i], groups);
+  for (int i = 0; i < 3; ++i) {
+    const int tokens_per_cta = groups / a.per_token[i ? 1 : 0];
+    long long n = heads[i] ? (tokens + tokens_per_cta - 1) / tokens_per_cta : 0;
+    // the backward's CTAs go round: each tensor gets its share of a fixed number
+    const long long share = (long long)kMaxBwdCtas * heads[i] / (heads[0] + heads[1] + heads[2]) + (heads[i] != 0);
+    a.ctas[i] = (int)(backward && n > share ? share : n);
   }
-  const int grid = bwd_ctas(a, d, a.per_token);
-  if (d == 64) rope_bwd_kernel<T, 64><<<grid, kThreads, 0, st>>>(a);
-  else rope_bwd_kernel<T, 128><<<grid, kThreads, 0, st>>>(a);
+  const unsigned grid = (unsigned)(a.ctas[0] + a.ctas[1] + a.ctas[2]);
+  void (*const fwd[])(RopeArgs) = {rope_fwd_kernel<T, 64, false>, rope_fwd_kernel<T, 64, true>,
+                                   rope_fwd_kernel<T, 128, false>, rope_fwd_kernel<T, 128, true>};
+  void (*const bwd[])(RopeArgs) = {rope_bwd_kernel<T, 64, false>, rope_bwd_kernel<T, 64, true>,
+                                   rope_bwd_kernel<T, 128, false>, rope_bwd_kernel<T, 128, true>};
+  const int kind = (d == 128 ? 2 : 0) + a.interleaved;
+  (backward ? bwd : fwd)[kind]<<<grid, kThreads, 0, st>>>(a);
   note_launch();
+  if (!backward) return cudaGetLastError();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.norm) return e;
-  rope_dw_kernel<<<2 * d / 32, 256, 0, st>>>(a.part, grid, d, dwq, dwk);
+  rope_dw_kernel<<<dim3(d / 32, 2), 256, 0, st>>>(a.part, a.ctas[0], a.ctas[1], d, dwq, dwk);
   note_launch();
   return cudaGetLastError();
 }
@@ -415,7 +475,7 @@ extern "C" size_t gbs_qkv_rope_workspace_bytes(const gbs_rope_params* p) {
   set_last_error("");
   RopeArgs a;
   if (resolve_rope(p, &a) != GBS_OK) return 0;
-  return 256 + (size_t)kMaxBwdCtas * 2 * p->d * sizeof(float);
+  return 256 + (size_t)(kMaxBwdCtas + 3) * p->d * sizeof(float);
 }
 
 extern "C" gbs_status gbs_qkv_rope_fwd(const gbs_rope_params* p, const gbs_heads* q, const gbs_heads* k,

@@ -321,7 +321,7 @@ GBS_API size_t gbs_qkv_rope_workspace_bytes(const gbs_rope_params* p);
 
 /*   q, k, v   inputs [B, Hq | Hkv, N, d]; v and V both NULL leave values out.
  *   wq, wk    [d] weights, both or neither (NULL: no norm).
- *   cos_tab, sin_tab  [max_pos, rot / 2] fp32 (not read with rot = 0).
+ *   cos_tab, sin_tab  [max_pos, rot / 2] fp32, 16-byte aligned (not read with rot = 0).
  *   pos       [B, N, n_axes] int32; a position outside [0, max_pos) is clamped
  *             and reported by gbs_check(ws) as GBS_ERR_INVALID_ARG.
  *   Q, K, V   outputs, the same shapes; they must not overlap the inputs.
