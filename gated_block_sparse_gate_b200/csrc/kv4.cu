@@ -18,25 +18,6 @@ namespace {
 constexpr int kBS = 64;
 constexpr float kMaxValue = 60000.f;  // below fp16's largest, so that m + 15 s cannot overflow it
 
-// Four channels of a row as one load.
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 u = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 struct RowArgs {
   int B, Hkv, T, N;
   Kv4 c;
@@ -71,6 +52,72 @@ __device__ __forceinline__ int token_count(const RowArgs& a, int b) {
   return n;
 }
 
+__device__ __forceinline__ float low_half(uint32_t w) {
+  return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
+}
+__device__ __forceinline__ float high_half(uint32_t w) {
+  return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+
+// Append and read give a row to d / 32 lanes, 16 code bytes to each: halfwords 8 p ..
+// 8 p + 7 of lane p, which hold kSpan consecutive channels of every group, from channel
+// 32 k + kSpan p of group k on. So a lane moves 16 bytes at a time on both sides, and a
+// group's extremes take one or two shuffles for all rows of a warp at once.
+template <int D>
+struct RowLanes {
+  static constexpr int NG = D / 32, kSpan = 32 / NG;
+};
+
+// kSpan channels from or to p.
+template <int N>
+__device__ __forceinline__ void load_span(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p + i));
+    v[i] = u.x; v[i + 1] = u.y; v[i + 2] = u.z; v[i + 3] = u.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_span(const __nv_bfloat16* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i + j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_span(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void store_span(__nv_bfloat16* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// min and max of three that keep a NaN
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // fp16((hi - m) / 15) as through 64 bits: the fp32 product is within 2^-22 of the
 // quotient, so it decides unless the fp16 on both sides of it differ.
 __device__ __forceinline__ __half group_scale(float hi, float m) {
@@ -80,87 +127,174 @@ __device__ __forceinline__ __half group_scale(float hi, float m) {
   return __float2half_rn((float)(((double)hi - (double)m) / 15.0));
 }
 
-// (x - m) / s rounded and limited as in 64 bits: fp32 is off by less than 2^-16
-// in 0..15, so only quotients that near to a half are computed in 64 bits.
-__device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv) {
-  const float t = (x - m) * inv;
-  float n = rintf(t);
-  if (fabsf(fabsf(t - n) - 0.5f) < 0x1p-14f) n = (float)rint(((double)x - (double)m) / (double)s);
-  return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+// Parameter word of a group with extremes lo and hi.
+__device__ __forceinline__ uint32_t group_params(float lo, float hi) {
+  if (isnan(lo)) return 0x7fff7fffu;
+  const __half m = __float2half_rn(fminf(fmaxf(lo, -kMaxValue), kMaxValue));
+  const __half s = group_scale(fminf(fmaxf(hi, -kMaxValue), kMaxValue), __half2float(m));
+  return (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(m) << 16;
 }
 
-// One row by D / 4 lanes, four channels each; a group's 8 lanes find its
-// extremes by shuffles.
+constexpr float kUnsure = 0.5f - 0x1p-17f;
+// The codes of four channels as 16 bits, from i15 = 1 / (15 s). In fp32 (x - m) / s is
+// within 2^-18 of the quotient in 0..15, so it decides unless it is within 2^-17 of a
+// half: *unsure tells that one is. Saturation to 0..1 limits the codes and makes a NaN 0.
+__device__ __forceinline__ uint32_t codes_of(const float* x, float m, float i15, bool* unsure) {
+  using namespace sm100;
+  constexpr float kRound = 12582912.f;  // 1.5 2^23: adding it rounds to whole numbers, ties to even
+  const f32x2 m2 = f2_make(m, m), fifteen = f2_make(15.f, 15.f), up = f2_make(kRound, kRound);
+  f32x2 n[2];
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // channels i and i + 2, so that both halves take the same step below
+    float d0, d1, e0, e1;
+    f2_split(f2_sub(f2_make(x[i], x[i + 2]), m2), d0, d1);
+    const f32x2 t = f2_make(__saturatef(d0 * i15), __saturatef(d1 * i15));
+    n[i] = f2_sub(f2_fma(t, fifteen, up), up);
+    f2_split(f2_sub(f2_mul(t, fifteen), n[i]), e0, e1);
+    far = fmaxf(far, fmaxf(fabsf(e0), fabsf(e1)));
+  }
+  *unsure = far > kUnsure;
+  float lo, hi;
+  f2_split(f2_fma(n[1], f2_make(16.f, 16.f), n[0]), lo, hi);
+  return (uint32_t)fmaf(hi, 256.f, lo);
+}
+// Row of a lane: sequence, head and token; token -1 behind the last.
+struct RowPlace {
+  int b, h, t;
+};
+template <int D>
+__device__ __forceinline__ RowPlace row_place(const RowArgs& a) {
+  const unsigned row = (blockIdx.x * 256u + threadIdx.x) / (unsigned)RowLanes<D>::NG;
+  if (row >= (unsigned)a.B * a.Hkv * a.T) return {0, 0, -1};
+  const unsigned bh = row / (unsigned)a.T;
+  return {(int)(bh / (unsigned)a.Hkv), (int)(bh % (unsigned)a.Hkv), (int)(row - bh * (unsigned)a.T)};
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int LANES = D / 4, NG = D / 32;
-  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
-  const int lane = threadIdx.x % LANES, grp = lane / 8, chunk = lane % 8;
-  const long long rows = (long long)a.B * a.Hkv * a.T;
+  using R = RowLanes<D>;
+  constexpr int NG = R::NG, kSpan = R::kSpan;
+  const int p = threadIdx.x % NG;
+  const RowPlace r = row_place<D>(a);
   const Heads& src = blockIdx.y ? a.t[1] : a.t[0];
   long long at = -1;
-  float x[4] = {};
-  if (row < rows) {
-    const int t = (int)(row % a.T), bh = (int)(row / a.T), b = bh / a.Hkv, h = bh % a.Hkv;
-    if (t < token_count(a, b)) at = cache_row(a, b, h, t);
-    if (at >= 0)
-      load4(reinterpret_cast<const T*>(src.ptr) + b * src.sb + h * src.sh + t * src.sn + 4 * lane, x);
-  }
-  float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-  float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-  int bad = isnan(x[0]) || isnan(x[1]) || isnan(x[2]) || isnan(x[3]);
+  if (r.t >= 0 && r.t < token_count(a, r.b)) at = cache_row(a, r.b, r.h, r.t);
+  float x[NG][kSpan];
+  if (at >= 0) {
+    const T* row = reinterpret_cast<const T*>(src.ptr) + r.b * src.sb + r.h * src.sh + r.t * src.sn;
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    for (int k = 0; k < NG; ++k) load_span<kSpan>(row + 32 * k + kSpan * p, x[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+#pragma unroll
+      for (int i = 0; i < kSpan; ++i) x[k][i] = 0.f;
+  }
+  float lo[NG], hi[NG];
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    lo[k] = hi[k] = x[k][0];
+#pragma unroll
+    for (int i = 1; i < kSpan; i += 2) {
+      lo[k] = min_nan(lo[k], x[k][i], x[k][i + 1 < kSpan ? i + 1 : i]);
+      hi[k] = max_nan(hi[k], x[k][i], x[k][i + 1 < kSpan ? i + 1 : i]);
+    }
+#pragma unroll
+    for (int o = NG / 2; o > 0; o >>= 1) {
+      const float l = __shfl_xor_sync(0xffffffffu, lo[k], o), h = __shfl_xor_sync(0xffffffffu, hi[k], o);
+      lo[k] = min_nan(lo[k], l, l);
+      hi[k] = max_nan(hi[k], h, h);
+    }
+  }
+  // a lane makes the parameters of group p and gets the others' from its row's lanes
+  float my_lo = lo[0], my_hi = hi[0];
+#pragma unroll
+  for (int k = 1; k < NG; ++k) {
+    my_lo = k == p ? lo[k] : my_lo;
+    my_hi = k == p ? hi[k] : my_hi;
+  }
+  const uint32_t mine = group_params(my_lo, my_hi);
+  const float my_scale = low_half(mine), my_i15 = my_scale > 0.f ? __frcp_rn(my_scale * 15.f) : 0.f;
+  uint32_t half[NG][kSpan / 4], params[NG], unsure = 0u;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    params[k] = __shfl_sync(0xffffffffu, mine, k, NG);
+    const float m = high_half(params[k]), i15 = __shfl_sync(0xffffffffu, my_i15, k, NG);
+#pragma unroll
+    for (int i = 0; i < kSpan / 4; ++i) {
+      bool u;
+      half[k][i] = codes_of(x[k] + 4 * i, m, i15, &u);
+      unsure |= u ? 1u << (i * NG + k) : 0u;
+    }
   }
   if (at < 0) return;
-  lo = fminf(fmaxf(lo, -kMaxValue), kMaxValue);
-  hi = fminf(fmaxf(hi, -kMaxValue), kMaxValue);
-  const __half m = __float2half_rn(lo);
-  const float mf = __half2float(m);
-  const __half s = group_scale(hi, mf);
-  const float sf = __half2float(s);
-  uint32_t word = 0, param = 0x7fff7fffu;
-  if (!bad) {
-    param = (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(m) << 16;
-    const float inv = 1.f / sf;
-    if (sf > 0.f)
+  // halfword j of the lane's eight: group j % NG, four channels j / NG
+  uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) word |= code_of(x[i], mf, sf, inv) << (4 * i);
+  for (int j = 0; j < 4; ++j)
+    w[j] = half[2 * j % NG][2 * j / NG] | half[(2 * j + 1) % NG][(2 * j + 1) / NG] << 16;
+  // Halfwords with a quotient next to a half, which 64 bits decide: one value in 65,000,
+  // but one in about 8,000 where bf16 values meet a border exactly. Channels are loaded
+  // again, so that x stays in registers above.
+  while (unsure) {
+    const int j = __ffs(unsure) - 1, k = j % NG;
+    unsure &= unsure - 1;
+    uint32_t param = params[0], bits = 0u;
+#pragma unroll
+    for (int q = 1; q < NG; ++q) param = q == k ? params[q] : param;
+    const float m = high_half(param), s = low_half(param), i15 = __frcp_rn(s * 15.f);
+    const T* at4 = reinterpret_cast<const T*>(src.ptr) + r.b * src.sb + r.h * src.sh + r.t * src.sn + 32 * k + kSpan * p + j / NG * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = to_f32<T>(at4[i]), t = __saturatef((v - m) * i15) * 15.f;
+      float n = rintf(t);
+      if (fabsf(t - n) > kUnsure - 0x1p-19f) {  // on which side of the half that t is next to?
+        const float below = floorf(t);
+        const double over = ((double)v - (double)m) - ((double)below + 0.5) * (double)s;
+        n = over > 0. || (over == 0. && ((int)below & 1)) ? below + 1.f : below;
+      }
+      bits |= (uint32_t)n << (4 * i);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q == j / 2) w[q] = j & 1 ? (w[q] & 0xffffu) | bits << 16 : (w[q] & 0xffff0000u) | bits;
   }
-  uint16_t* codes = reinterpret_cast<uint16_t*>(blockIdx.y ? a.c.vc : a.c.kc);
-  uint32_t* params = blockIdx.y ? a.c.vp : a.c.kp;
-  codes[at * (D / 4) + chunk * NG + grp] = (uint16_t)word;
-  if (chunk == 0) params[at * NG + grp] = param;
-}
-
-__device__ __forceinline__ float low_half(uint32_t w) {
-  return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
-}
-__device__ __forceinline__ float high_half(uint32_t w) {
-  return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+  reinterpret_cast<uint4*>((blockIdx.y ? a.c.vc : a.c.kc) + at * (D / 2))[p] = make_uint4(w[0], w[1], w[2], w[3]);
+  (blockIdx.y ? a.c.vp : a.c.kp)[at * NG + p] = mine;
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int LANES = D / 4, NG = D / 32;
-  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
-  const int lane = threadIdx.x % LANES, grp = lane / 8, chunk = lane % 8;
-  if (row >= (long long)a.B * a.Hkv * a.T) return;
+  using R = RowLanes<D>;
+  constexpr int NG = R::NG, kSpan = R::kSpan;
+  const int p = threadIdx.x % NG;
+  const RowPlace r = row_place<D>(a);
+  if (r.t < 0) return;
   const Heads& dst = blockIdx.y ? a.t[1] : a.t[0];
-  const int t = (int)(row % a.T), bh = (int)(row / a.T), b = bh / a.Hkv, h = bh % a.Hkv;
-  const long long at = t < token_count(a, b) ? cache_row(a, b, h, t) : -1;
-  float x[4] = {};
+  const long long at = r.t < token_count(a, r.b) ? cache_row(a, r.b, r.h, r.t) : -1;
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t param[NG] = {};
   if (at >= 0) {
-    const uint32_t word = reinterpret_cast<const uint16_t*>(blockIdx.y ? a.c.vc : a.c.kc)[at * (D / 4) + chunk * NG + grp];
-    const uint32_t param = (blockIdx.y ? a.c.vp : a.c.kp)[at * NG + grp];
-    const float s = low_half(param), m = high_half(param);
+    u = __ldg(reinterpret_cast<const uint4*>((blockIdx.y ? a.c.vc : a.c.kc) + at * (D / 2)) + p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = fmaf(s, (float)(word >> (4 * i) & 15u), m);
+    for (int k = 0; k < NG; ++k) param[k] = __ldg((blockIdx.y ? a.c.vp : a.c.kp) + at * NG + k);
   }
-  store4(reinterpret_cast<T*>(dst.ptr) + b * dst.sb + h * dst.sh + t * dst.sn + 4 * lane, x);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  T* row = reinterpret_cast<T*>(dst.ptr) + r.b * dst.sb + r.h * dst.sh + r.t * dst.sn;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    const float s = low_half(param[k]), m = high_half(param[k]);
+    float v[kSpan];
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+      const int j = i / 4 * NG + k;  // the halfword of the lane's eight
+      // the nibble as 2^23 + n, an exact fp32
+      const uint32_t n = (w[j / 2] >> (16 * (j & 1) + 4 * (i & 3)) & 15u) | 0x4b000000u;
+      v[i] = fmaf(s, __uint_as_float(n) - 8388608.f, m);
+    }
+    store_span<kSpan>(row + 32 * k + kSpan * p, v);
+  }
 }
 
 // ------------------------------------------------------------------ decode
@@ -931,7 +1065,7 @@ gbs_status rows_call(const char* where, const gbs_params* in, const gbs_kv4_cach
   a.B = p.B; a.Hkv = p.Hkv; a.T = T; a.N = p.N;
   a.start = start; a.count = count;
   a.c.err = static_cast<unsigned int*>(ws);
-  const int rows_per_cta = 256 / (p.d / 4);
+  const int rows_per_cta = 256 / (p.d / 32);
   const dim3 grid((unsigned)((rows + rows_per_cta - 1) / rows_per_cta), 2);
   cudaStream_t st = (cudaStream_t)stream;
 #define GBS_ROWS(T_, D_)                                       \
