@@ -442,24 +442,28 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------ tensor-core decode
-// bf16 queries. A CTA serves up to eight query heads of one selection row (one
-// head without a shared selection) over its share of the kept blocks. Each of its
-// four warps works alone until the end, on every fourth half block: 32 keys, whose
-// codes and parameters (5,120 bytes for d = 128) arrive by bulk copies into the warp's
-// own ring of stages, issued by its first lane when a stage has been read.
+// bf16 queries. A CTA serves up to four query heads of one selection row (one head
+// without a shared selection) over its share of the kept blocks. Each of its four warps
+// works alone until the end, on every fourth half block: 32 keys, whose codes and
+// parameters (5,120 bytes for d = 128) arrive by bulk copies into the warp's own ring of
+// stages, issued by its first lanes when a stage has been read.
 //
 //   z[key, head] = sum_g s_g sum_{i in g} n_i q_i + sum_g m_g sum_{i in g} q_i
-// The inner sums are m16n8k16 products of codes (rows: keys) and q (columns: heads) as
-// fp16, both exact: q is scaled by a power of two for each head so that it fits, scales
-// are applied to the fp32 sums, and the minima's part is one more product, of the raw
-// parameter words with the sums of q as two fp16 terms.
+// The inner sums are m16n8k16 products of codes (rows: keys) and q as fp16, both exact: q
+// is scaled by a power of two for each head so that it fits, scales are applied to the
+// fp32 sums, and the minima's part is one more product, of the raw parameter words with
+// the sums of q as two fp16 terms.
 //   O[channel, head] = sum_key n (s p) + sum_key m p
 // with codes as rows again, p and s p rounded to fp16 (2^-11 each, against the 2^-8 of
 // the bf16 result) and sums in fp32; where a scale is too small or large for that, values
 // m + s n are made first and rounded instead.
-// With channels and keys as the product's 16 rows, no part of it is padding but unused
-// heads. Its key and channel order is free, so lanes take whole words of codes: two words
-// of four channels, joined by a byte permute, become operand registers by masks alone.
+//
+// A nibble masked out of a 32-bit word of codes stands for an fp16 pair as it is (kLow,
+// kHigh below), one from a group 2 P (low half) and one from group 2 P + 1. Both go
+// through a product together: its eight columns are four heads times the two groups of a
+// pair, column c with zeros where the other group's factor would be. So codes need
+// nothing but masks and one shift, the accumulators have no padding but unused heads, and
+// the two groups' logits meet in one exchange between lanes.
 constexpr int kUnit = 32;  // keys of a warp's turn
 template <int D>
 struct Kv4Tile {
@@ -468,7 +472,7 @@ struct Kv4Tile {
   static constexpr int kStage = kVp + kUnit * PB;
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kWarp = kStages * kStage, kBytes = 4 * kWarp;
-  static_assert(kWarp >= 8 * D * 4, "a warp's sums are joined in its stages' memory");
+  static_assert(kWarp >= 4 * D * 4, "a warp's sums are joined in its stages' memory");
 };
 constexpr int kMmaThreads = 128;
 constexpr uint64_t kWaitNs = 4000000000ull;
@@ -537,15 +541,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
   using Tile = Kv4Tile<D>;
-  constexpr int NG = Tile::NG, S = Tile::kStages;
+  constexpr int NG = Tile::NG, NP = NG / 2, S = Tile::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full_all[4][S];
-  __shared__ float bias_all[4][S], s_m[4][8], s_l[4][8];
+  __shared__ float bias_all[4][S], s_m[4][4], s_l[4][4];
   __shared__ int rows_all[4][S], s_abort;
-  __shared__ uint4 s_q[NG][32];
-  __shared__ float s_qsum[8][NG];
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* full = full_all[warp];
@@ -556,12 +558,12 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   // the CTA's selection row and heads
   int b, kvh, h0, nh, srow;
   if (a.grouped) {
-    const int n_sub = (p.G + 7) / 8, sub = blockIdx.x % n_sub;
+    const int n_sub = (p.G + 3) / 4, sub = blockIdx.x % n_sub;
     srow = blockIdx.x / n_sub;
     b = srow / p.Hkv;
     kvh = srow % p.Hkv;
-    h0 = kvh * p.G + sub * 8;
-    nh = min(8, p.G - sub * 8);
+    h0 = kvh * p.G + sub * 4;
+    nh = min(4, p.G - sub * 4);
   } else {
     srow = blockIdx.x;
     b = srow / p.Hq;
@@ -622,61 +624,68 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   look_up(lane);
   for (int s = 0; s < S && s < turns; ++s) issue(s, s);
 
+  // column g of a product: head g & 3, group parity g >> 2; result columns 2 t and 2 t + 1:
+  // heads 2 t & 3 and the next, parity t >> 1
   const int g = lane >> 2, t = lane & 3;
-  // q of head g, channels 8 t .. 8 t + 7 of every group, as fp16 times a power of two;
-  // each group is converted by one warp
+  uint32_t qb[NP][8], qm0 = 0u, qm1 = 0u;
   float zs[2];
   {
-    const uint4* q = reinterpret_cast<const uint4*>(
-        reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + g) * D + 8 * t);
-    uint4 mine = make_uint4(0u, 0u, 0u, 0u);
-    __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
+    const int h = g & 3, par = g >> 2;
+    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + h) * D + 32 * par + 8 * t;
+    float v[NP][8], mx = 0.f;
 #pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      const uint4 u = g < nh ? __ldg(q + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
-      if (k == warp) mine = u;
+    for (int P = 0; P < NP; ++P) {
+      const uint4 u = h < nh ? __ldg(reinterpret_cast<const uint4*>(q + 64 * P)) : make_uint4(0u, 0u, 0u, 0u);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+      for (int i = 0; i < 8; ++i) {
+        v[P][i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        mx = fmaxf(mx, fabsf(v[P][i]));
+      }
     }
-    float mx = fmaxf(__low2float(most), __high2float(most));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 8;  // 2^(ex + 8) <= mx < 2^(ex + 9)
-    if (ex == 120 || ex == -135) ex = 0;                  // infinite, zero or subnormal: as it is
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    // q as fp16 times a power of two: the largest of a head in 2^8 .. 2^9
+    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 8;
+    if (ex == 120 || ex == -135) ex = 0;  // infinite, zero or subnormal: as it is
     // the codes' products are 2^-24 of what they stand for, the scales' and minima's not
     const float down = ldexpf(1.f, -ex), zscale = p.scale_log2 * ldexpf(1.f, ex) * 0x1p24f;
-    zs[0] = __shfl_sync(0xffffffffu, zscale, 8 * t);  // of the heads 2 t and 2 t + 1
-    zs[1] = __shfl_sync(0xffffffffu, zscale, 8 * t + 4);
-    if (warp < NG) {
-      const uint32_t w[4] = {mine.x, mine.y, mine.z, mine.w};
-      float v[8], sum = 0.f;
+    zs[0] = __shfl_sync(0xffffffffu, zscale, 4 * (2 * t & 3));
+    zs[1] = __shfl_sync(0xffffffffu, zscale, 4 * (2 * t & 3) + 4);
+    float qsum = 0.f;
+#pragma unroll
+    for (int P = 0; P < NP; ++P) {
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = __half2float(__float2half_rn(__uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * down));
-        sum += v[i];
+        const __half x = __float2half_rn(v[P][i] * down);
+        sum += __half2float(x);
+        // channel i of eight: nibble i % 4 of the lane's word i / 4. High nibbles count 16
+        // times; of q, that rounds only what is below 2^-15 of its largest
+        const uint32_t bits = __half_as_ushort(i & 1 ? __hmul(x, __ushort_as_half(0x2c00)) : x);  // 2^-4
+        qb[P][i] = par ? bits << 16 : bits;
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t == 0) s_qsum[g][warp] = sum;
-      // high nibbles count 16 times; of q, that rounds only what is below 2^-15 of its largest
-      s_q[warp][lane] = make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1] * 0x1p-4f, v[5] * 0x1p-4f),
-                                   pack_half2(v[2], v[6]), pack_half2(v[3] * 0x1p-4f, v[7] * 0x1p-4f));
+      // the minima's product takes parameter word t of a key as (s, m): group t's sum to m
+      const float of_t = __shfl_sync(0xffffffffu, sum, 4 * (h + 4 * (t & 1)) + t);
+      if (t >> 1 == P && par == 0) qsum = of_t;
     }
+    const float hi = __half2float(__float2half_rn(qsum));
+    qm0 = pack_half2(0.f, hi);
+    qm1 = pack_half2(0.f, qsum - hi);
   }
-  __syncthreads();
-  const float qsum = t < NG ? s_qsum[g][t] : 0.f;
-  // parameter word t is (s, m): its product takes 0 s + qsum m, qsum in two terms
-  const float qs_hi = __half2float(__float2half_rn(qsum));
-  const uint32_t qm0 = pack_half2(0.f, qs_hi), qm1 = pack_half2(0.f, qsum - qs_hi);
+  __syncthreads();  // s_abort is set
 
-  // sums of heads 2 t and 2 t + 1; a head that is not there never raises its maximum
-  // (o in units of 2^-24 and 2^-20 of low and high nibbles; om: the minima's part, groups g)
-  float o[NG * 2][4], om[4] = {0.f, 0.f, 0.f, 0.f}, m[2], l[2] = {0.f, 0.f};
-  m[0] = 2 * t < nh ? -INFINITY : INFINITY;
-  m[1] = 2 * t + 1 < nh ? -INFINITY : INFINITY;
+  // sums of the result columns' heads; a head that is not there never raises its maximum
+  // (o in units of 2^-24 and 2^-20 of low and high nibbles; om: the minima's part, group g)
+  float o[NP * 2][4], om[4] = {0.f, 0.f, 0.f, 0.f}, m[2], l[2] = {0.f, 0.f};
+  const int hc = 2 * t & 3;  // head of column 2 t
+  m[0] = hc < nh ? -INFINITY : INFINITY;
+  m[1] = hc + 1 < nh ? -INFINITY : INFINITY;
 #pragma unroll
-  for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int i = 0; i < NP * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
   // the product's row n is key n ^ (n >> 1 & 1) of eight, an order in which neither
   // kind of load meets a bank twice more than it must
@@ -685,6 +694,10 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   const int at_v0 = Tile::kV + row_v0 * Tile::RB + g * (Tile::RB / 8);
   const int at_v1 = Tile::kV + row_v1 * Tile::RB + g * (Tile::RB / 8);
   const int at_vp0 = Tile::kVp + row_v0 * Tile::PB, at_vp1 = Tile::kVp + row_v1 * Tile::PB;
+  const int par_k = 4 * (t >> 1), par_v = 4 * (g >> 2);
+  // byte selectors that put the low or high half of a word into the half of column g's parity
+  const uint32_t sel0 = g >> 2 ? 0x1044u : 0x4410u, sel1 = g >> 2 ? 0x3244u : 0x4432u;
+  auto word_at = [](const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); };
 
   int s = 0;
   uint32_t parity = 0;
@@ -714,36 +727,35 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       float z[2][4];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        uint32_t kw[2][NG], kp[2][NG], km[2];
+        uint32_t kw[2][NG], km[2];
+        float sc[2][NP];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int r = 16 * y + 8 * x;
           load_words<NG>(st + at_k + r * Tile::RB, kw[x]);
-          load_words<NG>(st + at_kp + r * Tile::PB, kp[x]);
-          km[x] = t < NG ? *reinterpret_cast<const uint32_t*>(st + at_kp + r * Tile::PB + 4 * t) : 0u;
+#pragma unroll
+          for (int P = 0; P < NP; ++P) sc[x][P] = low_half(word_at(st + at_kp + r * Tile::PB + 8 * P + par_k));
+          km[x] = t < NG ? word_at(st + at_kp + r * Tile::PB + 4 * t) : 0u;
         }
         mma16816(z[y], km[0], km[1], km[0], km[1], qm0, qm1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[y][i] *= 0x1p-24f;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          uint32_t w[2], h[2];
+        for (int P = 0; P < NP; ++P) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            // the group's two words of four channels, from the lane's NG words
-            w[x] = __byte_perm(kw[x][k / 2], kw[x][NG / 2 + k / 2], k & 1 ? 0x7632 : 0x5410);
-            h[x] = w[x] >> 8;
+          for (int j = 0; j < 2; ++j) {  // four channels 2 t + j of both groups
+            const uint32_t w0 = kw[0][NP * j + P], w1 = kw[1][NP * j + P], h0 = w0 >> 8, h1 = w1 >> 8;
+            mma16816_add(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qb[P][4 * j], qb[P][4 * j + 1]);
+            mma16816_add(c, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qb[P][4 * j + 2], qb[P][4 * j + 3]);
           }
-          const uint4 qk = s_q[k][lane];
-          float c[4];
-          mma16816(c, w[0] & kLow, w[1] & kLow, w[0] & kHigh, w[1] & kHigh, qk.x, qk.y);
-          mma16816_add(c, h[0] & kLow, h[1] & kLow, h[0] & kHigh, h[1] & kHigh, qk.z, qk.w);
-          const float s0 = low_half(kp[0][k]), s1 = low_half(kp[1][k]);
-          z[y][0] = fmaf(s0, c[0], z[y][0]);
-          z[y][1] = fmaf(s0, c[1], z[y][1]);
-          z[y][2] = fmaf(s1, c[2], z[y][2]);
-          z[y][3] = fmaf(s1, c[3], z[y][3]);
+          z[y][0] = fmaf(sc[0][P], c[0], z[y][0]);
+          z[y][1] = fmaf(sc[0][P], c[1], z[y][1]);
+          z[y][2] = fmaf(sc[1][P], c[2], z[y][2]);
+          z[y][3] = fmaf(sc[1][P], c[3], z[y][3]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[y][i] += __shfl_xor_sync(0xffffffffu, z[y][i], 2);  // the other parity's
       }
       if (ends) {
         __syncwarp();
@@ -771,7 +783,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           l[c] *= f;
           om[c] *= f;
 #pragma unroll
-          for (int i = 0; i < NG * 2; ++i) {
+          for (int i = 0; i < NP * 2; ++i) {
             o[i][c] *= f;
             o[i][2 + c] *= f;
           }
@@ -802,14 +814,12 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           l[1] += p1;
           pb[v] = transpose8x8(pack_half2(p0, p1));
         }
-        uint32_t vw[2][2][NG / 2], vp[2][2][NG];
+        uint32_t vw[2][2][NP];  // of keys row_v0 and row_v1: four channels g of both groups of a pair
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int r = 16 * y + 8 * v;
-          load_words<NG / 2>(st + at_v0 + r * Tile::RB, vw[v][0]);
-          load_words<NG / 2>(st + at_v1 + r * Tile::RB, vw[v][1]);
-          load_words<NG>(st + at_vp0 + r * Tile::PB, vp[v][0]);
-          load_words<NG>(st + at_vp1 + r * Tile::PB, vp[v][1]);
+          load_words<NP>(st + at_v0 + r * Tile::RB, vw[v][0]);
+          load_words<NP>(st + at_v1 + r * Tile::RB, vw[v][1]);
         }
         if (plain) {
           uint32_t mi[2] = {0u, 0u};
@@ -817,41 +827,41 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               const int r = 16 * y + 8 * v;
-              mi[v] = __byte_perm(*reinterpret_cast<const uint32_t*>(st + at_vp0 + r * Tile::PB + 4 * g),
-                                  *reinterpret_cast<const uint32_t*>(st + at_vp1 + r * Tile::PB + 4 * g), 0x7632);
+              mi[v] = __byte_perm(word_at(st + at_vp0 + r * Tile::PB + 4 * g), word_at(st + at_vp1 + r * Tile::PB + 4 * g), 0x7632);
             }
           mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
+        }
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            uint32_t w[2], h[2], ps[2];
+        for (int v = 0; v < 2; ++v) {
+          const int r = 16 * y + 8 * v;
+          const uint32_t p0 = __byte_perm(pb[v], 0u, sel0), p1 = __byte_perm(pb[v], 0u, sel1);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              w[v] = __byte_perm(vw[v][0][k / 2], vw[v][1][k / 2], k & 1 ? 0x7632 : 0x5410);
-              h[v] = w[v] >> 8;
-              ps[v] = as_word(__hmul2(as_half2(pb[v]), as_half2(__byte_perm(vp[v][0][k], vp[v][1][k], 0x5410))));
-            }
-            mma16816_add(o[2 * k], w[0] & kLow, w[0] & kHigh, w[1] & kLow, w[1] & kHigh, ps[0], ps[1]);
-            mma16816_add(o[2 * k + 1], h[0] & kLow, h[0] & kHigh, h[1] & kLow, h[1] & kHigh, ps[0], ps[1]);
-          }
-        } else {
+          for (int P = 0; P < NP; ++P) {
+            const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
+            const uint8_t *sp0 = st + at_vp0 + r * Tile::PB + 8 * P, *sp1 = st + at_vp1 + r * Tile::PB + 8 * P;
+            if (plain) {
+              const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(word_at(sp0 + par_v)))));
+              const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(word_at(sp1 + par_v)))));
+              mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
+              mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
+            } else {
+              __half2 n[2][4];
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            __half2 n[2][4];
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t even = word_at(j ? sp1 : sp0), odd = word_at((j ? sp1 : sp0) + 4);
+                const __half2 sc = as_half2(__byte_perm(even, odd, 0x5410)), mn = as_half2(__byte_perm(even, odd, 0x7632));
+                unpack4(j ? w1 : w0, n[j]);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              unpack4(__byte_perm(vw[v][0][k / 2], vw[v][1][k / 2], k & 1 ? 0x7632 : 0x5410), n[v]);
-              const __half2 sc = as_half2(__byte_perm(vp[v][0][k], vp[v][1][k], 0x5410));
-              const __half2 mn = as_half2(__byte_perm(vp[v][0][k], vp[v][1][k], 0x7632));
+                for (int i = 0; i < 4; ++i) n[j][i] = __hfma2(n[j][i], sc, mn);
+              }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) n[v][i] = __hfma2(n[v][i], sc, mn);
-            }
+              for (int u = 0; u < 2; ++u) {
+                float c[4];
+                mma16816(c, as_word(n[0][2 * u]), as_word(n[0][2 * u + 1]), as_word(n[1][2 * u]),
+                         as_word(n[1][2 * u + 1]), p0, p1);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float c[4];
-              mma16816(c, as_word(n[0][2 * u]), as_word(n[0][2 * u + 1]), as_word(n[1][2 * u]),
-                       as_word(n[1][2 * u + 1]), pb[0], pb[1]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[2 * k + u][i] = fmaf(c[i], i < 2 ? 0x1p-24f : 0x1p-20f, o[2 * k + u][i]);
+                for (int i = 0; i < 4; ++i) o[2 * P + u][i] = fmaf(c[i], i < 2 ? 0x1p-24f : 0x1p-20f, o[2 * P + u][i]);
+              }
             }
           }
         }
@@ -869,24 +879,24 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
     l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
   }
-  float least[NG][2];
+  float least[NP][2];
 #pragma unroll
-  for (int k = 0; k < NG; ++k)
+  for (int P = 0; P < NP; ++P)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) least[k][c] = __shfl_sync(0xffffffffu, om[c], 4 * k + t);
+    for (int c = 0; c < 2; ++c) least[P][c] = __shfl_sync(0xffffffffu, om[c], 4 * (2 * P + (t >> 1)) + t);
   // the warp's stages are all read: their memory takes its sums
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    if (2 * t + c < nh) {
-      float* sum = reinterpret_cast<float*>(ring) + (2 * t + c) * D + 4 * g;
+    if (hc + c < nh) {
+      float* sum = reinterpret_cast<float*>(ring) + (hc + c) * D + 32 * (t >> 1) + 4 * g;
 #pragma unroll
-      for (int k = 0; k < NG; ++k)
-        *reinterpret_cast<float4*>(sum + 32 * k) =
-            make_float4(fmaf(o[2 * k][c], 0x1p24f, least[k][c]), fmaf(o[2 * k][2 + c], 0x1p20f, least[k][c]),
-                        fmaf(o[2 * k + 1][c], 0x1p24f, least[k][c]), fmaf(o[2 * k + 1][2 + c], 0x1p20f, least[k][c]));
-      if (g == 0) {
-        s_m[warp][2 * t + c] = m[c];
-        s_l[warp][2 * t + c] = l[c];
+      for (int P = 0; P < NP; ++P)
+        *reinterpret_cast<float4*>(sum + 64 * P) =
+            make_float4(fmaf(o[2 * P][c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
+                        fmaf(o[2 * P + 1][c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
+      if (g == 0 && t < 2) {
+        s_m[warp][hc + c] = m[c];
+        s_l[warp][hc + c] = l[c];
       }
     }
   __syncthreads();
@@ -939,9 +949,9 @@ __global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant_
   if (lane == 0) a.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
 }
 
-// CTA rows of the tensor-core decode: selection rows, times slices of eight heads.
+// CTA rows of the tensor-core decode: selection rows, times slices of four heads.
 int decode4_rows(const DecodeArgs& a) {
-  return a.grouped ? a.p.B * a.p.Hkv * ((a.p.G + 7) / 8) : a.p.B * a.p.Hq;
+  return a.grouped ? a.p.B * a.p.Hkv * ((a.p.G + 3) / 4) : a.p.B * a.p.Hq;
 }
 
 // Splits of every CTA row's n_ent blocks. A CTA costs its share and about two blocks'
