@@ -5,6 +5,7 @@
 // minimum m) and codes n in 0..15; a code stands for m + s n. Channel c has
 // nibble c % 4 of the row's 16-bit word (c % 32) / 4 * (d / 32) + c / 32.
 #include <atomic>
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -302,7 +303,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ R
 struct DecodeArgs {
   Problem p;
   Kv4 c;
-  Selection sel;
+  const float* S;  // scores, where the kernel selects for itself; else null and
+  Selection sel;   // the selection's lists
   const int32_t* seq_lens;
   const void* q;
   void* O;
@@ -472,9 +474,11 @@ struct Kv4Tile {
   static constexpr int kStage = kVp + kUnit * PB;
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kWarp = kStages * kStage, kBytes = 4 * kWarp;
-  static_assert(kWarp >= 4 * D * 4, "a warp's sums are joined in its stages' memory");
+  static_assert(kWarp >= 8 * D * 4, "a warp's sums, and the CTA's behind warp 0's, go into its stages' memory");
+  static_assert(kBytes >= 4 * 8192, "a row's keys are held in the stages' memory before copies begin");
 };
 constexpr int kMmaThreads = 128;
+constexpr int kMaxCluster = 16;  // splits of a row, which join their sums in one cluster
 constexpr uint64_t kWaitNs = 4000000000ull;
 // Weights are 2^(z - m), at most 2^kRoom, with m kLift below the largest z when it was
 // set. Products of weights with scales from 2^-9 to below 2^10 then stay inside fp16, and
@@ -521,17 +525,20 @@ __device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
   n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
 }
 
+// N words of shared memory at an address and a constant offset from it.
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-  } else if constexpr (N == 2) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x; w[1] = u.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+__device__ __forceinline__ void load_words(uint32_t at, int off, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at + off));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at + off));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at + off));
+}
+__device__ __forceinline__ uint32_t load_word(uint32_t at, int off) {
+  uint32_t w[1];
+  load_words<1>(at, off, w);
+  return w[0];
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -540,14 +547,298 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Selection of the decode (that of select.cu: the min(topk, r) largest of r scores, ties
+// to the lower index, in threshold mode those whose gate reaches tau) by the 128 threads
+// of a CTA. The k-th largest key is found by bisection between the smallest and the
+// largest, on scores first and on their ordered bits at the end, until a threshold has k
+// keys on its upper side; no histogram, in which the few exponents of real scores would
+// all meet. Rows of up to 2048 blocks first drop what cannot be among k <= 96 kept ones:
+// at least k keys reach the k-th largest of the threads' own maxima, and those that reach
+// it are few (some 60 of 2048 for k = 32), so that each warp finishes among them alone.
+struct SelectScratch {
+  unsigned u[2][4];
+  float f[4];
+  int32_t idx[GBS_MAX_TOPK];
+  float score[GBS_MAX_TOPK];
+};
+constexpr int kSelectMax = 8192, kSelectRegs = 16;  // blocks of a row; keys a thread holds
+
+__device__ __forceinline__ float key_score(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+// Smallest threshold below the k-th largest key, by a warp whose lanes hold N keys each (0:
+// none): keys above the result are kept, and the first *need_eq of those equal to it. At
+// most `rounds` of bisection: a result of less is a bound that at least k keys reach.
+template <int N>
+__device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&u)[N], int k, int rounds, int* need_eq) {
+  uint32_t hi = 0u, lo = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    hi = max(hi, u[i]);
+    if (u[i]) lo = min(lo, u[i]);
+  }
+  uint32_t T = __reduce_min_sync(0xffffffffu, lo), above = __reduce_max_sync(0xffffffffu, hi) + 1u;
+  int n_above = 0;
+  for (int it = 0; above - T > 1u && it < rounds; ++it) {
+    uint32_t mid = T + (above - T) / 2;
+    if (it < 14) {  // between the scores, where that is inside
+      const uint32_t x = ordered_key(0.5f * key_score(T) + 0.5f * key_score(above - 1u));
+      if (x > T && x < above) mid = x;
+    }
+    unsigned n = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += u[i] >= mid ? 1u : 0u;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((int)n == k) {
+      *need_eq = 0;
+      return mid - 1u;
+    }
+    if ((int)n > k) T = mid;
+    else above = mid, n_above = (int)n;
+  }
+  *need_eq = k - n_above;
+  return T;
+}
+
+constexpr int kCandidates = 256;
+
+// select_here for 256 < r <= 2048 and topk <= 96; -1 where too many keys are candidates.
+__device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
+                                           uint32_t* work, SelectScratch& sc, float* lse) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t *maxima = work, *cand_key = work + 128, *cand_idx = cand_key + kCandidates;
+  // a warp holds a contiguous part of the row, 32 at a time
+  const int part = (r + 127) / 128 * 32, c0 = warp * part + lane, c1 = min(r, warp * part + part);
+  uint32_t u[kSelectRegs], hi = 0u;
+#pragma unroll
+  for (int i = 0; i < kSelectRegs; ++i) {
+    u[i] = c0 + 32 * i < c1 ? ordered_key(__ldg(srow + c0 + 32 * i)) : 0u;
+    hi = max(hi, u[i]);
+  }
+  maxima[tid] = hi;
+  __syncthreads();
+  uint32_t most[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) most[w] = maxima[32 * w + lane];
+  const float top = key_score(__reduce_max_sync(0xffffffffu, max(max(most[0], most[1]), max(most[2], most[3]))));
+  int k = topk;
+  if (mode == GBS_THRESHOLD) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSelectRegs; ++i) s += u[i] ? expf(key_score(u[i]) - top) : 0.f;
+    s = warp_sum(s);
+    if (lane == 0) sc.f[warp] = s;
+    __syncthreads();
+    const float all = top + logf(sc.f[0] + sc.f[1] + sc.f[2] + sc.f[3]);
+    unsigned n = 0u;
+#pragma unroll
+    for (int i = 0; i < kSelectRegs; ++i) n += u[i] && key_score(u[i]) - all >= log_tau ? 1u : 0u;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sc.u[1][warp] = n;
+    __syncthreads();
+    k = min(k, (int)(sc.u[1][0] + sc.u[1][1] + sc.u[1][2] + sc.u[1][3]));
+    if (k == 0) return 0;
+  }
+  int need_eq;
+  uint32_t T = warp_threshold(most, k, 8, &need_eq);
+  if (need_eq > 0) T -= 1u;  // at least k keys are above it
+  unsigned mine = 0u;
+#pragma unroll
+  for (int i = 0; i < kSelectRegs; ++i) mine += u[i] > T ? 1u : 0u;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) sc.u[0][warp] = mine;
+  __syncthreads();
+  unsigned at = 0u, n = 0u;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < warp) at += sc.u[0][w];
+    n += sc.u[0][w];
+  }
+  if (n > kCandidates) return -1;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int i = 0; i < kSelectRegs; ++i) {
+    const uint32_t is = __ballot_sync(0xffffffffu, u[i] > T);
+    if (is == 0u) continue;
+    if (u[i] > T) {
+      const unsigned j = at + __popc(is & below);
+      cand_key[j] = u[i];
+      cand_idx[j] = c0 + 32 * i;
+    }
+    at += __popc(is);
+  }
+  __syncthreads();
+  // every warp finishes alone; the first one writes the lists
+  uint32_t v[kCandidates / 32];
+#pragma unroll
+  for (int i = 0; i < kCandidates / 32; ++i) v[i] = lane + 32 * i < (int)n ? cand_key[lane + 32 * i] : 0u;
+  T = warp_threshold(v, k, 1 << 20, &need_eq);
+  float sum = 0.f;
+  int out = 0, left = need_eq;
+#pragma unroll
+  for (int i = 0; i < kCandidates / 32; ++i) {
+    if (32 * i >= (int)n) break;
+    const uint32_t is_eq = __ballot_sync(0xffffffffu, v[i] == T);
+    const bool keep = v[i] > T || (v[i] == T && __popc(is_eq & below) < left);
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    const float score = key_score(v[i]);
+    if (keep) {
+      sum += expf(score - top);
+      if (warp == 0) {
+        const int j = out + __popc(kept & below);
+        sc.idx[j] = cand_idx[lane + 32 * i];
+        sc.score[j] = score;
+      }
+    }
+    out += __popc(kept);
+    left -= min(left, __popc(is_eq));
+  }
+  *lse = top + logf(warp_sum(sum));
+  __syncthreads();
+  return k;
+}
+
+// Returns how many are kept; sc.idx gets them in ascending order and sc.score their
+// scores, *lse the logarithm of the sum of their exponentials. keys: r words of shared memory.
+__device__ __forceinline__ int select_here(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
+                                           uint32_t* keys, SelectScratch& sc, float* lse) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int k = min(topk, r);
+  *lse = 0.f;
+  if (k == 0) return 0;
+  if (r > kCandidates && r <= 128 * kSelectRegs && k <= 96) {
+    const int n = select_fast(srow, r, topk, mode, log_tau, keys, sc, lse);
+    if (n >= 0) return n;
+    __syncthreads();
+  }
+  uint32_t u[kSelectRegs], hi = 0u, lo = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < kSelectRegs; ++i) {
+    const int c = tid + 128 * i;
+    u[i] = 0u;  // below every score's key
+    if (c < r) {
+      u[i] = ordered_key(__ldg(srow + c));
+      lo = min(lo, u[i]);
+    }
+    hi = max(hi, u[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kSelectRegs; ++i)
+    if (tid + 128 * i < r) keys[tid + 128 * i] = u[i];
+  for (int c = tid + 128 * kSelectRegs; c < r; c += 128) {
+    const uint32_t x = ordered_key(__ldg(srow + c));
+    keys[c] = x;
+    lo = min(lo, x);
+    hi = max(hi, x);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) sc.u[0][warp] = lo, sc.u[1][warp] = hi;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    lo = min(lo, sc.u[0][w]);
+    hi = max(hi, sc.u[1][w]);
+  }
+  const float top = key_score(hi);
+  __syncthreads();
+  // the number of keys that `counts` is true of, and with it a float of each
+  int round = 0;
+  auto count = [&](auto counts) {
+    unsigned n = 0u;
+#pragma unroll
+    for (int i = 0; i < kSelectRegs; ++i) n += counts(u[i]) ? 1u : 0u;
+    for (int c = tid + 128 * kSelectRegs; c < r; c += 128) n += counts(keys[c]) ? 1u : 0u;
+    n = __reduce_add_sync(0xffffffffu, n);
+    unsigned* slot = sc.u[round++ & 1];
+    if (lane == 0) slot[warp] = n;
+    __syncthreads();
+    return (int)(slot[0] + slot[1] + slot[2] + slot[3]);
+  };
+  if (mode == GBS_THRESHOLD) {
+    float s = 0.f;
+    for (int c = tid; c < r; c += 128) s += expf(key_score(keys[c]) - top);
+    s = warp_sum(s);
+    if (lane == 0) sc.f[warp] = s;
+    __syncthreads();
+    const float all = top + logf(sc.f[0] + sc.f[1] + sc.f[2] + sc.f[3]);
+    k = min(k, count([&](uint32_t x) { return x != 0u && key_score(x) - all >= log_tau; }));
+    if (k == 0) return 0;
+  }
+  // keys above T are kept, and the first need_eq of those equal to it
+  uint32_t T = lo - 1u;
+  int need_eq = 0;
+  if (k < r) {
+    uint32_t above = hi + 1u;  // fewer than k keys reach it, at least k reach lo
+    int n_above = 0;
+    T = lo;
+    need_eq = -1;
+    for (int it = 0; above - T > 1u; ++it) {
+      uint32_t mid = T + (above - T) / 2;
+      if (it < 14) {  // between the scores, where that is inside
+        const uint32_t x = ordered_key(0.5f * key_score(T) + 0.5f * key_score(above - 1u));
+        if (x > T && x < above) mid = x;
+      }
+      const int n = count([&](uint32_t x) { return x >= mid; });
+      if (n == k) {
+        T = mid - 1u;
+        need_eq = 0;
+        break;
+      }
+      if (n > k) T = mid;
+      else above = mid, n_above = n;
+    }
+    if (need_eq < 0) need_eq = k - n_above;
+  }
+  // each warp compacts a contiguous part of the row
+  const int part = ((r + 31) / 32 + 3) / 4 * 32, c0 = warp * part, c1 = min(r, c0 + part);
+  int gt = 0, eq = 0;
+  for (int c = c0 + lane; c - lane < c1; c += 32) {
+    const uint32_t x = c < c1 ? keys[c] : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, c < c1 && x > T));
+    eq += __popc(__ballot_sync(0xffffffffu, c < c1 && x == T));
+  }
+  __syncthreads();  // the last count's slots are read
+  if (lane == 0) sc.u[0][warp] = (unsigned)gt, sc.u[1][warp] = (unsigned)eq;
+  __syncthreads();
+  int at = 0, left = need_eq;
+  for (int w = 0; w < warp; ++w) {
+    const int e = min(left, (int)sc.u[1][w]);
+    at += (int)sc.u[0][w] + e;
+    left -= e;
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int c = c0 + lane; c - lane < c1; c += 32) {
+    const uint32_t x = c < c1 ? keys[c] : 0u;
+    const uint32_t is_eq = __ballot_sync(0xffffffffu, c < c1 && x == T);
+    const bool keep = c < c1 && (x > T || (x == T && __popc(is_eq & below) < left));
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) {
+      const int j = at + __popc(kept & below);
+      sc.idx[j] = c;
+      sc.score[j] = key_score(x);
+    }
+    at += __popc(kept);
+    left -= min(left, __popc(is_eq));
+  }
+  __syncthreads();
+  float s = 0.f;
+  for (int j = lane; j < k; j += 32) s += expf(sc.score[j] - top);
+  *lse = top + logf(warp_sum(s));
+  return k;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
   using Tile = Kv4Tile<D>;
   constexpr int NG = Tile::NG, NP = NG / 2, S = Tile::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full_all[4][S];
   __shared__ float bias_all[4][S], s_m[4][4], s_l[4][4];
   __shared__ int rows_all[4][S], s_abort;
+  __shared__ SelectScratch select;
+  __shared__ float2 s_join[4];
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* full = full_all[warp];
@@ -573,14 +864,28 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
   }
   const int split = blockIdx.y;
   const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
-  const int n_hist = L > 0 ? dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err) : 0;
+  int n_hist = 0;
+  const int32_t* kept = select.idx;
+  const float* gates = select.score;
+  float lse = 0.f;
+  if (a.S) {
+    if (threadIdx.x == 0) s_abort = 0;
+    n_hist = select_here(a.S + (size_t)srow * p.Nb, cur, p.topk, p.mode, p.log_tau, reinterpret_cast<uint32_t*>(smem),
+                         select, &lse);
+    sm100::fence_proxy_async_smem();  // copies will write over the keys
+    __syncthreads();
+  } else {
+    if (threadIdx.x == 0) s_abort = 0;
+    if (L > 0) n_hist = dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err);
+    kept = a.sel.idx + (size_t)srow * p.topk;
+    gates = a.sel.logg + (size_t)srow * p.topk;
+  }
   const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
   const int e0 = split * per, e1 = min(n_ent, e0 + per);
   // this warp's blocks are first, first + 2, ...; it takes their keys half .. half + 31
   const int first = e0 + (warp >> 1), half = (warp & 1) * kUnit;
   const int turns = first < e1 ? (e1 - first + 1) / 2 : 0;
 
-  if (threadIdx.x == 0) s_abort = 0;
   if (lane == 0) {
     for (int s = 0; s < S; ++s) sm100::mbar_init(&full[s], 1);
     sm100::fence_barrier_init();
@@ -599,8 +904,8 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
     my_rows = 0;
     if (turn < turns) {
       const bool is_cur = e == n_hist;
-      const int c = is_cur ? cur : dcheck(a.sel.idx[(size_t)srow * p.topk + e], 0, cur - 1, a.c.err);
-      my_bias = is_cur ? 0.f : a.sel.logg[(size_t)srow * p.topk + e] * GBS_LOG2E;
+      const int c = is_cur ? cur : dcheck(kept[e], 0, cur - 1, a.c.err);
+      my_bias = is_cur ? 0.f : (gates[e] - lse) * GBS_LOG2E;
       const long long row = block_row(a, b, kvh, c);
       my_unit = (int)(row / kUnit) + (warp & 1);
       my_rows = row < 0 ? 0 : min(kUnit, is_cur ? L - cur * kBS - half : kUnit);
@@ -690,15 +995,14 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
   // the product's row n is key n ^ (n >> 1 & 1) of eight, an order in which neither
   // kind of load meets a bank twice more than it must
   const int row_k = g ^ (g >> 1 & 1), row_v0 = 2 * t ^ (t & 1), row_v1 = (2 * t + 1) ^ (t & 1);
-  const int at_k = row_k * Tile::RB + t * (Tile::RB / 4), at_kp = Tile::kKp + row_k * Tile::PB;
-  const int at_v0 = Tile::kV + row_v0 * Tile::RB + g * (Tile::RB / 8);
-  const int at_v1 = Tile::kV + row_v1 * Tile::RB + g * (Tile::RB / 8);
-  const int at_vp0 = Tile::kVp + row_v0 * Tile::PB, at_vp1 = Tile::kVp + row_v1 * Tile::PB;
-  const int par_k = 4 * (t >> 1), par_v = 4 * (g >> 2);
+  const uint32_t ring_at = sm100::smem_u32(ring);
+  const uint32_t at_k = row_k * Tile::RB + t * (Tile::RB / 4), at_kp = Tile::kKp + row_k * Tile::PB;
+  const uint32_t at_v0 = Tile::kV + row_v0 * Tile::RB + g * (Tile::RB / 8);
+  const uint32_t at_v1 = Tile::kV + row_v1 * Tile::RB + g * (Tile::RB / 8);
+  const uint32_t at_vp0 = Tile::kVp + row_v0 * Tile::PB, at_vp1 = Tile::kVp + row_v1 * Tile::PB;
+  const uint32_t par_k = 4 * (t >> 1), par_v = 4 * (g >> 2);
   // byte selectors that put the low or high half of a word into the half of column g's parity
   const uint32_t sel0 = g >> 2 ? 0x1044u : 0x4410u, sel1 = g >> 2 ? 0x3244u : 0x4432u;
-  auto word_at = [](const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); };
-
   int s = 0;
   uint32_t parity = 0;
   for (int turn = 0; turn < turns; ++turn) {
@@ -709,7 +1013,8 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
       __syncwarp();
       break;
     }
-    uint8_t* st = ring + s * Tile::kStage;
+    const uint32_t st = ring_at + s * Tile::kStage;
+    const uint32_t lk = st + at_k, lkp = st + at_kp, lv0 = st + at_v0, lv1 = st + at_v1, lvp0 = st + at_vp0, lvp1 = st + at_vp1;
     const int rows = s_rows[s];
     if (rows > 0) {
       const bool ends = rows < kUnit;  // the sequence ends in these keys
@@ -718,8 +1023,8 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
         if (lane >= rows)
 #pragma unroll
           for (int k = 0; k < NG; ++k) {  // whatever lies behind the sequence stands for zeros
-            reinterpret_cast<uint32_t*>(st + Tile::kKp + lane * Tile::PB)[k] = 0u;
-            reinterpret_cast<uint32_t*>(st + Tile::kVp + lane * Tile::PB)[k] = 0u;
+            uint32_t* params = reinterpret_cast<uint32_t*>(ring + s * Tile::kStage + Tile::kKp + lane * Tile::PB);
+            params[k] = params[Tile::kV / 4 + k] = 0u;
           }
         __syncwarp();
       }
@@ -732,10 +1037,10 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int r = 16 * y + 8 * x;
-          load_words<NG>(st + at_k + r * Tile::RB, kw[x]);
+          load_words<NG>(lk, r * Tile::RB, kw[x]);
 #pragma unroll
-          for (int P = 0; P < NP; ++P) sc[x][P] = low_half(word_at(st + at_kp + r * Tile::PB + 8 * P + par_k));
-          km[x] = t < NG ? word_at(st + at_kp + r * Tile::PB + 4 * t) : 0u;
+          for (int P = 0; P < NP; ++P) sc[x][P] = low_half(load_word(lkp + par_k, r * Tile::PB + 8 * P));
+          km[x] = t < NG ? load_word(lkp + 4 * t, r * Tile::PB) : 0u;
         }
         mma16816(z[y], km[0], km[1], km[0], km[1], qm0, qm1);
 #pragma unroll
@@ -795,7 +1100,7 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
       bool plain;
       {
         uint32_t sc[NG];
-        load_words<NG>(st + Tile::kVp + lane * Tile::PB, sc);
+        load_words<NG>(st + lane * Tile::PB, Tile::kVp, sc);
         __half2 lo = as_half2(sc[0]), hi = as_half2(sc[0]);
 #pragma unroll
         for (int k = 1; k < NG; ++k) {
@@ -818,8 +1123,8 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int r = 16 * y + 8 * v;
-          load_words<NP>(st + at_v0 + r * Tile::RB, vw[v][0]);
-          load_words<NP>(st + at_v1 + r * Tile::RB, vw[v][1]);
+          load_words<NP>(lv0, r * Tile::RB, vw[v][0]);
+          load_words<NP>(lv1, r * Tile::RB, vw[v][1]);
         }
         if (plain) {
           uint32_t mi[2] = {0u, 0u};
@@ -827,7 +1132,7 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               const int r = 16 * y + 8 * v;
-              mi[v] = __byte_perm(word_at(st + at_vp0 + r * Tile::PB + 4 * g), word_at(st + at_vp1 + r * Tile::PB + 4 * g), 0x7632);
+              mi[v] = __byte_perm(load_word(lvp0 + 4 * g, r * Tile::PB), load_word(lvp1 + 4 * g, r * Tile::PB), 0x7632);
             }
           mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
         }
@@ -838,17 +1143,17 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
 #pragma unroll
           for (int P = 0; P < NP; ++P) {
             const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
-            const uint8_t *sp0 = st + at_vp0 + r * Tile::PB + 8 * P, *sp1 = st + at_vp1 + r * Tile::PB + 8 * P;
+            const int at = r * Tile::PB + 8 * P;
             if (plain) {
-              const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(word_at(sp0 + par_v)))));
-              const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(word_at(sp1 + par_v)))));
+              const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
+              const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
               mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
               mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
             } else {
               __half2 n[2][4];
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t even = word_at(j ? sp1 : sp0), odd = word_at((j ? sp1 : sp0) + 4);
+                const uint32_t even = load_word(j ? lvp1 : lvp0, at), odd = load_word(j ? lvp1 : lvp0, at + 4);
                 const __half2 sc = as_half2(__byte_perm(even, odd, 0x5410)), mn = as_half2(__byte_perm(even, odd, 0x7632));
                 unpack4(j ? w1 : w0, n[j]);
 #pragma unroll
@@ -900,31 +1205,47 @@ __global__ void __launch_bounds__(kMmaThreads, 5) kv4_decode_mma_kernel(const __
       }
     }
   __syncthreads();
-  if (s_abort) return;  // reported in the error word; nothing is written
+  // the warps' sums as one; the splits of a row are a cluster and meet in shared memory
+  float* joined = reinterpret_cast<float*>(smem) + 4 * D;
   for (int i = threadIdx.x; i < nh * D; i += kMmaThreads) {
-    const int h = i / D, c = i % D;
-    float M = -INFINITY, l = 0.f, v = 0.f;
+    const int h = i / D;
+    float M = -INFINITY, sum = 0.f, v = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][h]);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const float f = s_m[w][h] == -INFINITY ? 1.f : fast_exp2(s_m[w][h] - M);
-      l += s_l[w][h] * f;
-      v += reinterpret_cast<const float*>(smem + w * Tile::kWarp)[h * D + c] * f;
+      sum += s_l[w][h] * f;
+      v += reinterpret_cast<const float*>(smem + w * Tile::kWarp)[i] * f;
     }
-    const size_t row = (size_t)b * p.Hq + h0 + h;
-    if (a.splits == 1) {
-      reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + c] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
-      if (c == 0) a.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
-    } else {
-      const size_t part = row * a.splits + split;
-      a.part_acc[part * D + c] = v;
-      if (c == 0) {
-        a.part_ml[part * 2] = M;
-        a.part_ml[part * 2 + 1] = l;
-      }
+    if (a.splits > 1) {
+      joined[i] = v;
+      if (i % D == 0) s_join[h] = make_float2(M, sum);
+    } else if (!s_abort) {  // (a wait that ran out is reported in the error word)
+      const size_t row = (size_t)b * p.Hq + h0 + h;
+      reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + i % D] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+      if (i % D == 0) a.LSE[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * GBS_LN2;
     }
   }
+  if (a.splits == 1) return;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int i = split * kMmaThreads + threadIdx.x; i < nh * D; i += a.splits * kMmaThreads) {
+    const int h = i / D;
+    float M = -INFINITY, sum = 0.f, v = 0.f;
+    for (int r = 0; r < a.splits; ++r) M = fmaxf(M, cluster.map_shared_rank(s_join, r)[h].x);
+    for (int r = 0; r < a.splits; ++r) {
+      const float2 ml = cluster.map_shared_rank(s_join, r)[h];
+      const float f = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+      sum += ml.y * f;
+      v += cluster.map_shared_rank(joined, r)[i] * f;
+    }
+    const size_t row = (size_t)b * p.Hq + h0 + h;
+    reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + i % D] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+    if (i % D == 0) a.LSE[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * GBS_LN2;
+  }
+  cluster.sync();  // the others have read this CTA's sums
 }
 
 // Joins the splits of a row: one warp each. A row without a key (a length of 0)
@@ -954,16 +1275,17 @@ int decode4_rows(const DecodeArgs& a) {
   return a.grouped ? a.p.B * a.p.Hkv * ((a.p.G + 3) / 4) : a.p.B * a.p.Hq;
 }
 
-// Splits of every CTA row's n_ent blocks. A CTA costs its share and about two blocks'
-// worth of beginning and end; while all CTAs fit on the GPU at once the largest share
-// is what counts, beyond that their number (64 x 131072, K = 32, 2048 rows: 1 split
-// 160 us, 2 splits 166, 4 splits 184; 102 rows of 49 blocks: 1 split 30 us, 4 splits 16).
-int decode4_splits(int rows, int n_ent, int slots) {
+// Splits of every CTA row's n_ent blocks. A CTA costs its share and about twelve blocks'
+// worth of selection, beginning and end; while all CTAs fit on the GPU at once the largest
+// share is what counts, beyond that their number (64 x 131072, K = 32: 2048 rows take
+// 157 us with 1 split, 201 with 2, 512 rows 50 and 64; 102 rows of 49 blocks with d = 64
+// take 33 us with 1, 27 with 2, 21 with 4, 31 with 8).
+int decode4_splits(int rows, int n_ent, int slots, int most) {
   int best = 1;
   float least = 0.f;
-  for (int s = 1; s <= n_ent && s <= kMaxDecodeSplits; ++s) {
+  for (int s = 1; s <= n_ent && s <= most; ++s) {
     const float load = (float)rows * s / slots;
-    const float cost = (load <= 1.f ? 1.f : load + 0.5f) * ((n_ent + s - 1) / s + 2);
+    const float cost = (load <= 1.f ? 1.f : load + 0.5f) * ((n_ent + s - 1) / s + 12);
     if (s == 1 || cost < least) {
       best = s;
       least = cost;
@@ -990,15 +1312,28 @@ cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
     if (device >= 64 || !(ready.load(std::memory_order_acquire) >> device & 1)) {
       e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                Kv4Tile<D>::kBytes);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       if (device < 64) ready.fetch_or(1ull << device, std::memory_order_release);
     }
+    cudaLaunchConfig_t launch{};
+    launch.gridDim = dim3(decode4_rows(a), a.splits);
+    launch.blockDim = dim3(kMmaThreads);
+    launch.dynamicSmemBytes = Kv4Tile<D>::kBytes;
+    launch.stream = st;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = 1;
+    cluster.val.clusterDim.y = a.splits;
+    cluster.val.clusterDim.z = 1;
+    launch.attrs = &cluster;
+    launch.numAttrs = a.splits > 1 ? 1 : 0;
     timer_begin(GBS_OP_DECODE, st);
-    kv4_decode_mma_kernel<D><<<dim3(decode4_rows(a), a.splits), kMmaThreads, Kv4Tile<D>::kBytes, st>>>(a);
+    e = cudaLaunchKernelEx(&launch, kv4_decode_mma_kernel<D>, a);
     timer_end(GBS_OP_DECODE, st);
     note_launch();
-    e = cudaGetLastError();
-    if (e != cudaSuccess || a.splits == 1) return e;
+    return e;
   } else {
     timer_begin(GBS_OP_DECODE, st);
     kv4_decode_simt_kernel<T, D><<<dim3(rows, a.splits), 128, 0, st>>>(a);
@@ -1175,14 +1510,19 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = sm_count(device, &sms);
   if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/device");
-  e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode,
-                                p.log_tau, a.sel.idx, a.sel.cnt, a.sel.logg, nullptr, st, nullptr, nullptr, 0, seq);
-  if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/select");
-  const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1;
+  const bool bf16 = p.dtype == GBS_BF16;
+  if (bf16 && cur_max <= kSelectMax) {
+    a.S = S;
+  } else {
+    e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode, p.log_tau, a.sel.idx,
+                      a.sel.cnt, a.sel.logg, nullptr, st, nullptr, nullptr, 0, seq);
+    if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/select");
+  }
+  const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1, most = bf16 ? kMaxCluster : kMaxDecodeSplits;
   a.splits = num_splits;
-  if (a.splits == 0)
-    a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms);
+  if (a.splits == 0) a.splits = decode4_splits(bf16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms, most);
   if (a.splits > n_ent) a.splits = n_ent;
+  if (a.splits > most) a.splits = most;
   if (p.dtype == GBS_BF16)
     e = p.d == 64 ? launch_decode4<__nv_bfloat16, 64>(a, device, st) : launch_decode4<__nv_bfloat16, 128>(a, device, st);
   else

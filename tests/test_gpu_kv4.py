@@ -302,6 +302,52 @@ def test_decode_threshold(shared):
     _check(x, 2500, 16, shared, tau=tau)
 
 
+def _scores(kind, S):
+    """Scores of a kind, in the shape of S."""
+    n = S.shape[-1]
+    if kind == "ties":
+        return (2 * S).round() / 2
+    if kind == "equal":
+        return torch.zeros_like(S)
+    if kind == "ascending":
+        return torch.arange(n).float().expand_as(S).contiguous() / 64
+    if kind == "one high":
+        return torch.where(torch.arange(n) == n // 2, 50.0, -0.0 * S)
+    if kind == "wide":
+        return S * 10 ** (6 * S)
+    return S
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "equal", "ascending", "one high", "wide"])
+@pytest.mark.parametrize("k", [1, 32, 96, 97, 256])
+def test_decode_selects_in_rows_of_many_blocks(kind, k):
+    L = [16500, 20011, 70000][k % 3]  # 258, 313 and 1094 blocks
+    x = _decode_case(k, 1, 4, 2, 64, L, None, False, paged=False)
+    x["S"] = _scores(kind, x["S"]).clamp(-80, 80)
+    _check(x, L, k, False)
+
+
+@pytest.mark.parametrize("L", [131072, 131137, 200000, 524289, 530000])
+@pytest.mark.parametrize("kind", ["normal", "ties"])
+def test_decode_rows_at_the_borders_of_the_selections(L, kind):
+    """2048 and 2049 blocks, 8192 and more: the selections that the kernel does itself, and the one before it."""
+    x = _decode_case(L, 1, 2, 1, 64, L, None, True, paged=False)
+    x["S"] = _scores(kind, x["S"])
+    _check(x, L, 20, True)
+
+
+@pytest.mark.parametrize("tau", [1e-6, 1e-3, 0.01])
+def test_decode_threshold_in_long_rows(tau):
+    x = _decode_case(1, 2, 2, 2, 64, 40000, [40000, 17000], False)
+    S = x["S"].numpy()
+    for b, n in enumerate(x["lens"].tolist()):
+        cur = (n - 1) // 64
+        for h in range(2):
+            band = [oracle.threshold_count(S[b, h], cur, tau * math.exp(s)) for s in (1e-4, -1e-4)]
+            assert min(band[0], 40) == min(band[1], 40)
+    _check(x, 40000, 40, False, tau=tau)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_idle_slots(dtype):
     """Length 0 gives 0 and -infinity, whatever the slot's pages hold."""
