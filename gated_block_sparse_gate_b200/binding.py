@@ -141,6 +141,27 @@ _F16 = (torch.float16,)
 _WEIGHTS = (torch.float32, torch.bfloat16)
 
 
+def _fits(t, dtypes, device_index, shape):
+    """Whether a tensor plainly is on that device, of one of the dtypes, of that shape
+    (None: any) and contiguous; by csrc/marshal.cpp where that is built."""
+    return (type(t) is torch.Tensor and t.get_device() == device_index and t.dtype in dtypes
+            and (shape is None or t.shape == shape) and t.is_contiguous())
+
+
+def _heads_of(t, dtypes, device_index, shape, token_major, written):
+    """gbs_heads of a tensor as bytes, or None for anything out of the ordinary; by
+    csrc/marshal.cpp where that is built."""
+    return None
+
+
+try:
+    from gated_block_sparse_gate_b200 import _marshal
+except ImportError:  # built without the headers: the checks below do all of it
+    _marshal = None
+else:
+    _fits, _heads_of = _marshal.fits, _marshal.heads
+
+
 def _invalid(where, detail):
     return GbsError(1, where, detail)
 
@@ -158,8 +179,7 @@ def _device(where, name, t):
 def _need(where, name, t, shape, dtypes, device):
     """t is a contiguous tensor on ``device`` with one of ``dtypes`` and, unless
     ``shape`` is None, exactly that shape: the layout the C ABI reads."""
-    if (type(t) is torch.Tensor and t.get_device() == device.index and t.dtype in dtypes
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
+    if _fits(t, dtypes, device.index, shape):
         return
     if not isinstance(t, torch.Tensor):
         raise _invalid(where, f"{name} must be a torch.Tensor")
@@ -467,18 +487,20 @@ assert struct.calcsize("5P3i4x") == ctypes.sizeof(Kv4CacheDesc)
 assert struct.calcsize("8i64s3if") == ctypes.sizeof(RopeParams)
 
 
-def _heads(where, name, t, shape, dtype, device, token_major=False, out=False):
+def _heads(where, name, t, shape, dtypes, device, token_major=False, out=False):
     """A [B, H, N, d] tensor (``token_major``: [B, N, H, d]) with contiguous
     channels as gbs_heads."""
-    if not (type(t) is torch.Tensor and t.get_device() == device.index and t.dtype is dtype and t.shape == shape):
-        if not isinstance(t, torch.Tensor):
-            raise _invalid(where, f"{name} must be a torch.Tensor")
-        if t.device != device:
-            raise _invalid(where, f"{name} is on {t.device}; expected {device}")
-        if t.dtype is not dtype:
-            raise _invalid(where, f"{name} has dtype {t.dtype}; expected {dtype}")
-        if tuple(t.shape) != shape:
-            raise _invalid(where, f"{name} has shape {tuple(t.shape)}; expected {shape}")
+    h = _heads_of(t, dtypes, device.index, shape, token_major, out)
+    if h is not None:
+        return h
+    if not isinstance(t, torch.Tensor):
+        raise _invalid(where, f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise _invalid(where, f"{name} is on {t.device}; expected {device}")
+    if t.dtype not in dtypes:
+        raise _invalid(where, f"{name} has dtype {t.dtype}; expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != shape:
+        raise _invalid(where, f"{name} has shape {tuple(t.shape)}; expected {shape}")
     b, x, y, c = t.stride()
     if c != 1:
         raise _invalid(where, f"{name} must have contiguous channels")
@@ -593,7 +615,7 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
         with ctx:
             return qkv_rope(q, k, v, cos, sin, pos, wq, wk, eps, axes, interleaved, out, ws)
     p, (B, N, Hq, Hkv, d) = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
-    act = q.dtype
+    act = (q.dtype,)
     hq = _heads(where, "q", q, (B, N, Hq, d), act, dev, True)
     hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev, True)
     hv = None if v is None else _heads(where, "v", v, (B, N, Hkv, d), act, dev, True)
@@ -627,7 +649,7 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
         with ctx:
             return qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV, wq, wk, eps, axes, interleaved, grads, ws)
     p, (B, N, Hq, Hkv, d) = _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev)
-    act = q.dtype
+    act = (q.dtype,)
     hq = _heads(where, "q", q, (B, N, Hq, d), act, dev, True)
     hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev, True)
     zq = _heads(where, "dQ", dQ, (B, Hq, N, d), act, dev)
@@ -713,8 +735,7 @@ def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out,
     if K.dim() != 4:
         raise _invalid(where, "K must be [B, Hkv, T, d]")
     B, _, T, d = K.shape
-    act = K.dtype
-    _act_dtype(where, "K", K)
+    act = _act_dtype(where, "K", K)
     desc, Hkv, L = _check_kv4(where, cache, B, d, dev, block, block_table)
     hk = _heads(where, "K", K, (B, Hkv, T, d), act, dev, False, out)
     hv = _heads(where, "V", V, (B, Hkv, T, d), act, dev, False, out)
@@ -724,7 +745,7 @@ def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out,
     _check_ws(where, ws, dev)
     if T == 0:
         return
-    s = fn(_PARAMS(B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[act], 0.0, 0.0), desc, hk, hv, T, start.data_ptr(),
+    s = fn(_PARAMS(B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[K.dtype], 0.0, 0.0), desc, hk, hv, T, start.data_ptr(),
            _addr(count), _addr(ws), _current(dev))
     if s:
         _check(s, where)

@@ -12,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgbs.so")
 DEBUG_LIB = os.path.join(HERE, "libgbs_debug.so")
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,8 +43,37 @@ def _stale(lib=LIB):
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def build_marshal(force: bool = False, verbose: bool = False):
+    """The binding's argument checks on the tensors themselves (csrc/marshal.cpp), where
+    Python's and torch's headers are installed; the binding does them in Python where the
+    module is missing."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > max(
+            map(os.path.getmtime, (src, os.path.join(INCLUDE, "gbs.h")))):
+        return MARSHAL
+    import torch
+    from torch.utils import cpp_extension
+
+    include = sysconfig.get_paths()["include"]
+    dirs = [include, *cpp_extension.include_paths(), INCLUDE]
+    if not all(any(os.path.exists(os.path.join(d, h)) for d in dirs)
+               for h in ("Python.h", "torch/csrc/autograd/python_variable.h")):
+        return None
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(x for d in dirs for x in ("-isystem", d)), src, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-o", MARSHAL + ".tmp"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
+    build_marshal(force, verbose)
     if not force and not _stale(lib):
         return lib
     nvcc = os.environ.get("NVCC", "nvcc")

@@ -195,13 +195,45 @@ def test_rope_layouts(on_meta):
 def test_outputs_whose_elements_share_memory(on_meta):
     dev = torch.device("meta")
     h = lambda t, out: gb.Heads.from_buffer_copy(  # noqa: E731
-        gb._heads("t", "X", t, tuple(t.shape), BF, dev, out=out))
+        gb._heads("t", "X", t, tuple(t.shape), (BF,), dev, out=out))
     shared = meta(2, 1, 9, 64).expand(2, 4, 9, 64)
     assert h(shared, False).stride_h == 0
     assert "share memory" in rejected(h, shared, True)
     window = torch.empty(1, device="meta", dtype=BF).expand(4096).as_strided((2, 2, 9, 64), (2048, 512, 64, 1))
     assert "share memory" in rejected(h, window, True)
     assert h(meta(2, 9, 4, 64).transpose(1, 2), True).stride_n == 256
+
+
+@pytest.mark.skipif(gb._marshal is None, reason="built without the headers")
+def test_native_checks_say_what_those_in_python_say():
+    """On host tensors (device index -1), whose answers need no GPU."""
+    x = torch.zeros(2, 3, 5, 64, dtype=BF)
+    views = [x, x.transpose(1, 2), x[:, :, :, ::2], x[:, :1].expand(2, 3, 5, 64), x[:1], x.float(), x.view(-1),
+             torch.nn.Parameter(x.float()), None, 3, torch.zeros(0, 3, 5, 64, dtype=BF)]
+    python_fits = lambda t, dt, i, s: (isinstance(t, torch.Tensor) and t.get_device() == i and t.dtype in dt  # noqa: E731
+                                       and (s is None or t.shape == s) and t.is_contiguous())
+    for t in views:
+        for dt in ((BF,), (F32, BF), (F32,)):
+            for shape in (None, (2, 3, 5, 64), (2, 5, 3, 64), (1, 3, 5, 64)):
+                for index in (-1, 0, None):
+                    assert gb._marshal.fits(t, dt, index, shape) == python_fits(t, dt, index, shape)
+    h = lambda t, **kw: gb.Heads.from_buffer_copy(gb._marshal.heads(  # noqa: E731
+        t, (BF,), -1, tuple(t.shape), kw.get("token_major", False), kw.get("written", False)))
+    for t in views[:5]:
+        for token_major in (False, True):
+            if t.stride(3) != 1:
+                assert gb._marshal.heads(t, (BF,), -1, tuple(t.shape), token_major, False) is None
+                continue
+            got = h(t, token_major=token_major)
+            st = [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
+            want = (st[0], st[2], st[1]) if token_major else (st[0], st[1], st[2])
+            assert (got.ptr, got.stride_b, got.stride_h, got.stride_n) == (t.data_ptr(), *want)
+    assert gb._marshal.heads(views[1], (BF,), -1, (2, 5, 3, 64), True, True) is None  # written, and not contiguous
+    assert h(x, written=True).stride_h == 5 * 64
+    with pytest.raises(TypeError):
+        gb._marshal.heads(x, (BF,), -1)
+    with pytest.raises(TypeError):
+        gb._marshal.fits(x, BF, -1, None)
 
 
 def test_kv4_layouts(on_meta):
