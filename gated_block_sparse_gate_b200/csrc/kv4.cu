@@ -308,7 +308,7 @@ struct DecodeArgs {
   const int32_t* seq_lens;
   const void* q;
   void* O;
-  float *LSE, *part_ml, *part_acc;
+  float* LSE;
   int grouped, splits;
 };
 
@@ -336,217 +336,6 @@ __device__ __forceinline__ long long block_row(const DecodeArgs& a, int b, int k
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// One query head and split per CTA, all in fp32. A lane holds 32 channels of a
-// row (16 code bytes), so D / 32 lanes hold a row and a warp 32 / (D / 32) rows.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int NG = D / 32, LANES = NG, ROWS = 128 / LANES;
-  __shared__ float s_acc[4][D], s_m[4], s_l[4];
-  const Problem& p = a.p;
-  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, split = blockIdx.y, kvh = hq / p.G;
-  const int srow = a.grouped ? b * p.Hkv + kvh : blockIdx.x;
-  const int lane = threadIdx.x % LANES, row_in = threadIdx.x / LANES;
-  const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
-  const int n_hist = L > 0 ? dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err) : 0;
-  const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
-  const int e0 = split * per, e1 = min(n_ent, e0 + per);
-  // 16-bit word 8 lane + i / 4 holds channels 4 chunk + i % 4 of group grp
-  float q[32], acc[32] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int hw = 8 * lane + i / 4, c = 32 * (hw % NG) + 4 * (hw / NG) + i % 4;
-    q[i] = to_f32<T>(reinterpret_cast<const T*>(a.q)[((size_t)b * p.Hq + hq) * D + c]) * p.scale_log2;
-  }
-  for (int e = e0; e < e1; ++e) {
-    const bool is_cur = e == n_hist;
-    const int c = is_cur ? cur : dcheck(a.sel.idx[(size_t)srow * p.topk + e], 0, cur - 1, a.c.err);
-    const float bias = is_cur ? 0.f : a.sel.logg[(size_t)srow * p.topk + e] * GBS_LOG2E;
-    const long long row0 = block_row(a, b, kvh, c);
-    if (row0 < 0) continue;
-    const int nrows = is_cur ? L - cur * kBS : kBS;
-    for (int r = row_in; r < kBS; r += ROWS) {
-      float z = 0.f;
-      const bool there = r < nrows;
-      const long long at = row0 + (there ? r : 0);
-      const uint4 kw = __ldg(reinterpret_cast<const uint4*>(a.c.kc + at * (D / 2)) + lane);
-      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-      float ks[NG], km[NG], vs[NG], vm[NG];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t kp = __ldg(a.c.kp + at * NG + g), vp = __ldg(a.c.vp + at * NG + g);
-        ks[g] = low_half(kp); km[g] = high_half(kp);
-        vs[g] = low_half(vp); vm[g] = high_half(vp);
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int g = (i / 4) % NG;
-        z = fmaf(q[i], fmaf(ks[g], (float)(w[i / 8] >> (4 * (i % 8)) & 15u), km[g]), z);
-      }
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      if (!there) continue;
-      z += bias;
-      if (z > m) {
-        const float f = exp2f(m - z);
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] *= f;
-        m = z;
-      }
-      // a NaN or infinite score leaves m where it was and makes the row's sum NaN
-      const float pr = exp2f(z - m);
-      l += pr;
-      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(a.c.vc + at * (D / 2)) + lane);
-      const uint32_t x[4] = {vw.x, vw.y, vw.z, vw.w};
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int g = (i / 4) % NG;
-        acc[i] = fmaf(pr, fmaf(vs[g], (float)(x[i / 8] >> (4 * (i % 8)) & 15u), vm[g]), acc[i]);
-      }
-    }
-  }
-  // join the rows of a warp, then the warps
-  float M = m;
-#pragma unroll
-  for (int o = LANES; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float f = m == -INFINITY ? 0.f : exp2f(m - M);
-  l *= f;
-#pragma unroll
-  for (int o = LANES; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const int warp = threadIdx.x / 32;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float v = m == -INFINITY ? acc[i] : acc[i] * f;
-#pragma unroll
-    for (int o = LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int hw = 8 * lane + i / 4;
-    if (threadIdx.x % 32 < LANES) s_acc[warp][32 * (hw % NG) + 4 * (hw / NG) + i % 4] = v;
-  }
-  if (threadIdx.x % 32 == 0) s_m[warp] = M, s_l[warp] = l;
-  __syncthreads();
-  float MM = -INFINITY, ll = 0.f;
-  for (int w = 0; w < 4; ++w) MM = fmaxf(MM, s_m[w]);
-  float fw[4];
-  for (int w = 0; w < 4; ++w) {
-    fw[w] = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - MM);
-    ll += s_l[w] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
-  }
-  const size_t row = (size_t)b * p.Hq + hq, part = row * a.splits + split;
-  for (int c = threadIdx.x; c < D; c += 128) {
-    float v = 0.f;
-    for (int w = 0; w < 4; ++w) v += s_acc[w][c] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
-    a.part_acc[part * D + c] = v;
-  }
-  if (threadIdx.x == 0) {
-    a.part_ml[part * 2] = MM;
-    a.part_ml[part * 2 + 1] = ll;
-  }
-}
-
-// ------------------------------------------------------------ tensor-core decode
-// bf16 queries. A CTA serves up to four query heads of one selection row (one head
-// without a shared selection) over its share of the kept blocks. Each of its four warps
-// works alone until the end, on every fourth half block: 32 keys, whose codes and
-// parameters (5,120 bytes for d = 128) arrive by bulk copies into the warp's own ring of
-// stages, issued by its first lanes when a stage has been read.
-//
-//   z[key, head] = sum_g s_g sum_{i in g} n_i q_i + sum_g m_g sum_{i in g} q_i
-// The inner sums are m16n8k16 products of codes (rows: keys) and q as fp16, both exact: q
-// is scaled by a power of two for each head so that it fits, scales are applied to the
-// fp32 sums, and the minima's part is one more product, of the raw parameter words with
-// the sums of q as two fp16 terms.
-//   O[channel, head] = sum_key n (s p) + sum_key m p
-// with codes as rows again, p and s p rounded to fp16 (2^-11 each, against the 2^-8 of
-// the bf16 result) and sums in fp32; where a scale is too small or large for that, values
-// m + s n are made first and rounded instead.
-//
-// A nibble masked out of a 32-bit word of codes stands for an fp16 pair as it is (kLow,
-// kHigh below), one from a group 2 P (low half) and one from group 2 P + 1. Both go
-// through a product together: its eight columns are four heads times the two groups of a
-// pair, column c with zeros where the other group's factor would be. So codes need
-// nothing but masks and one shift, the accumulators have no padding but unused heads, and
-// the two groups' logits meet in one exchange between lanes.
-constexpr int kUnit = 32;  // keys of a warp's turn
-template <int D>
-struct Kv4Tile {
-  static constexpr int NG = D / 32, RB = D / 2, PB = NG * 4;
-  static constexpr int kKp = kUnit * RB, kV = kKp + kUnit * PB, kVp = kV + kKp;
-  static constexpr int kStage = kVp + kUnit * PB;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kWarp = kStages * kStage, kBytes = 4 * kWarp;
-  static_assert(kWarp >= 8 * D * 4, "a warp's sums, and the CTA's behind warp 0's, go into its stages' memory");
-  static_assert(kBytes >= 4 * 8192, "a row's keys are held in the stages' memory before copies begin");
-};
-constexpr int kMmaThreads = 128;
-constexpr int kMaxCluster = 16;  // splits of a row, which join their sums in one cluster
-constexpr uint64_t kWaitNs = 4000000000ull;
-// Weights are 2^(z - m), at most 2^kRoom, with m kLift below the largest z when it was
-// set. Products of weights with scales from 2^-9 to below 2^10 then stay inside fp16, and
-// what its steps of 2^-24 cut off is small against the largest of them.
-constexpr float kLift = 2.f, kRoom = 5.f;
-#define kLeastScale __ushort_as_half(0x1800)  // 2^-9
-#define kMostScale __ushort_as_half(0x6400)   // 2^10
-// A nibble alone is the fp16 of its code times 2^-24 (low in its byte) or 2^-20 (high):
-// products take it as it is, exactly, and the power of two goes into what it meets.
-constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-
-// c = a b, and c += a b
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma16816_add(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
-__device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return as_word(__floats2half2_rn(lo, hi)); }
-
-// The transpose of an 8 x 8 matrix of fp16: a lane's word is row lane / 4, columns 2 (lane % 4) and the next.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
-  return r;
-}
-
-// Nibbles i = 0..3 of both halves of w as pairs of fp16 whole numbers.
-__device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
-  const uint32_t h = w >> 8;
-  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);  // 1024, 64: steps of 1 at bits 0 and 4
-  n[0] = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), big);
-  n[1] = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), small);
-  n[2] = __hsub2(as_half2((h & 0x000f000fu) | 0x64006400u), big);
-  n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
-}
-
-// N words of shared memory at an address and a constant offset from it.
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t at, int off, uint32_t (&w)[N]) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at + off));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at + off));
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at + off));
-}
-__device__ __forceinline__ uint32_t load_word(uint32_t at, int off) {
-  uint32_t w[1];
-  load_words<1>(at, off, w);
-  return w[0];
-}
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Selection of the decode (that of select.cu: the min(topk, r) largest of r scores, ties
 // to the lower index, in threshold mode those whose gate reaches tau) by the 128 threads
 // of a CTA. The k-th largest key is found by bisection between the smallest and the
@@ -562,6 +351,8 @@ struct SelectScratch {
   float score[GBS_MAX_TOPK];
 };
 constexpr int kSelectMax = 8192, kSelectRegs = 16;  // blocks of a row; keys a thread holds
+constexpr int kSelectWork = 640;                   // least words of shared memory
+constexpr int kMaxCluster = 16;  // splits of a row, which join their sums in one cluster
 
 __device__ __forceinline__ float key_score(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
@@ -602,6 +393,7 @@ __device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&u)[N], int k
 }
 
 constexpr int kCandidates = 256;
+static_assert(128 + 2 * kCandidates <= kSelectWork, "");
 
 // select_here for 256 < r <= 2048 and topk <= 96; -1 where too many keys are candidates.
 __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
@@ -829,6 +621,265 @@ __device__ __forceinline__ int select_here(const float* __restrict__ srow, int r
   return k;
 }
 
+// Where a CTA finds its row's kept blocks: its own selection, or the lists made before.
+struct Kept {
+  int n;
+  const int32_t* idx;
+  const float* gate;  // log gates: gate[e] - lse
+  float lse;
+};
+__device__ __forceinline__ Kept kept_blocks(const DecodeArgs& a, int srow, int cur, uint32_t* keys, SelectScratch& sc) {
+  Kept r = {0, sc.idx, sc.score, 0.f};
+  if (a.S) {
+    r.n = select_here(a.S + (size_t)srow * a.p.Nb, cur, a.p.topk, a.p.mode, a.p.log_tau, keys, sc, &r.lse);
+  } else {
+    if (cur > 0) r.n = dcheck(a.sel.cnt[srow], 0, min(a.p.topk, cur), a.c.err);
+    r.idx = a.sel.idx + (size_t)srow * a.p.topk;
+    r.gate = a.sel.logg + (size_t)srow * a.p.topk;
+  }
+  return r;
+}
+
+// Joins the splits of a row, which are a cluster: each CTA's sums of n channels (joined) and
+// (maximum, sum) of each head of D channels are in its shared memory; the first of them goes to
+// output element `out`. A row without a key (a length of 0) gives 0 and -infinity.
+template <typename T, int D>
+__device__ __forceinline__ void join_splits(const DecodeArgs& a, float* joined, float2* ml, int n, int split, size_t row0) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int i = split * 128 + threadIdx.x; i < n; i += a.splits * 128) {
+    const int h = i / D;
+    float M = -INFINITY, l = 0.f, v = 0.f;
+    for (int r = 0; r < a.splits; ++r) M = fmaxf(M, cluster.map_shared_rank(ml, r)[h].x);
+    for (int r = 0; r < a.splits; ++r) {
+      const float2 x = cluster.map_shared_rank(ml, r)[h];
+      const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - M);
+      l += x.y * f;
+      v += cluster.map_shared_rank(joined, r)[i] * f;
+    }
+    store_out(reinterpret_cast<T*>(a.O) + row0 * D + i, l == 0.f ? 0.f : v / l);
+    if (i % D == 0) a.LSE[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
+  }
+  cluster.sync();  // the others have read this CTA's sums
+}
+
+// fp32 queries: one query head and split per CTA, all in fp32. A lane holds 32 channels of a
+// row (16 code bytes), so D / 32 lanes hold a row and a warp 32 / (D / 32) rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int NG = D / 32, LANES = NG, ROWS = 128 / LANES;
+  extern __shared__ uint32_t s_keys[];
+  __shared__ SelectScratch select;
+  __shared__ float s_acc[4][D], s_m[4], s_l[4];
+  __shared__ float2 s_join;
+  const Problem& p = a.p;
+  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, split = blockIdx.y, kvh = hq / p.G;
+  const int srow = a.grouped ? b * p.Hkv + kvh : blockIdx.x;
+  const int lane = threadIdx.x % LANES, row_in = threadIdx.x / LANES;
+  const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
+  const Kept kept = kept_blocks(a, srow, cur, s_keys, select);
+  const int n_hist = kept.n;
+  const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
+  const int e0 = split * per, e1 = min(n_ent, e0 + per);
+  // 16-bit word 8 lane + i / 4 holds channels 4 chunk + i % 4 of group grp
+  float q[32], acc[32] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int hw = 8 * lane + i / 4, c = 32 * (hw % NG) + 4 * (hw / NG) + i % 4;
+    q[i] = to_f32<T>(reinterpret_cast<const T*>(a.q)[((size_t)b * p.Hq + hq) * D + c]) * p.scale_log2;
+  }
+  for (int e = e0; e < e1; ++e) {
+    const bool is_cur = e == n_hist;
+    const int c = is_cur ? cur : dcheck(kept.idx[e], 0, cur - 1, a.c.err);
+    const float bias = is_cur ? 0.f : (kept.gate[e] - kept.lse) * GBS_LOG2E;
+    const long long row0 = block_row(a, b, kvh, c);
+    if (row0 < 0) continue;
+    const int nrows = is_cur ? L - cur * kBS : kBS;
+    for (int r = row_in; r < kBS; r += ROWS) {
+      float z = 0.f;
+      const bool there = r < nrows;
+      const long long at = row0 + (there ? r : 0);
+      const uint4 kw = __ldg(reinterpret_cast<const uint4*>(a.c.kc + at * (D / 2)) + lane);
+      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+      float ks[NG], km[NG], vs[NG], vm[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t kp = __ldg(a.c.kp + at * NG + g), vp = __ldg(a.c.vp + at * NG + g);
+        ks[g] = low_half(kp); km[g] = high_half(kp);
+        vs[g] = low_half(vp); vm[g] = high_half(vp);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int g = (i / 4) % NG;
+        z = fmaf(q[i], fmaf(ks[g], (float)(w[i / 8] >> (4 * (i % 8)) & 15u), km[g]), z);
+      }
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      if (!there) continue;
+      z += bias;
+      if (z > m) {
+        const float f = exp2f(m - z);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] *= f;
+        m = z;
+      }
+      // a NaN or infinite score leaves m where it was and makes the row's sum NaN
+      const float pr = exp2f(z - m);
+      l += pr;
+      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(a.c.vc + at * (D / 2)) + lane);
+      const uint32_t x[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int g = (i / 4) % NG;
+        acc[i] = fmaf(pr, fmaf(vs[g], (float)(x[i / 8] >> (4 * (i % 8)) & 15u), vm[g]), acc[i]);
+      }
+    }
+  }
+  // join the rows of a warp, then the warps
+  float M = m;
+#pragma unroll
+  for (int o = LANES; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+  l *= f;
+#pragma unroll
+  for (int o = LANES; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const int warp = threadIdx.x / 32;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float v = m == -INFINITY ? acc[i] : acc[i] * f;
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int hw = 8 * lane + i / 4;
+    if (threadIdx.x % 32 < LANES) s_acc[warp][32 * (hw % NG) + 4 * (hw / NG) + i % 4] = v;
+  }
+  if (threadIdx.x % 32 == 0) s_m[warp] = M, s_l[warp] = l;
+  __syncthreads();
+  float MM = -INFINITY, ll = 0.f;
+  for (int w = 0; w < 4; ++w) MM = fmaxf(MM, s_m[w]);
+  float fw[4];
+  for (int w = 0; w < 4; ++w) {
+    fw[w] = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - MM);
+    ll += s_l[w] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
+  }
+  const size_t row = (size_t)b * p.Hq + hq;
+  for (int c = threadIdx.x; c < D; c += 128) {
+    float v = 0.f;
+    for (int w = 0; w < 4; ++w) v += s_acc[w][c] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
+    if (a.splits > 1) s_acc[0][c] = v;  // (column c is this thread's alone)
+    else store_out(reinterpret_cast<T*>(a.O) + row * D + c, ll == 0.f ? 0.f : v / ll);
+  }
+  if (threadIdx.x == 0) {
+    s_join = make_float2(MM, ll);
+    if (a.splits == 1) a.LSE[row] = ll == 0.f ? -INFINITY : (MM + log2f(ll)) * GBS_LN2;
+  }
+  if (a.splits > 1) join_splits<T, D>(a, s_acc[0], &s_join, D, split, row);
+}
+
+// ------------------------------------------------------------ tensor-core decode
+// bf16 queries. A CTA serves up to four query heads of one selection row (one head
+// without a shared selection) over its share of the kept blocks. Each of its four warps
+// works alone until the end, on every fourth half block: 32 keys, whose codes and
+// parameters (5,120 bytes for d = 128) arrive by bulk copies into the warp's own ring of
+// stages, issued by its first lanes when a stage has been read.
+//
+//   z[key, head] = sum_g s_g sum_{i in g} n_i q_i + sum_g m_g sum_{i in g} q_i
+// The inner sums are m16n8k16 products of codes (rows: keys) and q as fp16, both exact: q
+// is scaled by a power of two for each head so that it fits, scales are applied to the
+// fp32 sums, and the minima's part is one more product, of the raw parameter words with
+// the sums of q as two fp16 terms.
+//   O[channel, head] = sum_key n (s p) + sum_key m p
+// with codes as rows again, p and s p rounded to fp16 (2^-11 each, against the 2^-8 of
+// the bf16 result) and sums in fp32; where a scale is too small or large for that, values
+// m + s n are made first and rounded instead.
+//
+// A nibble masked out of a 32-bit word of codes stands for an fp16 pair as it is (kLow,
+// kHigh below), one from a group 2 P (low half) and one from group 2 P + 1. Both go
+// through a product together: its eight columns are four heads times the two groups of a
+// pair, column c with zeros where the other group's factor would be. So codes need
+// nothing but masks and one shift, the accumulators have no padding but unused heads, and
+// the two groups' logits meet in one exchange between lanes.
+constexpr int kUnit = 32;  // keys of a warp's turn
+template <int D>
+struct Kv4Tile {
+  static constexpr int NG = D / 32, RB = D / 2, PB = NG * 4;
+  static constexpr int kKp = kUnit * RB, kV = kKp + kUnit * PB, kVp = kV + kKp;
+  static constexpr int kStage = kVp + kUnit * PB;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kWarp = kStages * kStage, kBytes = 4 * kWarp;
+  static_assert(kWarp >= 8 * D * 4, "a warp's sums, and the CTA's behind warp 0's, go into its stages' memory");
+  static_assert(kBytes >= 4 * 8192, "a row's keys are held in the stages' memory before copies begin");
+};
+constexpr int kMmaThreads = 128;
+constexpr uint64_t kWaitNs = 4000000000ull;
+// Weights are 2^(z - m), at most 2^kRoom, with m kLift below the largest z when it was
+// set. Products of weights with scales from 2^-9 to below 2^10 then stay inside fp16, and
+// what its steps of 2^-24 cut off is small against the largest of them.
+constexpr float kLift = 2.f, kRoom = 5.f;
+#define kLeastScale __ushort_as_half(0x1800)  // 2^-9
+#define kMostScale __ushort_as_half(0x6400)   // 2^10
+// A nibble alone is the fp16 of its code times 2^-24 (low in its byte) or 2^-20 (high):
+// products take it as it is, exactly, and the power of two goes into what it meets.
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+
+// c = a b, and c += a b
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma16816_add(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+__device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return as_word(__floats2half2_rn(lo, hi)); }
+
+// The transpose of an 8 x 8 matrix of fp16: a lane's word is row lane / 4, columns 2 (lane % 4) and the next.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Nibbles i = 0..3 of both halves of w as pairs of fp16 whole numbers.
+__device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
+  const uint32_t h = w >> 8;
+  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);  // 1024, 64: steps of 1 at bits 0 and 4
+  n[0] = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), big);
+  n[1] = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), small);
+  n[2] = __hsub2(as_half2((h & 0x000f000fu) | 0x64006400u), big);
+  n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
+}
+
+// N words of shared memory at an address and a constant offset from it.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t at, int off, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at + off));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at + off));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at + off));
+}
+__device__ __forceinline__ uint32_t load_word(uint32_t at, int off) {
+  uint32_t w[1];
+  load_words<1>(at, off, w);
+  return w[0];
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
   using Tile = Kv4Tile<D>;
@@ -864,21 +915,12 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   }
   const int split = blockIdx.y;
   const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
-  int n_hist = 0;
-  const int32_t* kept = select.idx;
-  const float* gates = select.score;
-  float lse = 0.f;
+  if (threadIdx.x == 0) s_abort = 0;
+  const Kept kept = kept_blocks(a, srow, cur, reinterpret_cast<uint32_t*>(smem), select);
+  const int n_hist = kept.n;
   if (a.S) {
-    if (threadIdx.x == 0) s_abort = 0;
-    n_hist = select_here(a.S + (size_t)srow * p.Nb, cur, p.topk, p.mode, p.log_tau, reinterpret_cast<uint32_t*>(smem),
-                         select, &lse);
     sm100::fence_proxy_async_smem();  // copies will write over the keys
     __syncthreads();
-  } else {
-    if (threadIdx.x == 0) s_abort = 0;
-    if (L > 0) n_hist = dcheck(a.sel.cnt[srow], 0, min(p.topk, cur), a.c.err);
-    kept = a.sel.idx + (size_t)srow * p.topk;
-    gates = a.sel.logg + (size_t)srow * p.topk;
   }
   const int n_ent = L > 0 ? n_hist + 1 : 0, per = (n_ent + a.splits - 1) / a.splits;
   const int e0 = split * per, e1 = min(n_ent, e0 + per);
@@ -904,8 +946,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     my_rows = 0;
     if (turn < turns) {
       const bool is_cur = e == n_hist;
-      const int c = is_cur ? cur : dcheck(kept[e], 0, cur - 1, a.c.err);
-      my_bias = is_cur ? 0.f : (gates[e] - lse) * GBS_LOG2E;
+      const int c = is_cur ? cur : dcheck(kept.idx[e], 0, cur - 1, a.c.err);
+      my_bias = is_cur ? 0.f : (kept.gate[e] - kept.lse) * GBS_LOG2E;
       const long long row = block_row(a, b, kvh, c);
       my_unit = (int)(row / kUnit) + (warp & 1);
       my_rows = row < 0 ? 0 : min(kUnit, is_cur ? L - cur * kBS - half : kUnit);
@@ -1227,47 +1269,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       if (i % D == 0) a.LSE[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * GBS_LN2;
     }
   }
-  if (a.splits == 1) return;
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  for (int i = split * kMmaThreads + threadIdx.x; i < nh * D; i += a.splits * kMmaThreads) {
-    const int h = i / D;
-    float M = -INFINITY, sum = 0.f, v = 0.f;
-    for (int r = 0; r < a.splits; ++r) M = fmaxf(M, cluster.map_shared_rank(s_join, r)[h].x);
-    for (int r = 0; r < a.splits; ++r) {
-      const float2 ml = cluster.map_shared_rank(s_join, r)[h];
-      const float f = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
-      sum += ml.y * f;
-      v += cluster.map_shared_rank(joined, r)[i] * f;
-    }
-    const size_t row = (size_t)b * p.Hq + h0 + h;
-    reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + i % D] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
-    if (i % D == 0) a.LSE[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * GBS_LN2;
-  }
-  cluster.sync();  // the others have read this CTA's sums
-}
-
-// Joins the splits of a row: one warp each. A row without a key (a length of 0)
-// gives 0 and -infinity.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant__ DecodeArgs a) {
-  const int row = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (row >= a.p.B * a.p.Hq) return;
-  float M = -INFINITY, l = 0.f, acc[D / 32] = {};
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[((size_t)row * a.splits + s) * 2]);
-  for (int s = 0; s < a.splits; ++s) {
-    const size_t part = (size_t)row * a.splits + s;
-    const float m = a.part_ml[part * 2], f = m == -INFINITY ? 1.f : exp2f(m - M);
-    l += a.part_ml[part * 2 + 1] * f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] += a.part_acc[part * D + lane + 32 * i] * f;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    store_out(reinterpret_cast<T*>(a.O) + (size_t)row * D + lane + 32 * i, acc[i] * inv);
-  if (lane == 0) a.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
+  if (a.splits > 1) join_splits<__nv_bfloat16, D>(a, joined, s_join, nh * D, split, (size_t)b * p.Hq + h0);
 }
 
 // CTA rows of the tensor-core decode: selection rows, times slices of four heads.
@@ -1280,10 +1282,10 @@ int decode4_rows(const DecodeArgs& a) {
 // share is what counts, beyond that their number (64 x 131072, K = 32: 2048 rows take
 // 157 us with 1 split, 201 with 2, 512 rows 50 and 64; 102 rows of 49 blocks with d = 64
 // take 33 us with 1, 27 with 2, 21 with 4, 31 with 8).
-int decode4_splits(int rows, int n_ent, int slots, int most) {
+int decode4_splits(int rows, int n_ent, int slots) {
   int best = 1;
   float least = 0.f;
-  for (int s = 1; s <= n_ent && s <= most; ++s) {
+  for (int s = 1; s <= n_ent && s <= kMaxCluster; ++s) {
     const float load = (float)rows * s / slots;
     const float cost = (load <= 1.f ? 1.f : load + 0.5f) * ((n_ent + s - 1) / s + 12);
     if (s == 1 || cost < least) {
@@ -1303,48 +1305,44 @@ cudaError_t sm_count(int device, int* sms) {
   return e;
 }
 
+// One launch: rows x splits CTAs, the splits of a row a cluster.
 template <typename T, int D>
 cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
-  const int rows = a.p.B * a.p.Hq;
-  cudaError_t e;
-  if constexpr (sizeof(T) == 2) {
-    static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use this much shared memory
-    if (device >= 64 || !(ready.load(std::memory_order_acquire) >> device & 1)) {
-      e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Kv4Tile<D>::kBytes);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kv4_decode_mma_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-      if (device < 64) ready.fetch_or(1ull << device, std::memory_order_release);
-    }
-    cudaLaunchConfig_t launch{};
-    launch.gridDim = dim3(decode4_rows(a), a.splits);
-    launch.blockDim = dim3(kMmaThreads);
-    launch.dynamicSmemBytes = Kv4Tile<D>::kBytes;
-    launch.stream = st;
-    cudaLaunchAttribute cluster;
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = 1;
-    cluster.val.clusterDim.y = a.splits;
-    cluster.val.clusterDim.z = 1;
-    launch.attrs = &cluster;
-    launch.numAttrs = a.splits > 1 ? 1 : 0;
-    timer_begin(GBS_OP_DECODE, st);
-    e = cudaLaunchKernelEx(&launch, kv4_decode_mma_kernel<D>, a);
-    timer_end(GBS_OP_DECODE, st);
-    note_launch();
-    return e;
+  constexpr bool kMma = sizeof(T) == 2;
+  void (*kernel)(DecodeArgs);
+  size_t smem;
+  if constexpr (kMma) {
+    kernel = kv4_decode_mma_kernel<D>;
+    smem = Kv4Tile<D>::kBytes;
   } else {
-    timer_begin(GBS_OP_DECODE, st);
-    kv4_decode_simt_kernel<T, D><<<dim3(rows, a.splits), 128, 0, st>>>(a);
-    timer_end(GBS_OP_DECODE, st);
-    note_launch();
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    kernel = kv4_decode_simt_kernel<T, D>;
+    smem = a.S ? 4 * (size_t)(a.p.Nb > kSelectWork ? a.p.Nb : kSelectWork) : 0;
   }
-  kv4_combine_kernel<T, D><<<(rows + 3) / 4, 128, 0, st>>>(a);
+  cudaError_t e;
+  static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use large clusters and its memory
+  if (device >= 64 || !(ready.load(std::memory_order_acquire) >> device & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && kMma) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (device < 64) ready.fetch_or(1ull << device, std::memory_order_release);
+  }
+  cudaLaunchConfig_t launch{};
+  launch.gridDim = dim3(kMma ? decode4_rows(a) : a.p.B * a.p.Hq, a.splits);
+  launch.blockDim = dim3(128);
+  launch.dynamicSmemBytes = smem;
+  launch.stream = st;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = 1;
+  cluster.val.clusterDim.y = a.splits;
+  cluster.val.clusterDim.z = 1;
+  launch.attrs = &cluster;
+  launch.numAttrs = a.splits > 1 ? 1 : 0;
+  timer_begin(GBS_OP_DECODE, st);
+  e = cudaLaunchKernelEx(&launch, kernel, a);
+  timer_end(GBS_OP_DECODE, st);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 // ------------------------------------------------------------------ arguments
@@ -1432,8 +1430,10 @@ gbs_status rows_call(const char* where, const gbs_params* in, const gbs_kv4_cach
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// The error word and, for rows too long for the decode to select from, the lists.
 size_t carve_kv4(const Problem& p, char* base, DecodeArgs* a) {
-  size_t off = 256;  // the device error word
+  size_t off = 256;
+  if ((p.N - 1) / p.bs <= kSelectMax) return off;
   const size_t rows = (size_t)p.B * p.Hq;
   auto take = [&](size_t bytes) {
     char* at = base + off;
@@ -1443,8 +1443,6 @@ size_t carve_kv4(const Problem& p, char* base, DecodeArgs* a) {
   a->sel.idx = reinterpret_cast<int32_t*>(take(rows * p.topk * 4));
   a->sel.cnt = reinterpret_cast<int32_t*>(take(rows * 4));
   a->sel.logg = reinterpret_cast<float*>(take(rows * p.topk * 4));
-  a->part_ml = reinterpret_cast<float*>(take(rows * kMaxDecodeSplits * 8));
-  a->part_acc = reinterpret_cast<float*>(take(rows * kMaxDecodeSplits * p.d * 4));
   return off;
 }
 
@@ -1510,19 +1508,18 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = sm_count(device, &sms);
   if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/device");
-  const bool bf16 = p.dtype == GBS_BF16;
-  if (bf16 && cur_max <= kSelectMax) {
+  if (cur_max <= kSelectMax) {
     a.S = S;
   } else {
     e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode, p.log_tau, a.sel.idx,
                       a.sel.cnt, a.sel.logg, nullptr, st, nullptr, nullptr, 0, seq);
     if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/select");
   }
-  const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1, most = bf16 ? kMaxCluster : kMaxDecodeSplits;
+  const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1;
   a.splits = num_splits;
-  if (a.splits == 0) a.splits = decode4_splits(bf16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms, most);
+  if (a.splits == 0) a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms);
   if (a.splits > n_ent) a.splits = n_ent;
-  if (a.splits > most) a.splits = most;
+  if (a.splits > kMaxCluster) a.splits = kMaxCluster;
   if (p.dtype == GBS_BF16)
     e = p.d == 64 ? launch_decode4<__nv_bfloat16, 64>(a, device, st) : launch_decode4<__nv_bfloat16, 128>(a, device, st);
   else

@@ -160,7 +160,7 @@ def test_decode_arguments(lib):
                dict(p=gb.make_params(2, 4, 2, 250, 64, 64, 4, "threshold", tau=0.0), n=1 << 30),
                dict(p=gb.make_params(2, 3, 2, 250, 64, 64, 4, "sparse"), n=1 << 30)):
         assert call(**kw) == 1, kw
-    assert call(ws=None) == 5 and call(ws=OK + 64) == 5 and call(n=1000) == 5
+    assert call(ws=None) == 5 and call(ws=OK + 64) == 5 and call(n=255) == 5
     assert call(p=gb.make_params(2, 4, 2, 250, 64, 32, 4, "sparse"), n=1 << 30) == 2
 
 
