@@ -395,6 +395,65 @@ __device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&u)[N], int k
 constexpr int kCandidates = 256;
 static_assert(128 + 2 * kCandidates <= kSelectWork, "");
 
+// The end of a selection: of n <= kCandidates keys, lane l of every warp holding those of
+// l, l + 32, ..., keeps the k largest. idx(j): the block of the j-th; top: the largest
+// score. The first warp writes the lists.
+template <typename Index>
+__device__ __forceinline__ void keep_largest(const uint32_t (&v)[kCandidates / 32], int n, int k, float top,
+                                             SelectScratch& sc, float* lse, Index idx) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1u;
+  int left, out = 0;
+  const uint32_t T = warp_threshold(v, k, 1 << 20, &left);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kCandidates / 32; ++i) {
+    if (32 * i >= n) break;
+    const uint32_t is_eq = __ballot_sync(0xffffffffu, v[i] == T);
+    const bool keep = v[i] > T || (v[i] == T && __popc(is_eq & below) < left);
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) {
+      const float score = key_score(v[i]);
+      sum += expf(score - top);
+      if (warp == 0) {
+        const int j = out + __popc(kept & below);
+        sc.idx[j] = idx(lane + 32 * i);
+        sc.score[j] = score;
+      }
+    }
+    out += __popc(kept);
+    left -= min(left, __popc(is_eq));
+  }
+  *lse = top + logf(warp_sum(sum));
+  __syncthreads();
+}
+
+// select_here for r <= 256: every warp alone holds the row.
+__device__ __forceinline__ int select_short(const float* __restrict__ srow, int r, int k, int mode, float log_tau,
+                                            SelectScratch& sc, float* lse) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[kCandidates / 32], hi = 0u;
+#pragma unroll
+  for (int i = 0; i < kCandidates / 32; ++i) {
+    v[i] = lane + 32 * i < r ? ordered_key(__ldg(srow + lane + 32 * i)) : 0u;
+    hi = max(hi, v[i]);
+  }
+  const float top = key_score(__reduce_max_sync(0xffffffffu, hi));
+  if (mode == GBS_THRESHOLD) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCandidates / 32; ++i) s += v[i] ? expf(key_score(v[i]) - top) : 0.f;
+    const float all = top + logf(warp_sum(s));
+    unsigned n = 0u;
+#pragma unroll
+    for (int i = 0; i < kCandidates / 32; ++i) n += v[i] && key_score(v[i]) - all >= log_tau ? 1u : 0u;
+    k = min(k, (int)__reduce_add_sync(0xffffffffu, n));
+    if (k == 0) return 0;
+  }
+  keep_largest(v, r, k, top, sc, lse, [](int j) { return j; });
+  return k;
+}
+
 // select_here for 256 < r <= 2048 and topk <= 96; -1 where too many keys are candidates.
 __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
                                            uint32_t* work, SelectScratch& sc, float* lse) {
@@ -461,33 +520,10 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
     at += __popc(is);
   }
   __syncthreads();
-  // every warp finishes alone; the first one writes the lists
   uint32_t v[kCandidates / 32];
 #pragma unroll
   for (int i = 0; i < kCandidates / 32; ++i) v[i] = lane + 32 * i < (int)n ? cand_key[lane + 32 * i] : 0u;
-  T = warp_threshold(v, k, 1 << 20, &need_eq);
-  float sum = 0.f;
-  int out = 0, left = need_eq;
-#pragma unroll
-  for (int i = 0; i < kCandidates / 32; ++i) {
-    if (32 * i >= (int)n) break;
-    const uint32_t is_eq = __ballot_sync(0xffffffffu, v[i] == T);
-    const bool keep = v[i] > T || (v[i] == T && __popc(is_eq & below) < left);
-    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
-    const float score = key_score(v[i]);
-    if (keep) {
-      sum += expf(score - top);
-      if (warp == 0) {
-        const int j = out + __popc(kept & below);
-        sc.idx[j] = cand_idx[lane + 32 * i];
-        sc.score[j] = score;
-      }
-    }
-    out += __popc(kept);
-    left -= min(left, __popc(is_eq));
-  }
-  *lse = top + logf(warp_sum(sum));
-  __syncthreads();
+  keep_largest(v, (int)n, k, top, sc, lse, [&](int j) { return (int)cand_idx[j]; });
   return k;
 }
 
@@ -499,7 +535,8 @@ __device__ __forceinline__ int select_here(const float* __restrict__ srow, int r
   int k = min(topk, r);
   *lse = 0.f;
   if (k == 0) return 0;
-  if (r > kCandidates && r <= 128 * kSelectRegs && k <= 96) {
+  if (r <= kCandidates) return select_short(srow, r, k, mode, log_tau, sc, lse);
+  if (r <= 128 * kSelectRegs && k <= 96) {
     const int n = select_fast(srow, r, topk, mode, log_tau, keys, sc, lse);
     if (n >= 0) return n;
     __syncthreads();
