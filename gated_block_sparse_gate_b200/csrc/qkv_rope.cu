@@ -25,9 +25,10 @@ using namespace sm100;  // f32x2
 
 constexpr int kThreads = 256;
 // Rows whose loads a lane group has in flight before any arithmetic. Two, with the
-// registers held to four (backward: three) CTAs an SM, measured best: forward of 65536
-// tokens (32 + 16 heads, d = 128, bf16) 297 us against 305 with four rows and three CTAs
-// and 342 with eight rows and two.
+// registers held to four (backward: three) CTAs an SM and the lines of the next two asked
+// for in L2, measured best: forward of 65536 tokens (32 + 16 heads, d = 128, bf16) 272 us
+// (5.9 TB/s) against 312 without the prefetch, 299 with one four rounds ahead, and 342
+// with eight rows in flight and two CTAs; backward of 8192 tokens 70 us against 80 without.
 constexpr int kRows = 2;
 
 struct RopeArgs {
@@ -174,6 +175,13 @@ __device__ __forceinline__ uint32_t lane_axes(const RopeArgs& a, int lane) {
   return lane_rotates(a, lane) ? *reinterpret_cast<const uint32_t*>(a.axis + 4 * lane) : 0u;
 }
 
+// Asks for the lines of a row that is loaded a little later.
+template <typename T, int D>
+__device__ __forceinline__ void prefetch_row(const T* row, int lane, bool there) {
+  constexpr int kLines = D * (int)sizeof(T) / 128;
+  if (there && lane < kLines) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + lane * (128 / (int)sizeof(T))));
+}
+
 // First channels of a lane's two quads.
 template <bool INTER>
 __device__ __forceinline__ void quad_offsets(const RopeArgs& a, int lane, int* off) {
@@ -236,6 +244,7 @@ __device__ __forceinline__ void forward_tensor(const RopeArgs& a, const Role& ro
         raw[u][0] = __ldg(reinterpret_cast<const Q4*>(src + off[0]));
         raw[u][1] = __ldg(reinterpret_cast<const Q4*>(src + off[1]));
       }
+      prefetch_row<T, D>(src + kRows * in_step, lane, h + (u + kRows) * role.per_token < H);
       src += in_step;
     }
     if (WHICH < 2 && it == 0) {  // behind the rows' loads, which need not wait for the position
@@ -311,6 +320,9 @@ __device__ __forceinline__ void backward_tensor(const RopeArgs& a, const Role& r
             rx[u][1] = __ldg(reinterpret_cast<const Q4*>(x + off[1]));
           }
         }
+        const bool next = h + (u + kRows) * role.per_token < H;
+        prefetch_row<T, D>(dz + kRows * in_step, lane, next);
+        if (WHICH < 2) prefetch_row<T, D>(x + kRows * x_step, lane, next && a.norm);
         dz += in_step;
         x += x_step;
       }
@@ -364,20 +376,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_ker
 }
 
 // dw[c] = sum of the CTAs' partial sums, in a fixed order: blockIdx.y 0 for q, 1 for k.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 rope_dw_kernel(const float* __restrict__ part, int n_q, int n_k, int d, float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ float s_sum[8][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), row0 = threadIdx.x >> 5;
+  __shared__ float s_sum[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   const int begin = blockIdx.y ? n_q : 0, end = blockIdx.y ? n_q + n_k : n_q;
   float s = 0.f;
-  for (int r = begin + row0; r < end; r += 8) s += part[(size_t)r * d + col];
-  s_sum[row0][threadIdx.x & 31] = s;
+#pragma unroll 8
+  for (int r = begin + warp; r < end; r += 32) s += part[(size_t)r * d + col];
+  s_sum[warp][lane] = s;
   __syncthreads();
-  if (row0 == 0) {
-    float v = 0.f;
-    for (int r = 0; r < 8; ++r) v += s_sum[r][threadIdx.x];
-    (blockIdx.y ? dwk : dwq)[col] = v;
-  }
+  const float v = warp_sum(s_sum[lane][warp]);  // warp w: column w of the 32
+  if (lane == 0) (blockIdx.y ? dwk : dwq)[blockIdx.x * 32 + warp] = v;
 }
 
 gbs_status resolve_rope(const gbs_rope_params* in, RopeArgs* a) {
@@ -422,7 +432,7 @@ gbs_status check_side(const RopeArgs& a, const void* wq, const void* wk, const f
 }
 
 constexpr int kSms = 148;
-constexpr int kMaxBwdCtas = 3 * kSms;  // one wave: 78 us for 8192 tokens against 84 with 8 x 148
+constexpr int kMaxBwdCtas = 512;  // of a tensor
 
 // Lane groups that share a token's heads (a power of two): one while there are tokens
 // enough to fill the GPU, so that a group walks along a token's heads and the groups of
@@ -442,9 +452,10 @@ cudaError_t launch_rope(RopeArgs& a, int d, bool backward, float* dwq, float* dw
   for (int i = 0; i < 3; ++i) {
     const int tokens_per_cta = groups / a.per_token[i ? 1 : 0];
     long long n = heads[i] ? (tokens + tokens_per_cta - 1) / tokens_per_cta : 0;
-    // the backward's CTAs go round: each tensor gets its share of a fixed number
-    const long long share = (long long)kMaxBwdCtas * heads[i] / (heads[0] + heads[1] + heads[2]) + (heads[i] != 0);
-    a.ctas[i] = (int)(backward && n > share ? share : n);
+    // the backward's CTAs take equal numbers of runs of tokens, so that at most kMaxBwdCtas
+    // partial sums of dw are left
+    const long long runs = (n + kMaxBwdCtas - 1) / kMaxBwdCtas;
+    a.ctas[i] = (int)(backward && n ? (n + runs - 1) / runs : n);
   }
   const unsigned grid = (unsigned)(a.ctas[0] + a.ctas[1] + a.ctas[2]);
   void (*const fwd[])(RopeArgs) = {rope_fwd_kernel<T, 64, false>, rope_fwd_kernel<T, 64, true>,
@@ -457,7 +468,7 @@ cudaError_t launch_rope(RopeArgs& a, int d, bool backward, float* dwq, float* dw
   if (!backward) return cudaGetLastError();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.norm) return e;
-  rope_dw_kernel<<<dim3(d / 32, 2), 256, 0, st>>>(a.part, a.ctas[0], a.ctas[1], d, dwq, dwk);
+  rope_dw_kernel<<<dim3(d / 32, 2), 1024, 0, st>>>(a.part, a.ctas[0], a.ctas[1], d, dwq, dwk);
   note_launch();
   return cudaGetLastError();
 }
@@ -475,7 +486,7 @@ extern "C" size_t gbs_qkv_rope_workspace_bytes(const gbs_rope_params* p) {
   set_last_error("");
   RopeArgs a;
   if (resolve_rope(p, &a) != GBS_OK) return 0;
-  return 256 + (size_t)(kMaxBwdCtas + 3) * p->d * sizeof(float);
+  return 256 + (size_t)2 * kMaxBwdCtas * p->d * sizeof(float);
 }
 
 extern "C" gbs_status gbs_qkv_rope_fwd(const gbs_rope_params* p, const gbs_heads* q, const gbs_heads* k,
