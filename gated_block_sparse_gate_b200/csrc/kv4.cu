@@ -166,7 +166,8 @@ struct RowPlace {
 };
 template <int D>
 __device__ __forceinline__ RowPlace row_place(const RowArgs& a) {
-  const unsigned row = (blockIdx.x * 256u + threadIdx.x) / (unsigned)RowLanes<D>::NG;
+  constexpr unsigned NG = RowLanes<D>::NG;
+  const unsigned row = blockIdx.x * (256u / NG) + threadIdx.x / NG;
   if (row >= (unsigned)a.B * a.Hkv * a.T) return {0, 0, -1};
   const unsigned bh = row / (unsigned)a.T;
   return {(int)(bh / (unsigned)a.Hkv), (int)(bh % (unsigned)a.Hkv), (int)(row - bh * (unsigned)a.T)};
@@ -1378,7 +1379,8 @@ cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
   timer_begin(GBS_OP_DECODE, st);
   e = cudaLaunchKernelEx(&launch, kernel, a);
   timer_end(GBS_OP_DECODE, st);
-  note_launch();
+  if (e != cudaSuccess) cudaGetLastError();  // not left for a later launch to find
+  else note_launch();
   return e;
 }
 

@@ -38,9 +38,13 @@ PyObject* fits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "fits(t, dtypes, device_index, shape)");
     return nullptr;
   }
-  const at::Tensor* x = plain(a[0], a[1], a[2], a[3]);
-  if (PyErr_Occurred()) return nullptr;
-  return PyBool_FromLong(x && x->is_contiguous());
+  try {
+    const at::Tensor* x = plain(a[0], a[1], a[2], a[3]);
+    if (PyErr_Occurred()) return nullptr;
+    return PyBool_FromLong(x && x->is_contiguous());
+  } catch (...) {  // a tensor without sizes or storage of its own: not plain
+    Py_RETURN_FALSE;
+  }
 }
 
 // heads(t, dtypes, device_index, shape, token_major, written): gbs_heads of a 4-D tensor
@@ -51,15 +55,19 @@ PyObject* heads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "heads(t, dtypes, device_index, shape, token_major, written)");
     return nullptr;
   }
-  const at::Tensor* x = plain(a[0], a[1], a[2], a[3]);
-  if (PyErr_Occurred()) return nullptr;
-  if (!x || (a[5] == Py_True && !x->is_contiguous())) Py_RETURN_NONE;
-  int64_t step[4];
-  for (int i = 0; i < 4; ++i) step[i] = i < 3 && x->size(i) == 1 ? 0 : x->stride(i);  // (that of one is never followed)
-  if (step[3] != 1) Py_RETURN_NONE;
-  const int h_at = a[4] == Py_True ? 2 : 1;
-  const gbs_heads h = {x->data_ptr(), step[0], step[h_at], step[3 - h_at]};
-  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&h), sizeof h);
+  try {
+    const at::Tensor* x = plain(a[0], a[1], a[2], a[3]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!x || (a[5] == Py_True && !x->is_contiguous())) Py_RETURN_NONE;
+    int64_t step[4];
+    for (int i = 0; i < 4; ++i) step[i] = i < 3 && x->size(i) == 1 ? 0 : x->stride(i);  // (that of one is never followed)
+    if (step[3] != 1) Py_RETURN_NONE;
+    const int h_at = a[4] == Py_True ? 2 : 1;
+    const gbs_heads h = {x->data_ptr(), step[0], step[h_at], step[3 - h_at]};
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&h), sizeof h);
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
 }
 
 PyMethodDef methods[] = {

@@ -422,7 +422,8 @@ gbs_status resolve_rope(const gbs_rope_params* in, RopeArgs* a) {
 gbs_status check_side(const RopeArgs& a, const void* wq, const void* wk, const float* cos_tab,
                       const float* sin_tab, const int32_t* pos) {
   if (!wq != !wk) return fail_status(GBS_ERR_INVALID_ARG, "give both weights or neither");
-  if (((uintptr_t)wq | (uintptr_t)wk) & 3u) return fail_status(GBS_ERR_INVALID_ARG, "a weight is not 4-byte aligned");
+  if (((uintptr_t)wq | (uintptr_t)wk) & (a.w_bf16 ? 1u : 3u))
+    return fail_status(GBS_ERR_INVALID_ARG, "a weight is not aligned to its elements");
   if (a.half && (!cos_tab || !sin_tab || !pos))
     return fail_status(GBS_ERR_INVALID_ARG, "cos_tab, sin_tab or pos is NULL");
   if (((uintptr_t)cos_tab | (uintptr_t)sin_tab) & 15u)

@@ -320,7 +320,7 @@ typedef struct gbs_rope_params {
 GBS_API size_t gbs_qkv_rope_workspace_bytes(const gbs_rope_params* p);
 
 /*   q, k, v   inputs [B, Hq | Hkv, N, d]; v and V both NULL leave values out.
- *   wq, wk    [d] weights, both or neither (NULL: no norm).
+ *   wq, wk    [d] weights of w_dtype, both or neither (NULL: no norm).
  *   cos_tab, sin_tab  [max_pos, rot / 2] fp32, 16-byte aligned (not read with rot = 0).
  *   pos       [B, N, n_axes] int32; a position outside [0, max_pos) is clamped
  *             and reported by gbs_check(ws) as GBS_ERR_INVALID_ARG.
@@ -409,8 +409,11 @@ GBS_API size_t gbs_kv4_workspace_bytes(const gbs_params* p);
  * the keys and values that the cache's codes stand for. q and O are p->dtype.
  *   seq_lens, group_shared  as in gbs_kv_layout, except that a length of 0 (an
  *          idle slot of a batch) is valid: its O is 0 and its LSE -infinity.
- *   S, LSE, num_splits  as in gbs_decode_ex.
- *   ws     gbs_kv4_workspace_bytes(p) bytes. */
+ *   S, LSE  as in gbs_decode_ex.
+ *   num_splits  partitions of a row's kept blocks, which join their sums in one
+ *          thread-block cluster: of more than 16, 16 are made; 0 = automatic.
+ *   ws     gbs_kv4_workspace_bytes(p) bytes (256 up to 8192 blocks a row).
+ *   Rows of bf16 queries whose |q| passes 2^100 are not supported. */
 GBS_API gbs_status gbs_kv4_decode(const gbs_params* p, const gbs_kv4_cache* cache,
                                   const int32_t* seq_lens, int group_shared, const void* q,
                                   const float* S, void* O, float* LSE, int num_splits, void* ws,

@@ -426,6 +426,29 @@ def test_pages_give_the_contiguous_bits():
         assert all(torch.equal(a, b) for a, b in zip(_run(x, L, 6, shared), _run(y, L, 6, shared)))
 
 
+def test_rows_beyond_32_bit_offsets():
+    """A pool of more than 2^32 code bytes: pages at its end are written, read and decoded like those at its
+    beginning."""
+    B, Hq, Hkv, d, L, pages = 2, 2, 1, 128, 200, 1 << 20
+    g = torch.Generator().manual_seed(3)
+    cache = [torch.empty(pages, Hkv, 64, d // 2, dtype=torch.uint8, device=DEV),
+             torch.empty(pages, Hkv, 64, d // 32, 2, dtype=torch.float16, device=DEV)]
+    cache += [torch.empty_like(t) for t in cache]
+    assert cache[0].numel() == 1 << 32
+    K, V = (torch.randn(1, Hkv, L, d, generator=g).to(BF).to(DEV).expand(B, Hkv, L, d) for _ in "kv")
+    table = torch.tensor([[0, 1, 2, 3], [pages - 1, pages - 3, pages - 4, pages - 2]], dtype=torch.int32, device=DEV)
+    start = torch.zeros(B, dtype=torch.int32, device=DEV)
+    gb.kv4_append(K, V, cache, start, block_table=table)
+    back = gb.kv4_read(cache, start, L, block_table=table, dtype=F32)
+    assert all(torch.equal(t[0], t[1]) for t in back)
+    _within(back[0][0], kv4_quantised(K[0]))
+    q = torch.randn(1, Hq, d, generator=g).expand(B, Hq, d).contiguous().to(DEV)
+    S = torch.randn(1, Hq, 4, generator=g).expand(B, Hq, 4).contiguous().to(DEV)
+    for dtype in (BF, F32):
+        O, LSE = gb.kv4_decode(q.to(dtype), cache, S, L, topk=2, block_table=table)
+        assert torch.equal(O[0], O[1]) and torch.equal(LSE[0], LSE[1]) and bool(torch.isfinite(LSE).all())
+
+
 def test_decode_on_another_stream_in_a_graph_and_twice():
     x = _decode_case(10, 2, 4, 2, 128, 900, [900, 80], True)
     want = _run(x, 900, 8, True)
@@ -448,6 +471,28 @@ def test_decode_on_another_stream_in_a_graph_and_twice():
     torch.cuda.synchronize()
     again = call()
     assert all(torch.equal(a, b) for a, b in zip(kept, again)) and not torch.equal(kept[0], want[0])
+
+
+def test_debug_build_finds_every_index_in_range():
+    """libgbs_debug.so checks what is read from lists and must give the same bits."""
+    saved, out = gb._lib, []
+    cases = [(_decode_case(30, 2, 4, 2, 64, 3000, [3000, 65], False), 3000, 8),
+             (_decode_case(31, 1, 2, 1, 64, 530000, None, True, paged=False), 530000, 20),
+             (_decode_case(32, 2, 4, 2, 128, 500, [500, 0], True, F32), 500, 3)]
+    try:
+        for debug in (False, True):
+            gb._lib = None
+            gb.load_library(build(debug=debug))
+            for x, L, k in cases:
+                B, Hq, d = x["q"].shape
+                p = gb.make_params(B, Hq, x["cache"][0].shape[1], L, d, 64, k, "sparse", x["q"].dtype)
+                ws = torch.zeros(gb.kv4_workspace_bytes(p), dtype=torch.uint8, device=DEV)
+                out.append(_run(x, L, k, x["S"].shape[1] < Hq, ws=ws))
+                gb.check(ws)
+    finally:
+        gb._lib = saved
+    for a, b in zip(out[:3], out[3:]):
+        assert all(torch.equal(t, u) for t, u in zip(a, b))
 
 
 # ------------------------------------------------------------------ together
