@@ -829,8 +829,7 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 // the sums of q as two fp16 terms.
 //   O[channel, head] = sum_key n (s p) + sum_key m p
 // with codes as rows again, p and s p rounded to fp16 (2^-11 each, against the 2^-8 of
-// the bf16 result) and sums in fp32; where a scale is too small or large for that, values
-// m + s n are made first and rounded instead.
+// the bf16 result) and sums in fp32.
 //
 // A nibble masked out of a 32-bit word of codes stands for an fp16 pair as it is (kLow,
 // kHigh below), one from a group 2 P (low half) and one from group 2 P + 1. Both go
@@ -851,12 +850,10 @@ struct Kv4Tile {
 };
 constexpr int kMmaThreads = 128;
 constexpr uint64_t kWaitNs = 4000000000ull;
-// Weights are 2^(z - m), at most 2^kRoom, with m kLift below the largest z when it was
-// set. Products of weights with scales from 2^-9 to below 2^10 then stay inside fp16, and
-// what its steps of 2^-24 cut off is small against the largest of them.
-constexpr float kLift = 2.f, kRoom = 5.f;
-#define kLeastScale __ushort_as_half(0x1800)  // 2^-9
-#define kMostScale __ushort_as_half(0x6400)   // 2^10
+// Weights are 2^(z - m), with m kLift below the largest z when it was set, and at most
+// 2^kRoom; where scales reach 2^e, e > 0, both are e less. So no product of a weight and a
+// scale leaves fp16, and its steps of 2^-24 are 2^-34 of the largest weight.
+constexpr float kLift = 10.f, kRoom = 14.f;
 // A nibble alone is the fp16 of its code times 2^-24 (low in its byte) or 2^-20 (high):
 // products take it as it is, exactly, and the power of two goes into what it meets.
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
@@ -884,16 +881,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
   return r;
-}
-
-// Nibbles i = 0..3 of both halves of w as pairs of fp16 whole numbers.
-__device__ __forceinline__ void unpack4(uint32_t w, __half2 (&n)[4]) {
-  const uint32_t h = w >> 8;
-  const __half2 big = as_half2(0x64006400u), small = as_half2(0x54005400u);  // 1024, 64: steps of 1 at bits 0 and 4
-  n[0] = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), big);
-  n[1] = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), small);
-  n[2] = __hsub2(as_half2((h & 0x000f000fu) | 0x64006400u), big);
-  n[3] = __hsub2(as_half2((h & 0x00f000f0u) | 0x54005400u), small);
 }
 
 // N words of shared memory at an address and a constant offset from it.
@@ -1148,7 +1135,17 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
         for (int i = 0; i < 8; ++i)  // scales of the heads are not negative
           if (row_k + 8 * (i >> 1) >= rows) z[i >> 2][i & 3] = -INFINITY;
       }
-      // logarithms of the weights; m is raised only where one would pass kRoom, so the
+      // what the value scales of the 32 keys (a lane looks at one's) leave of kRoom
+      float room = kRoom;
+      {
+        uint32_t sc[NG], most = 0u;
+        load_words<NG>(st + lane * Tile::PB, Tile::kVp, sc);
+#pragma unroll
+        for (int k = 0; k < NG; ++k) most = max(most, sc[k] & 0xffffu);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (most >= 0x3c00u) room -= (float)((int)(most >> 10) - 14);  // fp16 of 1 and more
+      }
+      // logarithms of the weights; m is raised only where one would pass that, so the
       // exchange between lanes that a maximum takes is seldom needed
       const float bias = s_bias[s];
       float x[2][4];
@@ -1157,13 +1154,14 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       float mx[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(x[0][c], x[0][2 + c]), fmaxf(x[1][c], x[1][2 + c]));
-      if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > kRoom)) {
+      if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > room)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           mx[c] = fmaxf(fmaxf(z[0][c], z[0][2 + c]), fmaxf(z[1][c], z[1][2 + c]));
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], w));
-          const float mn = fmaxf(m[c], fmaf(mx[c], zs[c], bias) - kLift), f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
+          const float mn = fmaxf(m[c], fmaf(mx[c], zs[c], bias) + (kRoom - kLift - room));
+          const float f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
           m[c] = mn;
           l[c] *= f;
           om[c] *= f;
@@ -1175,19 +1173,6 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = fmaf(z[i >> 2][i & 3], zs[i & 1], bias - m[i & 1]);
-      }
-      // a lane looks at one row's value scales: do they all suit fp16 products with weights?
-      bool plain;
-      {
-        uint32_t sc[NG];
-        load_words<NG>(st + lane * Tile::PB, Tile::kVp, sc);
-        __half2 lo = as_half2(sc[0]), hi = as_half2(sc[0]);
-#pragma unroll
-        for (int k = 1; k < NG; ++k) {
-          lo = __hmin2_nan(lo, as_half2(sc[k]));
-          hi = __hmax2_nan(hi, as_half2(sc[k]));
-        }
-        plain = __all_sync(0xffffffffu, __low2half(lo) >= kLeastScale && __low2half(hi) < kMostScale);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -1206,16 +1191,14 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           load_words<NP>(lv0, r * Tile::RB, vw[v][0]);
           load_words<NP>(lv1, r * Tile::RB, vw[v][1]);
         }
-        if (plain) {
-          uint32_t mi[2] = {0u, 0u};
-          if (g < NG)
+        uint32_t mi[2] = {0u, 0u};
+        if (g < NG)
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const int r = 16 * y + 8 * v;
-              mi[v] = __byte_perm(load_word(lvp0 + 4 * g, r * Tile::PB), load_word(lvp1 + 4 * g, r * Tile::PB), 0x7632);
-            }
-          mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
-        }
+          for (int v = 0; v < 2; ++v) {
+            const int r = 16 * y + 8 * v;
+            mi[v] = __byte_perm(load_word(lvp0 + 4 * g, r * Tile::PB), load_word(lvp1 + 4 * g, r * Tile::PB), 0x7632);
+          }
+        mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int r = 16 * y + 8 * v;
@@ -1224,30 +1207,10 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           for (int P = 0; P < NP; ++P) {
             const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
             const int at = r * Tile::PB + 8 * P;
-            if (plain) {
-              const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
-              const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
-              mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
-              mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
-            } else {
-              __half2 n[2][4];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t even = load_word(j ? lvp1 : lvp0, at), odd = load_word(j ? lvp1 : lvp0, at + 4);
-                const __half2 sc = as_half2(__byte_perm(even, odd, 0x5410)), mn = as_half2(__byte_perm(even, odd, 0x7632));
-                unpack4(j ? w1 : w0, n[j]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) n[j][i] = __hfma2(n[j][i], sc, mn);
-              }
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                float c[4];
-                mma16816(c, as_word(n[0][2 * u]), as_word(n[0][2 * u + 1]), as_word(n[1][2 * u]),
-                         as_word(n[1][2 * u + 1]), p0, p1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[2 * P + u][i] = fmaf(c[i], i < 2 ? 0x1p-24f : 0x1p-20f, o[2 * P + u][i]);
-              }
-            }
+            const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
+            const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
+            mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
+            mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
           }
         }
       }

@@ -10,11 +10,12 @@ Decode, for one query over the kept keys (p the weights, v the values):
   O    the weights inherit the logits' error e (twice, in numerator and sum):
        2 e sum p |v|; sums of fp32 as above with at most 2^-16 of the same. With bf16
        queries weights p are rounded to fp16 (2^-11 of |v|), then products s p (2^-11 of
-       s n <= |v| + |m|, with |m| <= 6 spread in the caches below) or values (2^-11 of
-       |v|); a product below fp16's normal range is cut to steps of 2^-24, off by 2^-25
-       times a code of at most 15, against a sum of weights of at least 4: 2^-23 a key.
+       s n <= |v| + |m|, with |m| <= 6 spread in the caches below); a product below
+       fp16's normal range is cut to steps of 2^-24, off by 2^-25 times a code of at most
+       15, against weights of which the largest is at least 2^10 over twice the largest
+       scale, if that is above 1: 2^-30 (1 + spread) a key.
        In all (2 e + 2^-16) sum p |v|, with bf16 queries 2^-10 sum p |v| + 2^-11 6 spread
-       + 2^-23 keys more, and half a step of the output's type.
+       + 2^-30 (1 + spread) keys more, and half a step of the output's type.
 """
 import math
 
@@ -252,7 +253,7 @@ def _check(x, L, k, shared, tau=None, splits=0, scale=0.0, spread=1.0):
     assert (off <= 0).all(), off.max()
     slack = (2 * e[..., None] + 2.0 ** -16) * A
     if x["q"].dtype == BF:
-        slack += 2.0 ** -10 * A + 2.0 ** -11 * 6 * spread + 2.0 ** -23 * min(L, 64 * (k + 1))
+        slack += 2.0 ** -10 * A + 2.0 ** -11 * 6 * spread + 2.0 ** -30 * (1 + spread) * min(L, 64 * (k + 1))
     _within(O, Or, slack)
 
 
@@ -356,7 +357,7 @@ def test_idle_slots(dtype):
     _check(_decode_case(6, 1, 4, 2, 64, 300, [0], False, dtype), 300, 3, False)
 
 
-@pytest.mark.parametrize("spread", [1e-3, 30.0, 6000.0])
+@pytest.mark.parametrize("spread", [1e-5, 1e-3, 30.0, 6000.0])
 def test_decode_small_and_large_values(spread):
     _check(_decode_case(7, 2, 4, 2, 128, 700, None, True, spread=spread), 700, 6, True, scale=0.02, spread=spread)
 
