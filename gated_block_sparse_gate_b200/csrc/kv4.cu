@@ -344,9 +344,9 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __fl
 // keys on its upper side; no histogram, in which the few exponents of real scores would
 // all meet. Rows of up to 2048 blocks first drop what cannot be among k <= 96 kept ones:
 // at least k keys reach the k-th largest of the threads' own maxima, and those that reach
-// it are few (some 60 of 2048 for k = 32), so that each warp finishes among them alone.
+// it are few (some 60 of 2048 for k = 32), so that one warp finishes among them.
 struct SelectScratch {
-  unsigned u[2][4];
+  unsigned u[2][4], bound;
   float f[4];
   int32_t idx[GBS_MAX_TOPK];
   float score[GBS_MAX_TOPK];
@@ -396,19 +396,19 @@ __device__ __forceinline__ uint32_t warp_threshold(const uint32_t (&u)[N], int k
 constexpr int kCandidates = 256;
 static_assert(128 + 2 * kCandidates <= kSelectWork, "");
 
-// The end of a selection: of n <= kCandidates keys, lane l of every warp holding those of
-// l, l + 32, ..., keeps the k largest. idx(j): the block of the j-th; top: the largest
-// score. The first warp writes the lists.
-template <typename Index>
-__device__ __forceinline__ void keep_largest(const uint32_t (&v)[kCandidates / 32], int n, int k, float top,
-                                             SelectScratch& sc, float* lse, Index idx) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The end of a selection, by a warp whose lane l holds keys l, l + 32, ... of n: of the k
+// largest, idx(j) of the j-th key and its score go to sc where `write`; returns the
+// logarithm of the sum of their exponentials (top: the largest score).
+template <int N, typename Index>
+__device__ __forceinline__ float keep_largest(const uint32_t (&v)[N], int n, int k, float top, bool write,
+                                              SelectScratch& sc, Index idx) {
+  const int lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
   int left, out = 0;
   const uint32_t T = warp_threshold(v, k, 1 << 20, &left);
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kCandidates / 32; ++i) {
+  for (int i = 0; i < N; ++i) {
     if (32 * i >= n) break;
     const uint32_t is_eq = __ballot_sync(0xffffffffu, v[i] == T);
     const bool keep = v[i] > T || (v[i] == T && __popc(is_eq & below) < left);
@@ -416,7 +416,7 @@ __device__ __forceinline__ void keep_largest(const uint32_t (&v)[kCandidates / 3
     if (keep) {
       const float score = key_score(v[i]);
       sum += expf(score - top);
-      if (warp == 0) {
+      if (write) {
         const int j = out + __popc(kept & below);
         sc.idx[j] = idx(lane + 32 * i);
         sc.score[j] = score;
@@ -425,8 +425,7 @@ __device__ __forceinline__ void keep_largest(const uint32_t (&v)[kCandidates / 3
     out += __popc(kept);
     left -= min(left, __popc(is_eq));
   }
-  *lse = top + logf(warp_sum(sum));
-  __syncthreads();
+  return top + logf(warp_sum(sum));
 }
 
 // select_here for r <= 256: every warp alone holds the row.
@@ -451,7 +450,8 @@ __device__ __forceinline__ int select_short(const float* __restrict__ srow, int 
     k = min(k, (int)__reduce_add_sync(0xffffffffu, n));
     if (k == 0) return 0;
   }
-  keep_largest(v, r, k, top, sc, lse, [](int j) { return j; });
+  *lse = keep_largest(v, r, k, top, threadIdx.x < 32, sc, [](int j) { return j; });
+  __syncthreads();
   return k;
 }
 
@@ -492,9 +492,14 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
     k = min(k, (int)(sc.u[1][0] + sc.u[1][1] + sc.u[1][2] + sc.u[1][3]));
     if (k == 0) return 0;
   }
-  int need_eq;
-  uint32_t T = warp_threshold(most, k, 8, &need_eq);
-  if (need_eq > 0) T -= 1u;  // at least k keys are above it
+  if (warp == 0) {  // (one warp's instructions: the other CTAs of the SM use the rest)
+    int need_eq;
+    uint32_t t = warp_threshold(most, k, 5, &need_eq);
+    if (need_eq > 0) t -= 1u;  // at least k keys are above it
+    if (lane == 0) sc.bound = t;
+  }
+  __syncthreads();
+  const uint32_t T = sc.bound;
   unsigned mine = 0u;
 #pragma unroll
   for (int i = 0; i < kSelectRegs; ++i) mine += u[i] > T ? 1u : 0u;
@@ -521,10 +526,23 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
     at += __popc(is);
   }
   __syncthreads();
-  uint32_t v[kCandidates / 32];
+  if (warp == 0) {
+    const auto idx = [&](int j) { return (int)cand_idx[j]; };
+    const auto key = [&](int j) { return j < (int)n ? cand_key[j] : 0u; };
+    float sum;
+    if (n <= 64) {
+      const uint32_t v[2] = {key(lane), key(lane + 32)};
+      sum = keep_largest(v, (int)n, k, top, true, sc, idx);
+    } else {
+      uint32_t v[kCandidates / 32];
 #pragma unroll
-  for (int i = 0; i < kCandidates / 32; ++i) v[i] = lane + 32 * i < (int)n ? cand_key[lane + 32 * i] : 0u;
-  keep_largest(v, (int)n, k, top, sc, lse, [&](int j) { return (int)cand_idx[j]; });
+      for (int i = 0; i < kCandidates / 32; ++i) v[i] = key(lane + 32 * i);
+      sum = keep_largest(v, (int)n, k, top, true, sc, idx);
+    }
+    if (lane == 0) sc.f[0] = sum;
+  }
+  __syncthreads();
+  *lse = sc.f[0];
   return k;
 }
 
