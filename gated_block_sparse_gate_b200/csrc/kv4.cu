@@ -62,8 +62,8 @@ __device__ __forceinline__ float high_half(uint32_t w) {
 
 // Append and read give a row to d / 32 lanes, 16 code bytes to each: halfwords 8 p ..
 // 8 p + 7 of lane p, which hold kSpan consecutive channels of every group, from channel
-// 32 k + kSpan p of group k on. So a lane moves 16 bytes at a time on both sides, and a
-// group's extremes take one or two shuffles for all rows of a warp at once.
+// 32 k + kSpan p of group k on (append). So a lane moves 16 bytes at a time on both sides,
+// and a group's extremes take one or two shuffles for all rows of a warp at once.
 template <int D>
 struct RowLanes {
   static constexpr int NG = D / 32, kSpan = 32 / NG;
@@ -266,36 +266,53 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
   (blockIdx.y ? a.c.vp : a.c.kp)[at * NG + p] = mine;
 }
 
+// A lane writes 16 bytes at a time, next to its neighbours' (whole sectors): unit p, p + NG,
+// ... of a group's. 32768 tokens x 8 heads, d = 128: as fp32 68 us when a lane wrote its 32
+// bytes in two halves.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ RowArgs a) {
-  using R = RowLanes<D>;
-  constexpr int NG = R::NG, kSpan = R::kSpan;
+  constexpr int NG = RowLanes<D>::NG, kChunks = 4 / (int)sizeof(T);  // of four channels, in a unit
+  constexpr int kUnits = 8 / kChunks / NG, kWords = kChunks * NG / 2;  // of a lane; of a unit's codes
   const int p = threadIdx.x % NG;
   const RowPlace r = row_place<D>(a);
   if (r.t < 0) return;
   const Heads& dst = blockIdx.y ? a.t[1] : a.t[0];
   const long long at = r.t < token_count(a, r.b) ? cache_row(a, r.b, r.h, r.t) : -1;
-  uint4 u = make_uint4(0u, 0u, 0u, 0u);
-  uint32_t param[NG] = {};
+  uint32_t w[kUnits][kWords] = {}, param[NG] = {};
   if (at >= 0) {
-    u = __ldg(reinterpret_cast<const uint4*>((blockIdx.y ? a.c.vc : a.c.kc) + at * (D / 2)) + p);
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>((blockIdx.y ? a.c.vc : a.c.kc) + at * (D / 2));
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const uint32_t* from = codes + (p + u * NG) * kWords;
+      if constexpr (kWords == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(from));
+        w[u][0] = x.x; w[u][1] = x.y; w[u][2] = x.z; w[u][3] = x.w;
+      } else if constexpr (kWords == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(from));
+        w[u][0] = x.x; w[u][1] = x.y;
+      } else {
+        w[u][0] = __ldg(from);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < NG; ++k) param[k] = __ldg((blockIdx.y ? a.c.vp : a.c.kp) + at * NG + k);
   }
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   T* row = reinterpret_cast<T*>(dst.ptr) + r.b * dst.sb + r.h * dst.sh + r.t * dst.sn;
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
     const float s = low_half(param[k]), m = high_half(param[k]);
-    float v[kSpan];
 #pragma unroll
-    for (int i = 0; i < kSpan; ++i) {
-      const int j = i / 4 * NG + k;  // the halfword of the lane's eight
-      // the nibble as 2^23 + n, an exact fp32
-      const uint32_t n = (w[j / 2] >> (16 * (j & 1) + 4 * (i & 3)) & 15u) | 0x4b000000u;
-      v[i] = fmaf(s, __uint_as_float(n) - 8388608.f, m);
+    for (int u = 0; u < kUnits; ++u) {
+      float v[4 * kChunks];
+#pragma unroll
+      for (int i = 0; i < 4 * kChunks; ++i) {
+        const int j = i / 4 * NG + k;  // the halfword of the unit
+        // the nibble as 2^23 + n, an exact fp32
+        const uint32_t n = (w[u][j / 2] >> (16 * (j & 1) + 4 * (i & 3)) & 15u) | 0x4b000000u;
+        v[i] = fmaf(s, __uint_as_float(n) - 8388608.f, m);
+      }
+      store_span<4 * kChunks>(row + 32 * k + (p + u * NG) * 4 * kChunks, v);
     }
-    store_span<kSpan>(row + 32 * k + kSpan * p, v);
   }
 }
 
