@@ -63,7 +63,10 @@ __device__ __forceinline__ float high_half(uint32_t w) {
 // Append and read give a row to d / 32 lanes, 16 code bytes to each: halfwords 8 p ..
 // 8 p + 7 of lane p, which hold kSpan consecutive channels of every group, from channel
 // 32 k + kSpan p of group k on (append). So a lane moves 16 bytes at a time on both sides,
-// and a group's extremes take one or two shuffles for all rows of a warp at once.
+// and a group's extremes take one or two shuffles for all rows of a warp at once. Append
+// of 32768 tokens x 8 heads, d = 128, bf16 (176 MB, 27 us): 55 us, bound by issue (0.68 an
+// SM quarter's clock); append and read together took 289 us with four channels to a lane,
+// append 94 with every quotient decided in 64 bits.
 template <int D>
 struct RowLanes {
   static constexpr int NG = D / 32, kSpan = 32 / NG;
@@ -267,8 +270,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
 }
 
 // A lane writes 16 bytes at a time, next to its neighbours' (whole sectors): unit p, p + NG,
-// ... of a group's. 32768 tokens x 8 heads, d = 128: as fp32 68 us when a lane wrote its 32
-// bytes in two halves.
+// ... of a group's. Bound by memory: 32768 tokens x 8 heads, d = 128, as fp32 (310 MB) 53 us,
+// 5.8 TB/s (68 us when a lane wrote its 32 bytes in two halves), as bf16 33 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ RowArgs a) {
   constexpr int NG = RowLanes<D>::NG, kChunks = 4 / (int)sizeof(T);  // of four channels, in a unit
@@ -737,8 +740,10 @@ __device__ __forceinline__ void join_splits(const DecodeArgs& a, float* joined, 
   cluster.sync();  // the others have read this CTA's sums
 }
 
-// fp32 queries: one query head and split per CTA, all in fp32. A lane holds 32 channels of a
-// row (16 code bytes), so D / 32 lanes hold a row and a warp 32 / (D / 32) rows.
+// fp32 queries: one query head and split per CTA, all in fp32, so queries keep their 24
+// bits. A lane holds 32 channels of a row (16 code bytes), so D / 32 lanes hold a row and a
+// warp 32 / (D / 32) rows. Bound by its arithmetic (every value is unpacked for one head);
+// four uneven sequences of up to 4133 tokens, K = 8, take 10.4 us, most of it latency.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int NG = D / 32, LANES = NG, ROWS = 128 / LANES;
@@ -872,6 +877,18 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 // pair, column c with zeros where the other group's factor would be. So codes need
 // nothing but masks and one shift, the accumulators have no padding but unused heads, and
 // the two groups' logits meet in one exchange between lanes.
+//
+// Bytes would bound it (64 sequences x 131072, K = 32, d = 128: 679 MB that differ, 104 us
+// at the copy rate, and the kernel's copies alone take that); instructions do, about 1,300
+// of a warp for 64 keys, most of them masks, factors and the softmax (issue 0.65 a clock, ALU
+// pipe 58%, tensor pipe 18%). Measured: 142 us (4.8 TB/s) with a selection for each head,
+// 47 us (178 MB, floor 27) with one for four heads. Steps, calls per head / shared: one key a
+// thread in fp32 393 / 371 us, products with heads as rows 299 / 101, keys and channels as
+// rows 208 / 73, raw nibbles and a ring for each warp 189 / 70, both groups of a pair as
+// columns 173 / 65, selection and join inside 157 / 50, one path for all scales 148 / 50,
+// one warp ending the selection 145 / 48. Other shapes of it, each against its time's
+// kernel: three CTAs an SM 178 / 74 (161 / 54), five with 96 registers 157 / 58 (148 / 51),
+// three stages a warp 156 / 63 (141 / 47), the loop over channels rolled 167 / 57 (151 / 53).
 constexpr int kUnit = 32;  // keys of a warp's turn
 template <int D>
 struct Kv4Tile {
@@ -1316,8 +1333,8 @@ int decode4_rows(const DecodeArgs& a) {
 // Splits of every CTA row's n_ent blocks. A CTA costs its share and about twelve blocks'
 // worth of selection, beginning and end; while all CTAs fit on the GPU at once the largest
 // share is what counts, beyond that their number (64 x 131072, K = 32: 2048 rows take
-// 157 us with 1 split, 201 with 2, 512 rows 50 and 64; 102 rows of 49 blocks with d = 64
-// take 33 us with 1, 27 with 2, 21 with 4, 31 with 8).
+// 142 us with 1 split, 184 with 2, 512 rows 47 and 60; 102 rows of 49 blocks with d = 64
+// take 29 us with 1, 23 with 2, 19 with 4, 27 with 8).
 int decode4_splits(int rows, int n_ent, int slots) {
   int best = 1;
   float least = 0.f;
