@@ -375,6 +375,8 @@ constexpr int kSelectMax = 8192, kSelectRegs = 16;  // blocks of a row; keys a t
 constexpr int kSelectWork = 640;                   // least words of shared memory
 constexpr int kMaxCluster = 16;  // splits of a row, which join their sums in one cluster
 
+// A score as a key whose order is the scores'; 0 is left for "none" (only one NaN has it).
+__device__ __forceinline__ uint32_t score_key(float score) { return max(ordered_key(score), 1u); }
 __device__ __forceinline__ float key_score(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
@@ -455,7 +457,7 @@ __device__ __forceinline__ int select_short(const float* __restrict__ srow, int 
   uint32_t v[kCandidates / 32], hi = 0u;
 #pragma unroll
   for (int i = 0; i < kCandidates / 32; ++i) {
-    v[i] = lane + 32 * i < r ? ordered_key(__ldg(srow + lane + 32 * i)) : 0u;
+    v[i] = lane + 32 * i < r ? score_key(__ldg(srow + lane + 32 * i)) : 0u;
     hi = max(hi, v[i]);
   }
   const float top = key_score(__reduce_max_sync(0xffffffffu, hi));
@@ -485,7 +487,7 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
   uint32_t u[kSelectRegs], hi = 0u;
 #pragma unroll
   for (int i = 0; i < kSelectRegs; ++i) {
-    u[i] = c0 + 32 * i < c1 ? ordered_key(__ldg(srow + c0 + 32 * i)) : 0u;
+    u[i] = c0 + 32 * i < c1 ? score_key(__ldg(srow + c0 + 32 * i)) : 0u;
     hi = max(hi, u[i]);
   }
   maxima[tid] = hi;
@@ -586,7 +588,7 @@ __device__ __forceinline__ int select_here(const float* __restrict__ srow, int r
     const int c = tid + 128 * i;
     u[i] = 0u;  // below every score's key
     if (c < r) {
-      u[i] = ordered_key(__ldg(srow + c));
+      u[i] = score_key(__ldg(srow + c));
       lo = min(lo, u[i]);
     }
     hi = max(hi, u[i]);
@@ -595,7 +597,7 @@ __device__ __forceinline__ int select_here(const float* __restrict__ srow, int r
   for (int i = 0; i < kSelectRegs; ++i)
     if (tid + 128 * i < r) keys[tid + 128 * i] = u[i];
   for (int c = tid + 128 * kSelectRegs; c < r; c += 128) {
-    const uint32_t x = ordered_key(__ldg(srow + c));
+    const uint32_t x = score_key(__ldg(srow + c));
     keys[c] = x;
     lo = min(lo, x);
     hi = max(hi, x);

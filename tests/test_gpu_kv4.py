@@ -526,3 +526,18 @@ def test_a_prompt_and_steps_through_all_of_it():
         x = dict(q=Q[:, :, 0].cpu(), cache=[t.cpu() for t in cache], table=table.cpu(), lens=lens.cpu(),
                  S=torch.randn(B, Hkv, nb, generator=g))
         _check(x, L, 1, True)
+
+
+@pytest.mark.parametrize("L", [1000, 20000, 140000])
+@pytest.mark.parametrize("k", [0, 20, 96, 256])
+def test_a_nan_score_keeps_the_selection_in_range(L, k):
+    """Scores have to be finite; any NaN among them, the one of all bits set too, still gives blocks of the row."""
+    x = _decode_case(11, 2, 4, 2, 64, L, None, False, shared=False)
+    bits = x["S"].view(torch.int32)
+    bits[0, :2] = -1
+    bits[0, 2, ::3] = 0x7fffffff
+    O, LSE = _run(x, L, k, False)
+    y = dict(x, S=torch.zeros_like(x["S"]))
+    y["S"][1] = x["S"][1]
+    want = _run(y, L, k, False)
+    assert torch.equal(O[1], want[0][1]) and torch.equal(LSE[1], want[1][1])
