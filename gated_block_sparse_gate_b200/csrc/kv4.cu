@@ -1195,7 +1195,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
         uint32_t sc[NG], most = 0u;
         load_words<NG>(st + lane * Tile::PB, Tile::kVp, sc);
 #pragma unroll
-        for (int k = 0; k < NG; ++k) most = max(most, sc[k] & 0xffffu);
+        for (int k = 0; k < NG; ++k) most = max(most, sc[k] & 0x7fffu);  // (a group whose minimum rounds up may have s < 0)
         most = __reduce_max_sync(0xffffffffu, most);
         if (most >= 0x3c00u) room -= (float)((int)(most >> 10) - 14);  // fp16 of 1 and more
       }

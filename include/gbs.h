@@ -358,7 +358,7 @@ GBS_API gbs_status gbs_qkv_rope_bwd(const gbs_rope_params* p, const gbs_heads* q
  *   lo, hi  smallest and largest of the 32 values, limited to +-60000
  *   m = fp16(lo), s = fp16(fp32((hi - m) / 15))
  *   n = (x - m) / s rounded to the nearest whole number (ties to even) and
- *       limited to 0..15, as if computed in 64 bits; 0 where s = 0.
+ *       limited to 0..15, as if computed in 64 bits; 0 where s is not above 0.
  * A NaN among the 32 makes m and s NaN, so all 32 read back as NaN.
  * Layout (d / 2 code bytes and d / 8 parameter bytes a row, 80 in all for d = 128
  * against 256 in bf16): channel c has bits 4 (c % 4) .. + 3 of the row's

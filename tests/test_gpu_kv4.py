@@ -541,3 +541,17 @@ def test_a_nan_score_keeps_the_selection_in_range(L, k):
     y["S"][1] = x["S"][1]
     want = _run(y, L, k, False)
     assert torch.equal(O[1], want[0][1]) and torch.equal(LSE[1], want[1][1])
+
+
+def test_groups_of_one_value_whose_minimum_rounds_up():
+    """0.3 is 0.30005 in fp16, so such a group has a scale below 0 (and codes 0). One key with 8,255 others of 2^-18 of
+    its weight, which together make up 3 % of the sum: the weights have to keep them."""
+    L, d = 64 * 130, 64
+    K, V = torch.zeros(1, 1, L, d), torch.full((1, 1, L, d), 5.0)
+    K[0, 0, 0], V[0, 0, 0] = 12.5, 0.3
+    cache = gb.kv4_cache(1, 1, d, L, device=DEV)
+    gb.kv4_append(K.to(DEV), V.to(DEV), cache, torch.zeros(1, dtype=torch.int32, device=DEV))
+    assert float(cache[3][0, 0, 0, 0, 0]) < 0
+    x = dict(table=None, lens=None, cache=[t.cpu() for t in cache], q=torch.ones(1, 1, d, dtype=BF),
+             S=torch.zeros(1, 1, 130))
+    _check(x, L, 256, False, scale=1 / d)
