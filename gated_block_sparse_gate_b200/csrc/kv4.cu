@@ -1074,9 +1074,11 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     // q as fp16 times a power of two: the largest of a head in 2^8 .. 2^9
     int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 8;
-    if (ex == 120 || ex == -135) ex = 0;  // infinite, zero or subnormal: as it is
-    // the codes' products are 2^-24 of what they stand for, the scales' and minima's not
-    const float down = ldexpf(1.f, -ex), zscale = p.scale_log2 * ldexpf(1.f, ex) * 0x1p24f;
+    if (ex == 120) ex = 0;  // infinite: as it is
+    // in two steps, either of which fp32 can hold
+    const float down0 = ldexpf(1.f, -(ex / 2)), down1 = ldexpf(1.f, -(ex - ex / 2));
+    // (not 0, since keys behind the sequence have -infinity times it)
+    const float zscale = fmaxf(p.scale_log2 * ldexpf(1.f, ex / 2) * ldexpf(1.f, ex - ex / 2), 0x1p-126f);
     zs[0] = __shfl_sync(0xffffffffu, zscale, 4 * (2 * t & 3));
     zs[1] = __shfl_sync(0xffffffffu, zscale, 4 * (2 * t & 3) + 4);
     float qsum = 0.f;
@@ -1085,7 +1087,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const __half x = __float2half_rn(v[P][i] * down);
+        const __half x = __float2half_rn(v[P][i] * down0 * down1);
         sum += __half2float(x);
         // channel i of eight: nibble i % 4 of the lane's word i / 4. High nibbles count 16
         // times; of q, that rounds only what is below 2^-15 of its largest
@@ -1160,12 +1162,11 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           const int r = 16 * y + 8 * x;
           load_words<NG>(lk, r * Tile::RB, kw[x]);
 #pragma unroll
-          for (int P = 0; P < NP; ++P) sc[x][P] = low_half(load_word(lkp + par_k, r * Tile::PB + 8 * P));
+          for (int P = 0; P < NP; ++P)  // (the codes' products are 2^-24 of what they stand for)
+            sc[x][P] = low_half(load_word(lkp + par_k, r * Tile::PB + 8 * P)) * 0x1p24f;
           km[x] = t < NG ? load_word(lkp + 4 * t, r * Tile::PB) : 0u;
         }
         mma16816(z[y], km[0], km[1], km[0], km[1], qm0, qm1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[y][i] *= 0x1p-24f;
 #pragma unroll
         for (int P = 0; P < NP; ++P) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};

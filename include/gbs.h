@@ -412,8 +412,7 @@ GBS_API size_t gbs_kv4_workspace_bytes(const gbs_params* p);
  *   S, LSE  as in gbs_decode_ex.
  *   num_splits  partitions of a row's kept blocks, which join their sums in one
  *          thread-block cluster: of more than 16, 16 are made; 0 = automatic.
- *   ws     gbs_kv4_workspace_bytes(p) bytes (256 up to 8192 blocks a row).
- *   Rows of bf16 queries whose |q| passes 2^100 are not supported. */
+ *   ws     gbs_kv4_workspace_bytes(p) bytes (256 up to 8192 blocks a row). */
 GBS_API gbs_status gbs_kv4_decode(const gbs_params* p, const gbs_kv4_cache* cache,
                                   const int32_t* seq_lens, int group_shared, const void* q,
                                   const float* S, void* O, float* LSE, int num_splits, void* ws,

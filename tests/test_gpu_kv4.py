@@ -555,3 +555,13 @@ def test_groups_of_one_value_whose_minimum_rounds_up():
     x = dict(table=None, lens=None, cache=[t.cpu() for t in cache], q=torch.ones(1, 1, d, dtype=BF),
              S=torch.zeros(1, 1, 130))
     _check(x, L, 256, False, scale=1 / d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("power,scale", [(-124, 0.0), (-124, 2.0 ** 120), (-60, 2.0 ** 57), (60, 2.0 ** -63),
+                                         (118, 2.0 ** -121)])
+def test_decode_of_small_and_large_queries(power, scale, dtype):
+    """Queries near both ends of fp32's range, with a scale that makes their logits ordinary (or leaves them small)."""
+    x = _decode_case(13, 2, 4, 2, 64, 300, [300, 77], True, dtype)
+    x["q"] *= 2.0 ** power
+    _check(x, 300, 3, True, scale=scale)
