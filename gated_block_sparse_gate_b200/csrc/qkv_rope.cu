@@ -335,7 +335,8 @@ __device__ __forceinline__ void backward_tensor(const RopeArgs& a, const Role& r
           if (rotates) rotate<true>(g, ang);
           if (a.norm) {
             const Pairs v = widen<INTER>(rx[u][0], rx[u][1]), hw = times(g, w);
-            const float r = rsqrtf(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps);
+            // (0 for a row that is not there, whose zeros have no finite r where eps = 0)
+            const float sq = row_sum<LANES>(dot(v, v)), r = h < H ? rsqrtf(sq * (1.f / D) + a.eps) : 0.f;
             // mean(h xh) xh = x r^2 mean(h x)
             const float back = row_sum<LANES>(dot(hw, v)) * (1.f / D) * r * r;
             dw = fma(times(g, r), v, dw);  // rows left out have g = x = 0

@@ -218,3 +218,10 @@ def test_on_another_stream_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(kept, want))
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv", [(1, 1, 3, 1), (2, 37, 5, 3), (1, 700, 3, 1)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_eps(B, N, Hq, Hkv, dtype):
+    """Lanes without a row of their own add nothing to the weights' gradients, eps = 0 included."""
+    _check(dict(_case(31, B, N, Hq, Hkv, 64, 64, dtype), eps=0.0))
