@@ -53,8 +53,14 @@ struct Pairs {
 };
 
 template <typename T> struct Quad;  // four channels as one load
-template <> struct Quad<float> { using type = float4; };
-template <> struct Quad<__nv_bfloat16> { using type = uint2; };
+template <> struct Quad<float> {
+  using type = float4;
+  static __device__ __forceinline__ type ones() { return make_float4(1.f, 1.f, 1.f, 1.f); }
+};
+template <> struct Quad<__nv_bfloat16> {
+  using type = uint2;
+  static __device__ __forceinline__ type ones() { return make_uint2(0x3f803f80u, 0x3f803f80u); }
+};
 
 __device__ __forceinline__ f32x2 make2(uint32_t lo, uint32_t hi) {
   return f2_make(__uint_as_float(lo), __uint_as_float(hi));
@@ -311,7 +317,8 @@ __device__ __forceinline__ void backward_tensor(const RopeArgs& a, const Role& r
       Q4 rz[kRows][2], rx[kRows][2];
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
-        rz[u][0] = rz[u][1] = rx[u][0] = rx[u][1] = Q4{};
+        rz[u][0] = rz[u][1] = Q4{};
+        rx[u][0] = rx[u][1] = Quad<T>::ones();  // a row that is not there: r has to be finite with eps = 0
         if (h + u * role.per_token < H) {
           rz[u][0] = __ldg(reinterpret_cast<const Q4*>(dz + off[0]));
           rz[u][1] = __ldg(reinterpret_cast<const Q4*>(dz + off[1]));
@@ -335,11 +342,10 @@ __device__ __forceinline__ void backward_tensor(const RopeArgs& a, const Role& r
           if (rotates) rotate<true>(g, ang);
           if (a.norm) {
             const Pairs v = widen<INTER>(rx[u][0], rx[u][1]), hw = times(g, w);
-            // (0 for a row that is not there, whose zeros have no finite r where eps = 0)
-            const float sq = row_sum<LANES>(dot(v, v)), r = h < H ? rsqrtf(sq * (1.f / D) + a.eps) : 0.f;
+            const float r = rsqrtf(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps);
             // mean(h xh) xh = x r^2 mean(h x)
             const float back = row_sum<LANES>(dot(hw, v)) * (1.f / D) * r * r;
-            dw = fma(times(g, r), v, dw);  // rows left out have g = x = 0
+            dw = fma(times(g, r), v, dw);  // rows left out have g = 0
             g = times(fma(-back, v, hw), r);
           }
           narrow<INTER>(g, &rz[u][0], &rz[u][1]);

@@ -532,7 +532,7 @@ def test_a_prompt_and_steps_through_all_of_it():
 @pytest.mark.parametrize("k", [0, 20, 96, 256])
 def test_a_nan_score_keeps_the_selection_in_range(L, k):
     """Scores have to be finite; any NaN among them, the one of all bits set too, still gives blocks of the row."""
-    x = _decode_case(11, 2, 4, 2, 64, L, None, False, shared=False)
+    x = _decode_case(11, 2, 4, 2, 64, L, None, False, paged=False)
     bits = x["S"].view(torch.int32)
     bits[0, :2] = -1
     bits[0, 2, ::3] = 0x7fffffff
