@@ -112,6 +112,7 @@ def load_library(path: str = LIB_PATH):
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args
+    lib.native = struct.pack("7P", *(ctypes.cast(getattr(lib, name), vp).value for name in _NATIVE))
     _lib = lib
     return lib
 
@@ -160,6 +161,18 @@ except ImportError:  # built without the headers: the checks below do all of it
     _marshal = None
 else:
     _fits, _heads_of = _marshal.fits, _marshal.heads
+
+# The entry points that csrc/marshal.cpp calls, in its order.
+_NATIVE = ("gbs_qkv_rope_fwd", "gbs_qkv_rope_bwd", "gbs_qkv_rope_workspace_bytes", "gbs_kv4_append", "gbs_kv4_read",
+           "gbs_kv4_decode", "gbs_kv4_workspace_bytes")
+
+
+class _NoCalls:
+    """Stands for csrc/marshal.cpp's calls where it is missing: every one is left to this module."""
+    qkv_rope = qkv_rope_backward = kv4_append = kv4_read = kv4_decode = staticmethod(lambda *a: None)
+
+
+_native = _marshal or _NoCalls
 
 
 def _invalid(where, detail):
@@ -608,6 +621,12 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
     ``pos``: int32 [B, N], or [B, N, axes] with ``axes`` the axis of every pair
     (``rope_axes``). ``out``: (Q, K, V) to write to, strided too. Returns (Q, K, V)."""
     where = "gbs_qkv_rope_fwd"
+    if stream is None:
+        r = _native.qkv_rope(load_library().native, q, k, v, cos, sin, pos, wq, wk, eps, axes, interleaved, out, ws)
+        if r is not None:
+            if r[0]:
+                _check(r[0], where)
+            return r[1:]
     lib = load_library()
     dev = _device(where, "q", q)
     ctx = _elsewhere(dev, stream)
@@ -642,6 +661,13 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
     dwq, dwk [d] (None without weights). ``grads``: (dq, dk, dv) to write to,
     such as parts of one packed tensor."""
     where = "gbs_qkv_rope_bwd"
+    if stream is None:
+        r = _native.qkv_rope_backward(load_library().native, q, k, cos, sin, pos, dQ, dK, dV, wq, wk, eps, axes,
+                                      interleaved, grads, ws)
+        if r is not None:
+            if r[0]:
+                _check(r[0], where)
+            return r[1:]
     lib = load_library()
     dev = _device(where, "q", q)
     ctx = _elsewhere(dev, stream)
@@ -757,6 +783,12 @@ def kv4_append(K, V, cache, start, block_table=None, count=None, block=64, ws=No
     (``start`` int32 [B]); with ``count`` (int32 [B]) only its first count[b]
     tokens. ``block_table`` (int32 [B, max_blocks]) makes the cache page pools."""
     where = "gbs_kv4_append"
+    if stream is None:
+        r = _native.kv4_append(load_library().native, K, V, cache, start, block_table, count, block, ws)
+        if r is not None:
+            if r[0]:
+                _check(r[0], where)
+            return
     fn = load_library().gbs_kv4_append
     dev = _device(where, "K", K)
     ctx = _elsewhere(dev, stream)
@@ -772,6 +804,12 @@ def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16
     (K, V) [B, Hkv, T, d] of ``dtype`` (``out`` to write to, strided too); tokens
     from count[b] on are zeros."""
     where = "gbs_kv4_read"
+    if stream is None:
+        r = _native.kv4_read(load_library().native, cache, start, T, block_table, count, dtype, block, out, ws)
+        if r is not None:
+            if r[0]:
+                _check(r[0], where)
+            return r[1:]
     fn = load_library().gbs_kv4_read
     dev = _device(where, "start", start)
     ctx = _elsewhere(dev, stream)
@@ -808,6 +846,13 @@ def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block
     ``L`` the longest length; ``seq_lens`` int32 [B] may hold 0 for an idle slot,
     whose O is 0 and LSE -inf. Returns (O, LSE)."""
     where = "gbs_kv4_decode"
+    if stream is None:
+        r = _native.kv4_decode(load_library().native, q, cache, S, L, block, topk, scale, num_splits, block_table,
+                               seq_lens, group_shared, out, lse, ws, tau)
+        if r is not None:
+            if r[0]:
+                _check(r[0], where)
+            return r[1:]
     lib = load_library()
     dev = _device(where, "q", q)
     ctx = _elsewhere(dev, stream)

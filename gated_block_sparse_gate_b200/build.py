@@ -44,9 +44,9 @@ def _stale(lib=LIB):
 
 
 def build_marshal(force: bool = False, verbose: bool = False):
-    """The binding's argument checks on the tensors themselves (csrc/marshal.cpp), where
-    Python's and torch's headers are installed; the binding does them in Python where the
-    module is missing."""
+    """The binding's argument checks and calls on the tensors themselves (csrc/marshal.cpp),
+    where Python's, torch's and CUDA's headers are installed; the binding does them in Python
+    where the module is missing."""
     src = os.path.join(CSRC, "marshal.cpp")
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > max(
             map(os.path.getmtime, (src, os.path.join(INCLUDE, "gbs.h")))):
@@ -55,15 +55,17 @@ def build_marshal(force: bool = False, verbose: bool = False):
     from torch.utils import cpp_extension
 
     include = sysconfig.get_paths()["include"]
-    dirs = [include, *cpp_extension.include_paths(), INCLUDE]
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    dirs = [include, *cpp_extension.include_paths(), cuda, INCLUDE]
     if not all(any(os.path.exists(os.path.join(d, h)) for d in dirs)
-               for h in ("Python.h", "torch/csrc/autograd/python_variable.h")):
+               for h in ("Python.h", "torch/csrc/autograd/python_variable.h", "c10/cuda/CUDAStream.h",
+                         "cuda_runtime_api.h")):
         return None
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(x for d in dirs for x in ("-isystem", d)), src, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-o", MARSHAL + ".tmp"]
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", MARSHAL + ".tmp"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)

@@ -565,3 +565,74 @@ def test_decode_of_small_and_large_queries(power, scale, dtype):
     x = _decode_case(13, 2, 4, 2, 64, 300, [300, 77], True, dtype)
     x["q"] *= 2.0 ** power
     _check(x, 300, 3, True, scale=scale)
+
+
+def _rows_case():
+    g = torch.Generator().manual_seed(3)
+    K, V = (torch.randn(2, 2, 5, 64, generator=g).to(BF).to(DEV) for _ in "kv")
+    return K, V, torch.tensor([60, 0], dtype=torch.int32, device=DEV), torch.tensor([5, 3], dtype=torch.int32, device=DEV)
+
+
+def test_native_calls_give_what_the_bindings_own_path_gives(monkeypatch):
+    """csrc/marshal.cpp's calls and the Python path behind them: the same results, for given and new outputs, and the
+    same refusals."""
+    K, V, start, count = _rows_case()
+    table = torch.tensor([[2, 0], [1, 3]], dtype=torch.int32, device=DEV)
+    x = _decode_case(17, 2, 4, 2, 64, 300, [300, 77], True)
+    x = {n: t.to(DEV) if isinstance(t, torch.Tensor) else t for n, t in x.items()}
+    x["cache"] = tuple(t.to(DEV) for t in x["cache"])
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+
+    def results():
+        out = []
+        for pages, block_table in ((None, None), (4, table)):
+            cache = gb.kv4_cache(2, 2, 64, L=None if pages else 128, num_pages=pages, device=DEV)
+            for n in (None, count):
+                gb.kv4_append(K, V, cache, start, block_table, n, ws=ws if n is None else None)
+                out += [*cache, *gb.kv4_read(cache, start, 5, block_table, n, dtype=F32)]
+        for tau, splits, lens in ((None, 0, x["lens"]), (0.1, 2, None)):
+            given = dict(out=torch.empty_like(x["q"]), lse=torch.empty(2, 4, device=DEV), ws=ws)
+            for kw in ({}, given):
+                O, LSE = gb.kv4_decode(x["q"], x["cache"], x["S"], 300, topk=3, block_table=x["table"], seq_lens=lens,
+                                       group_shared=True, tau=tau, num_splits=splits, **kw)
+                assert not kw or O is kw["out"] and LSE is kw["lse"]
+                out += [O, LSE]
+        return [t.clone() for t in out]
+
+    def refusals():
+        text = []
+        cache = gb.kv4_cache(2, 2, 64, 128, device=DEV)
+        for call in (lambda: gb.kv4_append(K, V[:, :, :4], cache, start),
+                     lambda: gb.kv4_append(K, V, cache[:3], start),
+                     lambda: gb.kv4_append(K, V, cache, start.long()),
+                     lambda: gb.kv4_read(cache, start, 5, dtype=torch.float16),
+                     lambda: gb.kv4_read(cache, start[:1], 5),
+                     lambda: gb.kv4_decode(x["q"], x["cache"], x["S"], 301, topk=3, block_table=x["table"]),
+                     lambda: gb.kv4_decode(x["q"], x["cache"], x["S"], 300, topk=257, block_table=x["table"],
+                                           group_shared=True),
+                     lambda: gb.kv4_decode(x["q"], x["cache"], x["S"], 300, topk=3, block_table=x["table"],
+                                           group_shared=True, scale=-1.0),
+                     lambda: gb.kv4_decode(x["q"], x["cache"], x["S"], 300, topk=3, block_table=x["table"],
+                                           group_shared=True, ws=ws[:128])):
+            with pytest.raises(gb.GbsError) as e:
+                call()
+            text.append(str(e.value))
+        return text
+
+    assert gb._native is not gb._NoCalls
+    native = results(), refusals()
+    monkeypatch.setattr(gb, "_native", gb._NoCalls)
+    own = results(), refusals()
+    assert all(torch.equal(a, b) for a, b in zip(native[0], own[0])) and native[1] == own[1]
+
+
+def test_plain_calls_are_native(monkeypatch):
+    """Plain arguments do not reach the Python checks."""
+    K, V, start, count = _rows_case()
+    cache = gb.kv4_cache(2, 2, 64, 128, device=DEV)
+    q, S = torch.randn(2, 4, 64, device=DEV), torch.randn(2, 4, 2, device=DEV)
+    monkeypatch.setattr(gb, "_check_kv4", None)
+    gb.kv4_append(K, V, cache, start, count=count)
+    gb.kv4_read(cache, start, 5)
+    gb.kv4_decode(q, cache, S, 100, topk=1)
+    gb.kv4_decode(q.to(BF), cache, S, 100, topk=1, tau=0.5, scale=1)

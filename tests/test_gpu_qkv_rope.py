@@ -225,3 +225,58 @@ def test_on_another_stream_and_in_a_graph():
 def test_no_eps(B, N, Hq, Hkv, dtype):
     """Lanes without a row of their own add nothing to the weights' gradients, eps = 0 included."""
     _check(dict(_case(31, B, N, Hq, Hkv, 64, 64, dtype), eps=0.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("axes,norm,values", [(1, True, True), (3, False, True), (2, True, False)])
+def test_native_calls_give_what_the_bindings_own_path_gives(axes, norm, values, dtype, monkeypatch):
+    """csrc/marshal.cpp's calls and the Python path behind them: the same results and refusals."""
+    x = _dev(_case(41, 2, 37, 6, 2, 64, 48, dtype, axes=axes, norm=norm))
+    if not values:
+        x["v"] = x["dV"] = None
+    ws = torch.zeros(gb.qkv_rope_workspace_bytes(x["q"], x["k"], 48), dtype=torch.uint8, device=DEV)
+    fwd, bwd = ("q", "k", "v", "cos", "sin", "pos", "wq", "wk"), ("q", "k", "cos", "sin", "pos", "dQ", "dK", "dV", "wq", "wk")
+
+    def results():
+        out = []
+        for kw in ({}, dict(ws=ws)):
+            z = gb.qkv_rope(*(x[n] for n in fwd), axes=x["axes"], **kw)
+            out += [*z, *gb.qkv_rope(*(x[n] for n in fwd), axes=tuple(x["axes"]), out=tuple(
+                t if t is None else torch.empty_like(t) for t in z))]
+            g = gb.qkv_rope_backward(*(x[n] for n in bwd), axes=x["axes"], **kw)
+            out += [*g, *gb.qkv_rope_backward(*(x[n] for n in bwd), axes=x["axes"], grads=tuple(
+                t if t is None else torch.empty_like(t) for t in g[:3]))]
+        return out
+
+    def refusals():
+        text = []
+        for change in (dict(cos=x["cos"][:, :8]), dict(pos=x["pos"].long()), dict(wq=x["cos"][0]), dict(q=x["q"][:1]),
+                       dict(sin=None), dict(k=x["k"][:, :, :1].transpose(2, 3))):
+            y = {**x, **change}
+            with pytest.raises(gb.GbsError) as e:
+                gb.qkv_rope(*(y[n] for n in fwd), axes=x["axes"])
+            text.append(str(e.value))
+        for kw in (dict(axes=[9] * 24), dict(axes=[0]), dict(axes=x["axes"], eps=-1.0),
+                   dict(axes=x["axes"], ws=ws[:128]), dict(axes=x["axes"], interleaved=2)):
+            if "interleaved" in kw:  # any truth value is taken
+                assert gb.qkv_rope(*(x[n] for n in fwd), **kw) is not None
+                continue
+            with pytest.raises(gb.GbsError) as e:
+                gb.qkv_rope(*(x[n] for n in fwd), **kw)
+            text.append(str(e.value))
+        return text
+
+    native = results(), refusals()
+    monkeypatch.setattr(gb, "_native", gb._NoCalls)
+    own = results(), refusals()
+    assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(native[0], own[0]))
+    assert native[1] == own[1]
+
+
+def test_plain_calls_are_native(monkeypatch):
+    """Plain arguments do not reach the Python checks."""
+    x = _dev(_case(43, 1, 5, 4, 2, 64, 64, BF))
+    monkeypatch.setattr(gb, "_rope_call", None)
+    Q, K, V = gb.qkv_rope(*(x[n] for n in ("q", "k", "v", "cos", "sin", "pos", "wq", "wk")))
+    gb.qkv_rope_backward(*(x[n] for n in ("q", "k", "cos", "sin", "pos", "dQ", "dK", "dV", "wq", "wk")))
+    assert Q.shape == (1, 4, 5, 64)
