@@ -12,6 +12,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
@@ -135,18 +136,38 @@ gbs_heads heads_in(PyObject* o, int device, at::ScalarType type, Sizes shape, bo
   need(x.scalar_type() == type && x.sizes() == shape);
   return heads_of(x, token_major);
 }
+bool listed(PyObject* o, Py_ssize_t n) {
+  return (PyTuple_CheckExact(o) || PyList_CheckExact(o)) && PySequence_Fast_GET_SIZE(o) == n;
+}
 // What a call returns where it is not given: a new tensor, or the given one (contiguous).
 at::Tensor result(PyObject* o, const at::Tensor& like, at::ScalarType type, Sizes shape) {
   if (o == Py_None) return at::empty(shape, like.options().dtype(type));
   return dense(o, like.get_device(), type, shape);
 }
+// The same of four dimensions, the given one strided too: in the order of their steps,
+// each has to pass all that lies in the ones before, so that no two elements share memory.
+at::Tensor result4(PyObject* o, const at::Tensor& like, Sizes shape) {
+  if (o == Py_None) return at::empty(shape, like.options());
+  const at::Tensor& x = on_device(o, like.get_device());
+  need(x.scalar_type() == like.scalar_type() && x.sizes() == shape && x.stride(3) == 1);
+  if (x.is_contiguous()) return x;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int i, int j) { return x.stride(i) < x.stride(j); });
+  int64_t least = shape[3];
+  for (int i : order)
+    if (shape[i] > 1) {
+      need(x.stride(i) >= least);
+      least = x.stride(i) * shape[i];
+    }
+  return x;
+}
 // The three of a tuple of outputs; all None where there is none.
 void three(PyObject* o, bool third, PyObject** out) {
   out[0] = out[1] = out[2] = Py_None;
   if (o == Py_None) return;
-  need(PyTuple_CheckExact(o) && PyTuple_GET_SIZE(o) == 3);
+  need(listed(o, 3));
   for (int i = 0; i < 3; ++i) {
-    out[i] = PyTuple_GET_ITEM(o, i);
+    out[i] = PySequence_Fast_GET_ITEM(o, i);
     need((out[i] == Py_None) == (i == 2 && !third));
   }
 }
@@ -247,7 +268,7 @@ struct RopeCall {
     const int64_t n_axes = at_.dim() == 2 ? 1 : at_.size(2);
     pos = at_.dim() == 2 ? dense_ptr(pos_, device, at::kInt, {B, N}) : dense_ptr(pos_, device, at::kInt, {B, N, n_axes});
     if (axes != Py_None) {
-      need((PyTuple_CheckExact(axes) || PyList_CheckExact(axes)) && PySequence_Fast_GET_SIZE(axes) == half);
+      need(listed(axes, half));
       for (int i = 0; i < half; ++i) {
         const int v = whole(PySequence_Fast_GET_ITEM(axes, i));
         need(v >= 0 && v < n_axes);
@@ -283,10 +304,10 @@ PyObject* qkv_rope(const Library& lib, PyObject* const* a) {
   }
   PyObject* out[3];
   three(a[11], values, out);
-  at::Tensor Q = result(out[0], q, c.type, {c.B, c.Hq, c.N, c.d}), K = result(out[1], q, c.type, {c.B, c.Hkv, c.N, c.d}), V;
+  at::Tensor Q = result4(out[0], q, {c.B, c.Hq, c.N, c.d}), K = result4(out[1], q, {c.B, c.Hkv, c.N, c.d}), V;
   oq = heads_of(Q, false);
   ok = heads_of(K, false);
-  if (values) ov = heads_of(V = result(out[2], q, c.type, {c.B, c.Hkv, c.N, c.d}), false);
+  if (values) ov = heads_of(V = result4(out[2], q, {c.B, c.Hkv, c.N, c.d}), false);
   return returned(lib.rope_fwd(&c.p, &c.q, &c.k, values ? &v : nullptr, c.wq, c.wk, (const float*)c.cos,
                                (const float*)c.sin, (const int32_t*)c.pos, &oq, &ok, values ? &ov : nullptr, ws,
                                stream_of(c.device)),
@@ -309,10 +330,10 @@ PyObject* qkv_rope_backward(const Library& lib, PyObject* const* a) {
     ws = on_device(a[14], c.device);
     need(ws.scalar_type() == at::kByte && ws.is_contiguous());
   }
-  at::Tensor dq = result(out[0], q, c.type, {c.B, c.N, c.Hq, c.d}), dk = result(out[1], q, c.type, {c.B, c.N, c.Hkv, c.d}), dv;
+  at::Tensor dq = result4(out[0], q, {c.B, c.N, c.Hq, c.d}), dk = result4(out[1], q, {c.B, c.N, c.Hkv, c.d}), dv;
   oq = heads_of(dq, true);
   ok = heads_of(dk, true);
-  if (values) ov = heads_of(dv = result(out[2], q, c.type, {c.B, c.N, c.Hkv, c.d}), true);
+  if (values) ov = heads_of(dv = result4(out[2], q, {c.B, c.N, c.Hkv, c.d}), true);
   at::Tensor dwq, dwk;
   if (c.wq) {
     dwq = at::empty({c.d}, q.options().dtype(at::kFloat));
@@ -335,7 +356,7 @@ struct CacheCall {
   int64_t Hkv, d, most;  // most: the longest length that fits
 
   CacheCall(PyObject* cache, int64_t B, int device, int block, PyObject* table) {
-    need((PyTuple_CheckExact(cache) || PyList_CheckExact(cache)) && PySequence_Fast_GET_SIZE(cache) == 4 && block > 0);
+    need(listed(cache, 4) && block > 0);
     PyObject* const* t = PySequence_Fast_ITEMS(cache);
     const at::Tensor& kc = on_device(t[0], device);
     need(kc.dim() == 4);
@@ -392,9 +413,9 @@ PyObject* kv4_append(const Library& lib, PyObject* const* a) {
 // kv4_read(cache, start, T, block_table, count, dtype, block, out, ws), out None
 PyObject* kv4_read(const Library& lib, PyObject* const* a) {
   const at::Tensor& start = anchor(a[1]);
-  need(a[7] == Py_None && THPDtype_Check(a[5]) && PyTuple_CheckExact(a[0]) && PyTuple_GET_SIZE(a[0]) == 4);
+  need(a[7] == Py_None && THPDtype_Check(a[5]) && listed(a[0], 4));
   const auto type = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
-  const at::Tensor& kc = on_device(PyTuple_GET_ITEM(a[0], 0), start.get_device());
+  const at::Tensor& kc = on_device(PySequence_Fast_GET_ITEM(a[0], 0), start.get_device());
   const int T = whole(a[2]);
   need(kc.dim() == 4 && start.dim() == 1 && T > 0 && (type == at::kBFloat16 || type == at::kFloat));
   const int64_t shape[4] = {start.size(0), kc.size(1), T, 2 * kc.size(3)};

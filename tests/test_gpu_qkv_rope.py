@@ -279,4 +279,13 @@ def test_plain_calls_are_native(monkeypatch):
     monkeypatch.setattr(gb, "_rope_call", None)
     Q, K, V = gb.qkv_rope(*(x[n] for n in ("q", "k", "v", "cos", "sin", "pos", "wq", "wk")))
     gb.qkv_rope_backward(*(x[n] for n in ("q", "k", "cos", "sin", "pos", "dQ", "dK", "dV", "wq", "wk")))
+    packed = torch.zeros(1, 5, 8, 64, dtype=BF, device=DEV)
+    gb.qkv_rope_backward(*(x[n] for n in ("q", "k", "cos", "sin", "pos", "dQ", "dK", "dV", "wq", "wk")),
+                         grads=packed.split((4, 2, 2), 2))
+    monkeypatch.undo()
+    for grads in ((packed[:, :, :1].expand(1, 5, 4, 64), None, None), (packed.as_strided((1, 5, 4, 64), (2560, 256, 32, 1)),
+                                                                      None, None)):
+        with pytest.raises(gb.GbsError, match="share memory"):
+            gb.qkv_rope_backward(*(x[n] for n in ("q", "k", "cos", "sin", "pos", "dQ", "dK")), None, x["wq"], x["wk"],
+                                 grads=(grads[0], packed[:, :, 4:6], None))
     assert Q.shape == (1, 4, 5, 64)
