@@ -959,7 +959,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-template <int D>
+// ONE: a single head a CTA. Then the columns are the groups of a row (repeated where there
+// are fewer than eight), so that the value products of all pairs of groups share their
+// accumulators, and after the key products every lane holds the logit of one key of its own:
+// one exponential, and the minima's part as products of its own, for 32 keys.
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __grid_constant__ DecodeArgs a) {
   using Tile = Kv4Tile<D>;
   constexpr int NG = Tile::NG, NP = NG / 2, S = Tile::kStages;
@@ -984,7 +988,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     b = srow / p.Hkv;
     kvh = srow % p.Hkv;
     h0 = kvh * p.G + sub * 4;
-    nh = min(4, p.G - sub * 4);
+    nh = ONE ? 1 : min(4, p.G - sub * 4);
   } else {
     srow = blockIdx.x;
     b = srow / p.Hq;
@@ -1050,35 +1054,66 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   look_up(lane);
   for (int s = 0; s < S && s < turns; ++s) issue(s, s);
 
-  // column g of a product: head g & 3, group parity g >> 2; result columns 2 t and 2 t + 1:
-  // heads 2 t & 3 and the next, parity t >> 1
   const int g = lane >> 2, t = lane & 3;
+  // q as fp16 times a power of two, the largest of a head in 2^8 .. 2^9: 2^-ex in two steps,
+  // either of which fp32 can hold, and the logits' factor that undoes it (not 0, since keys
+  // behind the sequence have -infinity times it)
+  float down0, down1;
+  auto fit = [&](float mx) {
+    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 8;
+    if (ex == 120) ex = 0;  // infinite: as it is
+    down0 = ldexpf(1.f, -(ex / 2)), down1 = ldexpf(1.f, -(ex - ex / 2));
+    return fmaxf(p.scale_log2 * ldexpf(1.f, ex / 2) * ldexpf(1.f, ex - ex / 2), 0x1p-126f);
+  };
+  auto load_q = [&](const __nv_bfloat16* q, bool there, float (&v)[8], float& mx) {
+    const uint4 u = there ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      mx = fmaxf(mx, fabsf(v[i]));
+    }
+  };
+  // channel i of eight: nibble i % 4 of the lane's word i / 4. High nibbles count 16 times;
+  // of q, that rounds only what is below 2^-15 of its largest
+  auto operand = [&](float v, int i, float& sum) {
+    const __half x = __float2half_rn(v * down0 * down1);
+    sum += __half2float(x);
+    return (uint32_t)__half_as_ushort(i & 1 ? __hmul(x, __ushort_as_half(0x2c00)) : x);  // 2^-4
+  };
   uint32_t qb[NP][8], qm0 = 0u, qm1 = 0u;
-  float zs[2];
-  {
+  float zs[2], q_sum[2];
+  if constexpr (ONE) {
+    // column g of a product: group g % NG; result columns 2 t and 2 t + 1: groups 2 t % NG and the next
+    const int group = g & (NG - 1);
+    float v[8], mx = 0.f, sum = 0.f;
+    load_q(reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0) * D + 32 * group + 8 * t, true, v, mx);
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    zs[0] = fit(mx);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t bits = operand(v[i], i, sum);
+#pragma unroll
+      for (int P = 0; P < NP; ++P) qb[P][i] = group >> 1 == P ? bits << 16 * (group & 1) : 0u;
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) q_sum[c] = __shfl_sync(0xffffffffu, sum, 4 * ((2 * t & (NG - 1)) + c));
+  } else {
+    // column g of a product: head g & 3, group parity g >> 2; result columns 2 t and 2 t + 1:
+    // heads 2 t & 3 and the next, parity t >> 1
     const int h = g & 3, par = g >> 2;
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + h) * D + 32 * par + 8 * t;
     float v[NP][8], mx = 0.f;
 #pragma unroll
-    for (int P = 0; P < NP; ++P) {
-      const uint4 u = h < nh ? __ldg(reinterpret_cast<const uint4*>(q + 64 * P)) : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[P][i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-        mx = fmaxf(mx, fabsf(v[P][i]));
-      }
-    }
+    for (int P = 0; P < NP; ++P)
+      load_q(reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * p.Hq + h0 + h) * D + 32 * par + 8 * t + 64 * P,
+             h < nh, v[P], mx);
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-    // q as fp16 times a power of two: the largest of a head in 2^8 .. 2^9
-    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 8;
-    if (ex == 120) ex = 0;  // infinite: as it is
-    // in two steps, either of which fp32 can hold
-    const float down0 = ldexpf(1.f, -(ex / 2)), down1 = ldexpf(1.f, -(ex - ex / 2));
-    // (not 0, since keys behind the sequence have -infinity times it)
-    const float zscale = fmaxf(p.scale_log2 * ldexpf(1.f, ex / 2) * ldexpf(1.f, ex - ex / 2), 0x1p-126f);
+    const float zscale = fit(mx);
     zs[0] = __shfl_sync(0xffffffffu, zscale, 4 * (2 * t & 3));
     zs[1] = __shfl_sync(0xffffffffu, zscale, 4 * (2 * t & 3) + 4);
     float qsum = 0.f;
@@ -1086,14 +1121,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     for (int P = 0; P < NP; ++P) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __half x = __float2half_rn(v[P][i] * down0 * down1);
-        sum += __half2float(x);
-        // channel i of eight: nibble i % 4 of the lane's word i / 4. High nibbles count 16
-        // times; of q, that rounds only what is below 2^-15 of its largest
-        const uint32_t bits = __half_as_ushort(i & 1 ? __hmul(x, __ushort_as_half(0x2c00)) : x);  // 2^-4
-        qb[P][i] = par ? bits << 16 : bits;
-      }
+      for (int i = 0; i < 8; ++i) qb[P][i] = operand(v[P][i], i, sum) << 16 * par;
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       // the minima's product takes parameter word t of a key as (s, m): group t's sum to m
@@ -1108,12 +1136,14 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
 
   // sums of the result columns' heads; a head that is not there never raises its maximum
   // (o in units of 2^-24 and 2^-20 of low and high nibbles; om: the minima's part, group g)
-  float o[NP * 2][4], om[4] = {0.f, 0.f, 0.f, 0.f}, m[2], l[2] = {0.f, 0.f};
+  // (ONE: om of a lane's own keys, for every group)
+  constexpr int kSums = ONE ? 2 : NP * 2;
+  float o[kSums][4], om[4] = {0.f, 0.f, 0.f, 0.f}, m[2], l[2] = {0.f, 0.f};
   const int hc = 2 * t & 3;  // head of column 2 t
-  m[0] = hc < nh ? -INFINITY : INFINITY;
+  m[0] = ONE || hc < nh ? -INFINITY : INFINITY;
   m[1] = hc + 1 < nh ? -INFINITY : INFINITY;
 #pragma unroll
-  for (int i = 0; i < NP * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int i = 0; i < kSums; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
   // the product's row n is key n ^ (n >> 1 & 1) of eight, an order in which neither
   // kind of load meets a bank twice more than it must
@@ -1126,6 +1156,23 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   const uint32_t par_k = 4 * (t >> 1), par_v = 4 * (g >> 2);
   // byte selectors that put the low or high half of a word into the half of column g's parity
   const uint32_t sel0 = g >> 2 ? 0x1044u : 0x4410u, sel1 = g >> 2 ? 0x3244u : 0x4432u;
+  // ONE: a lane's own key among the 32, its column's group, and the selectors for that (or
+  // nothing, for the other pairs of groups)
+  const int my_key = 8 * t + row_k, group = g & (NG - 1);
+  uint32_t lo_to[NP], hi_to[NP];
+#pragma unroll
+  for (int P = 0; P < NP; ++P) {
+    lo_to[P] = group >> 1 != P ? 0x4444u : group & 1 ? 0x1044u : 0x4410u;
+    hi_to[P] = group >> 1 != P ? 0x4444u : group & 1 ? 0x3244u : 0x4432u;
+  }
+  // what the value scales of 32 keys, a key's parameters to a lane, leave of kRoom
+  auto room_for = [](const uint32_t (&params)[NG]) {
+    uint32_t most = 0u;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) most = max(most, params[k] & 0x7fffu);  // (a group whose minimum rounds up may have s < 0)
+    most = __reduce_max_sync(0xffffffffu, most);
+    return most >= 0x3c00u ? kRoom - (float)((int)(most >> 10) - 14) : kRoom;  // fp16 of 1 and more
+  };
   int s = 0;
   uint32_t parity = 0;
   for (int turn = 0; turn < turns; ++turn) {
@@ -1151,121 +1198,199 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           }
         __syncwarp();
       }
-      // of 16 keys y: z of keys row_k (z[y][0], z[y][1]: heads 2 t, 2 t + 1) and row_k + 8
-      float z[2][4];
+      if constexpr (ONE) {
+        const float bias = s_bias[s];
+        // the products of 16 keys y: c[y][0], c[y][1] of key row_k and c[y][2], c[y][3] of
+        // row_k + 8, with the groups of columns 2 t and 2 t + 1
+        float c[2][4];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t kw[2][NG], km[2];
-        float sc[2][NP];
+        for (int y = 0; y < 2; ++y) {
+          uint32_t kw[2][NG];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = 16 * y + 8 * x;
-          load_words<NG>(lk, r * Tile::RB, kw[x]);
+          for (int x = 0; x < 2; ++x) load_words<NG>(lk, (16 * y + 8 * x) * Tile::RB, kw[x]);
 #pragma unroll
-          for (int P = 0; P < NP; ++P)  // (the codes' products are 2^-24 of what they stand for)
-            sc[x][P] = low_half(load_word(lkp + par_k, r * Tile::PB + 8 * P)) * 0x1p24f;
-          km[x] = t < NG ? load_word(lkp + 4 * t, r * Tile::PB) : 0u;
+          for (int P = 0; P < NP; ++P)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w0 = kw[0][NP * j + P], w1 = kw[1][NP * j + P], h0 = w0 >> 8, h1 = w1 >> 8;
+              if (P == 0 && j == 0) mma16816(c[y], w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qb[P][0], qb[P][1]);
+              else mma16816_add(c[y], w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qb[P][4 * j], qb[P][4 * j + 1]);
+              mma16816_add(c[y], h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qb[P][4 * j + 2], qb[P][4 * j + 3]);
+            }
         }
-        mma16816(z[y], km[0], km[1], km[0], km[1], qm0, qm1);
+        // the logit of the lane's own key, 16 (t / 2) + 8 (t % 2) + row_k
+        const bool late = t >> 1, odd = t & 1;
+        auto logit = [&](float c0, float c1, int key) {  // of a key's two groups
+          uint32_t w[2];
+          load_words<2>(st + Tile::kKp + key * Tile::PB + 4 * (2 * t & (NG - 1)), 0, w);
+          return fmaf(fmaf(low_half(w[1]), c1, low_half(w[0]) * c0), 0x1p24f,
+                      fmaf(high_half(w[1]), q_sum[1], high_half(w[0]) * q_sum[0]));
+        };
+        float z;
+        const float c0 = late ? c[1][0] : c[0][0], c1 = late ? c[1][1] : c[0][1];
+        const float c2 = late ? c[1][2] : c[0][2], c3 = late ? c[1][3] : c[0][3];
+        if constexpr (NG == 4) {  // the lanes 2 and 2 + 1 of four hold two groups each
+          const int key = 16 * (t >> 1) + row_k;
+          const float z0 = logit(c0, c1, key), z1 = logit(c2, c3, key + 8);
+          z = (odd ? z1 : z0) + __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
+        } else {
+          z = logit(odd ? c2 : c0, odd ? c3 : c1, my_key);
+        }
+        if (my_key >= rows) z = -INFINITY;  // (the scale is not negative)
+        uint32_t vp[NG];
+        load_words<NG>(st + my_key * Tile::PB, Tile::kVp, vp);
+        const float room = room_for(vp);
+        float x = fmaf(z, zs[0], bias - m[0]);
+        if (__any_sync(0xffffffffu, x > room)) {  // as below
+          float mx = z;
 #pragma unroll
-        for (int P = 0; P < NP; ++P) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int w = 1; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const float mn = fmaxf(m[0], fmaf(mx, zs[0], bias) + (kRoom - kLift - room));
+          const float f = m[0] == mn ? 1.f : fast_exp2(m[0] - mn);
+          m[0] = mn;
+          l[0] *= f;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {  // four channels 2 t + j of both groups
-            const uint32_t w0 = kw[0][NP * j + P], w1 = kw[1][NP * j + P], h0 = w0 >> 8, h1 = w1 >> 8;
-            mma16816_add(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qb[P][4 * j], qb[P][4 * j + 1]);
-            mma16816_add(c, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qb[P][4 * j + 2], qb[P][4 * j + 3]);
+          for (int i = 0; i < 4; ++i) {
+            om[i] *= f;
+            o[0][i] *= f;
+            o[1][i] *= f;
           }
-          z[y][0] = fmaf(sc[0][P], c[0], z[y][0]);
-          z[y][1] = fmaf(sc[0][P], c[1], z[y][1]);
-          z[y][2] = fmaf(sc[1][P], c[2], z[y][2]);
-          z[y][3] = fmaf(sc[1][P], c[3], z[y][3]);
+          x = fmaf(z, zs[0], bias - m[0]);
         }
+        const float pr = fast_exp2(x);
+        l[0] += pr;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[y][i] += __shfl_xor_sync(0xffffffffu, z[y][i], 2);  // the other parity's
-      }
-      if (ends) {
-        __syncwarp();
+        for (int k = 0; k < NG; ++k) om[k] = fmaf(pr, high_half(vp[k]), om[k]);
+        // weights as fp16, of product rows 2 t and 2 t + 1 of each eight keys, in every column
+        const float other = __shfl_xor_sync(0xffffffffu, pr, 4);
+        const uint32_t two = g & 1 ? pack_half2(other, pr) : pack_half2(pr, other);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // scales of the heads are not negative
-          if (row_k + 8 * (i >> 1) >= rows) z[i >> 2][i & 3] = -INFINITY;
-      }
-      // what the value scales of the 32 keys (a lane looks at one's) leave of kRoom
-      float room = kRoom;
-      {
-        uint32_t sc[NG], most = 0u;
-        load_words<NG>(st + lane * Tile::PB, Tile::kVp, sc);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t pw = __shfl_sync(0xffffffffu, two, 8 * t + e);
+          uint32_t vw[2][NP];
+          load_words<NP>(lv0, 8 * e * Tile::RB, vw[0]);
+          load_words<NP>(lv1, 8 * e * Tile::RB, vw[1]);
+          const uint32_t sc = __byte_perm(load_word(lvp0 + 4 * group, 8 * e * Tile::PB),
+                                          load_word(lvp1 + 4 * group, 8 * e * Tile::PB), 0x5410);
+          const uint32_t ps = as_word(__hmul2(as_half2(pw), as_half2(sc)));
 #pragma unroll
-        for (int k = 0; k < NG; ++k) most = max(most, sc[k] & 0x7fffu);  // (a group whose minimum rounds up may have s < 0)
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (most >= 0x3c00u) room -= (float)((int)(most >> 10) - 14);  // fp16 of 1 and more
-      }
-      // logarithms of the weights; m is raised only where one would pass that, so the
-      // exchange between lanes that a maximum takes is seldom needed
-      const float bias = s_bias[s];
-      float x[2][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = fmaf(z[i >> 2][i & 3], zs[i & 1], bias - m[i & 1]);
-      float mx[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(x[0][c], x[0][2 + c]), fmaxf(x[1][c], x[1][2 + c]));
-      if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > room)) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mx[c] = fmaxf(fmaxf(z[0][c], z[0][2 + c]), fmaxf(z[1][c], z[1][2 + c]));
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], w));
-          const float mn = fmaxf(m[c], fmaf(mx[c], zs[c], bias) + (kRoom - kLift - room));
-          const float f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
-          m[c] = mn;
-          l[c] *= f;
-          om[c] *= f;
-#pragma unroll
-          for (int i = 0; i < NP * 2; ++i) {
-            o[i][c] *= f;
-            o[i][2 + c] *= f;
+          for (int P = 0; P < NP; ++P) {
+            const uint32_t w0 = vw[0][P], w1 = vw[1][P], h0 = w0 >> 8, h1 = w1 >> 8;
+            const uint32_t b0 = __byte_perm(ps, 0u, lo_to[P]), b1 = __byte_perm(ps, 0u, hi_to[P]);
+            mma16816_add(o[0], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
+            mma16816_add(o[1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
           }
         }
+      } else {
+        // of 16 keys y: z of keys row_k (z[y][0], z[y][1]: heads 2 t, 2 t + 1) and row_k + 8
+        float z[2][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t kw[2][NG], km[2];
+          float sc[2][NP];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = 16 * y + 8 * x;
+            load_words<NG>(lk, r * Tile::RB, kw[x]);
+#pragma unroll
+            for (int P = 0; P < NP; ++P)  // (the codes' products are 2^-24 of what they stand for)
+              sc[x][P] = low_half(load_word(lkp + par_k, r * Tile::PB + 8 * P)) * 0x1p24f;
+            km[x] = t < NG ? load_word(lkp + 4 * t, r * Tile::PB) : 0u;
+          }
+          mma16816(z[y], km[0], km[1], km[0], km[1], qm0, qm1);
+#pragma unroll
+          for (int P = 0; P < NP; ++P) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // four channels 2 t + j of both groups
+              const uint32_t w0 = kw[0][NP * j + P], w1 = kw[1][NP * j + P], h0 = w0 >> 8, h1 = w1 >> 8;
+              mma16816_add(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qb[P][4 * j], qb[P][4 * j + 1]);
+              mma16816_add(c, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qb[P][4 * j + 2], qb[P][4 * j + 3]);
+            }
+            z[y][0] = fmaf(sc[0][P], c[0], z[y][0]);
+            z[y][1] = fmaf(sc[0][P], c[1], z[y][1]);
+            z[y][2] = fmaf(sc[1][P], c[2], z[y][2]);
+            z[y][3] = fmaf(sc[1][P], c[3], z[y][3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[y][i] += __shfl_xor_sync(0xffffffffu, z[y][i], 2);  // the other parity's
+        }
+        if (ends) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // scales of the heads are not negative
+            if (row_k + 8 * (i >> 1) >= rows) z[i >> 2][i & 3] = -INFINITY;
+        }
+        uint32_t vp[NG];
+        load_words<NG>(st + lane * Tile::PB, Tile::kVp, vp);
+        const float room = room_for(vp);
+        // logarithms of the weights; m is raised only where one would pass that, so the
+        // exchange between lanes that a maximum takes is seldom needed
+        const float bias = s_bias[s];
+        float x[2][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = fmaf(z[i >> 2][i & 3], zs[i & 1], bias - m[i & 1]);
-      }
+        float mx[2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t pb[2];  // head g, keys of the columns 2 t and 2 t + 1
+        for (int c = 0; c < 2; ++c) mx[c] = fmaxf(fmaxf(x[0][c], x[0][2 + c]), fmaxf(x[1][c], x[1][2 + c]));
+        if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > room)) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const float p0 = fast_exp2(x[y][2 * v]), p1 = fast_exp2(x[y][2 * v + 1]);
-          l[0] += p0;
-          l[1] += p1;
-          pb[v] = transpose8x8(pack_half2(p0, p1));
+          for (int c = 0; c < 2; ++c) {
+            mx[c] = fmaxf(fmaxf(z[0][c], z[0][2 + c]), fmaxf(z[1][c], z[1][2 + c]));
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], w));
+            const float mn = fmaxf(m[c], fmaf(mx[c], zs[c], bias) + (kRoom - kLift - room));
+            const float f = m[c] == mn ? 1.f : fast_exp2(m[c] - mn);
+            m[c] = mn;
+            l[c] *= f;
+            om[c] *= f;
+#pragma unroll
+            for (int i = 0; i < NP * 2; ++i) {
+              o[i][c] *= f;
+              o[i][2 + c] *= f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = fmaf(z[i >> 2][i & 3], zs[i & 1], bias - m[i & 1]);
         }
-        uint32_t vw[2][2][NP];  // of keys row_v0 and row_v1: four channels g of both groups of a pair
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int r = 16 * y + 8 * v;
-          load_words<NP>(lv0, r * Tile::RB, vw[v][0]);
-          load_words<NP>(lv1, r * Tile::RB, vw[v][1]);
-        }
-        uint32_t mi[2] = {0u, 0u};
-        if (g < NG)
+        for (int y = 0; y < 2; ++y) {
+          uint32_t pb[2];  // head g, keys of the columns 2 t and 2 t + 1
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const float p0 = fast_exp2(x[y][2 * v]), p1 = fast_exp2(x[y][2 * v + 1]);
+            l[0] += p0;
+            l[1] += p1;
+            pb[v] = transpose8x8(pack_half2(p0, p1));
+          }
+          uint32_t vw[2][2][NP];  // of keys row_v0 and row_v1: four channels g of both groups of a pair
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int r = 16 * y + 8 * v;
-            mi[v] = __byte_perm(load_word(lvp0 + 4 * g, r * Tile::PB), load_word(lvp1 + 4 * g, r * Tile::PB), 0x7632);
+            load_words<NP>(lv0, r * Tile::RB, vw[v][0]);
+            load_words<NP>(lv1, r * Tile::RB, vw[v][1]);
           }
-        mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
+          uint32_t mi[2] = {0u, 0u};
+          if (g < NG)
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int r = 16 * y + 8 * v;
-          const uint32_t p0 = __byte_perm(pb[v], 0u, sel0), p1 = __byte_perm(pb[v], 0u, sel1);
+            for (int v = 0; v < 2; ++v) {
+              const int r = 16 * y + 8 * v;
+              mi[v] = __byte_perm(load_word(lvp0 + 4 * g, r * Tile::PB), load_word(lvp1 + 4 * g, r * Tile::PB), 0x7632);
+            }
+          mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
 #pragma unroll
-          for (int P = 0; P < NP; ++P) {
-            const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
-            const int at = r * Tile::PB + 8 * P;
-            const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
-            const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
-            mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
-            mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
+          for (int v = 0; v < 2; ++v) {
+            const int r = 16 * y + 8 * v;
+            const uint32_t p0 = __byte_perm(pb[v], 0u, sel0), p1 = __byte_perm(pb[v], 0u, sel1);
+#pragma unroll
+            for (int P = 0; P < NP; ++P) {
+              const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
+              const int at = r * Tile::PB + 8 * P;
+              const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
+              const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
+              mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
+              mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
+            }
           }
         }
       }
@@ -1277,31 +1402,49 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       parity ^= 1u;
     }
   }
-#pragma unroll
-  for (int w = 4; w < 32; w <<= 1) {
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
-    l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
-  }
-  float least[NP][2];
-#pragma unroll
-  for (int P = 0; P < NP; ++P)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) least[P][c] = __shfl_sync(0xffffffffu, om[c], 4 * (2 * P + (t >> 1)) + t);
   // the warp's stages are all read: their memory takes its sums
+  if constexpr (ONE) {
+    l[0] = warp_sum(l[0]);
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (hc + c < nh) {
-      float* sum = reinterpret_cast<float*>(ring) + (hc + c) * D + 32 * (t >> 1) + 4 * g;
+    for (int k = 0; k < NG; ++k) om[k] = warp_sum(om[k]);
+    if (t < NP)  // the columns of groups 2 t and 2 t + 1
 #pragma unroll
-      for (int P = 0; P < NP; ++P)
-        *reinterpret_cast<float4*>(sum + 64 * P) =
-            make_float4(fmaf(o[2 * P][c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
-                        fmaf(o[2 * P + 1][c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
-      if (g == 0 && t < 2) {
-        s_m[warp][hc + c] = m[c];
-        s_l[warp][hc + c] = l[c];
+      for (int c = 0; c < 2; ++c) {
+        const float least = t == 0 ? om[c] : om[2 + c];
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + 32 * (2 * t + c) + 4 * g) =
+            make_float4(fmaf(o[0][c], 0x1p24f, least), fmaf(o[0][2 + c], 0x1p20f, least),
+                        fmaf(o[1][c], 0x1p24f, least), fmaf(o[1][2 + c], 0x1p20f, least));
       }
+    if (lane == 0) {
+      s_m[warp][0] = m[0];
+      s_l[warp][0] = l[0];
     }
+  } else {
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
+    }
+    float least[NP][2];
+#pragma unroll
+    for (int P = 0; P < NP; ++P)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) least[P][c] = __shfl_sync(0xffffffffu, om[c], 4 * (2 * P + (t >> 1)) + t);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (hc + c < nh) {
+        float* sum = reinterpret_cast<float*>(ring) + (hc + c) * D + 32 * (t >> 1) + 4 * g;
+#pragma unroll
+        for (int P = 0; P < NP; ++P)
+          *reinterpret_cast<float4*>(sum + 64 * P) =
+              make_float4(fmaf(o[2 * P][c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
+                          fmaf(o[2 * P + 1][c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
+        if (g == 0 && t < 2) {
+          s_m[warp][hc + c] = m[c];
+          s_l[warp][hc + c] = l[c];
+        }
+      }
+  }
   __syncthreads();
   // the warps' sums as one; the splits of a row are a cluster and meet in shared memory
   float* joined = reinterpret_cast<float*>(smem) + 4 * D;
@@ -1362,13 +1505,13 @@ cudaError_t sm_count(int device, int* sms) {
 }
 
 // One launch: rows x splits CTAs, the splits of a row a cluster.
-template <typename T, int D>
+template <typename T, int D, bool ONE>
 cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
   constexpr bool kMma = sizeof(T) == 2;
   void (*kernel)(DecodeArgs);
   size_t smem;
   if constexpr (kMma) {
-    kernel = kv4_decode_mma_kernel<D>;
+    kernel = kv4_decode_mma_kernel<D, ONE>;
     smem = Kv4Tile<D>::kBytes;
   } else {
     kernel = kv4_decode_simt_kernel<T, D>;
@@ -1577,9 +1720,10 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   if (a.splits == 0) a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms);
   if (a.splits > n_ent) a.splits = n_ent;
   if (a.splits > kMaxCluster) a.splits = kMaxCluster;
-  if (p.dtype == GBS_BF16)
-    e = p.d == 64 ? launch_decode4<__nv_bfloat16, 64>(a, device, st) : launch_decode4<__nv_bfloat16, 128>(a, device, st);
-  else
-    e = p.d == 64 ? launch_decode4<float, 64>(a, device, st) : launch_decode4<float, 128>(a, device, st);
+  cudaError_t (*launch)(const DecodeArgs&, int, cudaStream_t);
+  if (p.dtype != GBS_BF16) launch = p.d == 64 ? launch_decode4<float, 64, true> : launch_decode4<float, 128, true>;
+  else if (!a.grouped || p.G == 1) launch = p.d == 64 ? launch_decode4<__nv_bfloat16, 64, true> : launch_decode4<__nv_bfloat16, 128, true>;
+  else launch = p.d == 64 ? launch_decode4<__nv_bfloat16, 64, false> : launch_decode4<__nv_bfloat16, 128, false>;
+  e = launch(a, device, st);
   return cuda_done(e, "gbs_kv4_decode");
 }
