@@ -911,6 +911,11 @@ constexpr float kLift = 10.f, kRoom = 14.f;
 // A nibble alone is the fp16 of its code times 2^-24 (low in its byte) or 2^-20 (high):
 // products take it as it is, exactly, and the power of two goes into what it meets.
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+// Value products take whole bytes, low + 16 high, beside the high nibbles, which are
+// subtracted from the sums at the end: an instruction less for the upper bytes of a word
+// (sums of up to 17 times the low nibbles' in fp32, whose steps stay below 2^-18 of them).
+constexpr uint32_t kByte = 0x00ff00ffu;
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
 
 // c = a b, and c += a b
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -1275,10 +1280,10 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
           const uint32_t ps = as_word(__hmul2(as_half2(pw), as_half2(sc)));
 #pragma unroll
           for (int P = 0; P < NP; ++P) {
-            const uint32_t w0 = vw[0][P], w1 = vw[1][P], h0 = w0 >> 8, h1 = w1 >> 8;
+            const uint32_t w0 = vw[0][P], w1 = vw[1][P], h0 = upper_bytes(w0), h1 = upper_bytes(w1);
             const uint32_t b0 = __byte_perm(ps, 0u, lo_to[P]), b1 = __byte_perm(ps, 0u, hi_to[P]);
-            mma16816_add(o[0], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
-            mma16816_add(o[1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
+            mma16816_add(o[0], w0 & kByte, w0 & kHigh, w1 & kByte, w1 & kHigh, b0, b1);
+            mma16816_add(o[1], h0, h0 & kHigh, h1, h1 & kHigh, b0, b1);
           }
         }
       } else {
@@ -1384,12 +1389,12 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
             const uint32_t p0 = __byte_perm(pb[v], 0u, sel0), p1 = __byte_perm(pb[v], 0u, sel1);
 #pragma unroll
             for (int P = 0; P < NP; ++P) {
-              const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
+              const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = upper_bytes(w0), h1 = upper_bytes(w1);
               const int at = r * Tile::PB + 8 * P;
               const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
               const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
-              mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
-              mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
+              mma16816_add(o[2 * P], w0 & kByte, w0 & kHigh, w1 & kByte, w1 & kHigh, b0, b1);
+              mma16816_add(o[2 * P + 1], h0, h0 & kHigh, h1, h1 & kHigh, b0, b1);
             }
           }
         }
@@ -1412,8 +1417,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       for (int c = 0; c < 2; ++c) {
         const float least = t == 0 ? om[c] : om[2 + c];
         *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + 32 * (2 * t + c) + 4 * g) =
-            make_float4(fmaf(o[0][c], 0x1p24f, least), fmaf(o[0][2 + c], 0x1p20f, least),
-                        fmaf(o[1][c], 0x1p24f, least), fmaf(o[1][2 + c], 0x1p20f, least));
+            make_float4(fmaf(o[0][c] - o[0][2 + c], 0x1p24f, least), fmaf(o[0][2 + c], 0x1p20f, least),
+                        fmaf(o[1][c] - o[1][2 + c], 0x1p24f, least), fmaf(o[1][2 + c], 0x1p20f, least));
       }
     if (lane == 0) {
       s_m[warp][0] = m[0];
@@ -1437,8 +1442,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
 #pragma unroll
         for (int P = 0; P < NP; ++P)
           *reinterpret_cast<float4*>(sum + 64 * P) =
-              make_float4(fmaf(o[2 * P][c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
-                          fmaf(o[2 * P + 1][c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
+              make_float4(fmaf(o[2 * P][c] - o[2 * P][2 + c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
+                          fmaf(o[2 * P + 1][c] - o[2 * P + 1][2 + c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
         if (g == 0 && t < 2) {
           s_m[warp][hc + c] = m[c];
           s_l[warp][hc + c] = l[c];
