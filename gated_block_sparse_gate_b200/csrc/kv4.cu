@@ -331,6 +331,7 @@ struct DecodeArgs {
   void* O;
   float* LSE;
   int grouped, splits;
+  int inbox;  // with splits: where an Inbox lies in a CTA's dynamic shared memory
 };
 
 __device__ __forceinline__ int sequence_length(const DecodeArgs& a, int b) {
@@ -718,28 +719,48 @@ __device__ __forceinline__ Kept kept_blocks(const DecodeArgs& a, int srow, int c
   return r;
 }
 
-// Joins the splits of a row, which are a cluster: each CTA's sums of n channels (joined) and
-// (maximum, sum) of each head of D channels are in its shared memory; the first of them goes to
-// output element `out`. A row without a key (a length of 0) gives 0 and -infinity.
+// The splits of a row are a cluster and join their sums of n = heads * D channels: every
+// CTA writes each 128 of its sums into the memory of the CTA that joins these 128, and the
+// (maximum, sum) of the heads in them, so that after one barrier all reads are local (reading
+// the others' memory, with a barrier on both sides, took about 1 us longer).
+struct Inbox {
+  float sums[kMaxCluster * 128];  // of split r, its x-th 128 of this CTA: at (x * splits + r) * 128
+  float2 ml[kMaxCluster][4];
+};
+static_assert(sizeof(Inbox) % 16 == 0, "");
+__device__ __forceinline__ void cluster_arrive_early() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Channel i's sum v, and its head's maximum M and sum l, to the CTA that joins it.
+template <int D>
+__device__ __forceinline__ void send_sum(const DecodeArgs& a, Inbox* inbox, int split, int i, float v, float M, float l) {
+  const int chunk = i / 128;
+  Inbox* to = cooperative_groups::this_cluster().map_shared_rank(inbox, chunk % a.splits);
+  to->sums[(chunk / a.splits * a.splits + split) * 128 + i % 128] = v;
+  if (i % D == 0) to->ml[split][i / D] = make_float2(M, l);
+}
+
+// The joined sums to output elements row0 * D + i. A row without a key (a length of 0) gives
+// 0 and -infinity.
 template <typename T, int D>
-__device__ __forceinline__ void join_splits(const DecodeArgs& a, float* joined, float2* ml, int n, int split, size_t row0) {
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  for (int i = split * 128 + threadIdx.x; i < n; i += a.splits * 128) {
+__device__ __forceinline__ void join_splits(const DecodeArgs& a, const Inbox* inbox, int n, int split, size_t row0) {
+  cluster_arrive();
+  cluster_wait();
+  for (int i = split * 128 + threadIdx.x, x = 0; i < n; i += a.splits * 128, ++x) {
     const int h = i / D;
     float M = -INFINITY, l = 0.f, v = 0.f;
-    for (int r = 0; r < a.splits; ++r) M = fmaxf(M, cluster.map_shared_rank(ml, r)[h].x);
+    for (int r = 0; r < a.splits; ++r) M = fmaxf(M, inbox->ml[r][h].x);
+#pragma unroll 4
     for (int r = 0; r < a.splits; ++r) {
-      const float2 x = cluster.map_shared_rank(ml, r)[h];
-      const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - M);
-      l += x.y * f;
-      v += cluster.map_shared_rank(joined, r)[i] * f;
+      const float2 ml = inbox->ml[r][h];
+      const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
+      l += ml.y * f;
+      v += inbox->sums[(x * a.splits + r) * 128 + i % 128] * f;
     }
     store_out(reinterpret_cast<T*>(a.O) + row0 * D + i, l == 0.f ? 0.f : v / l);
     if (i % D == 0) a.LSE[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * GBS_LN2;
   }
-  cluster.sync();  // the others have read this CTA's sums
 }
 
 // fp32 queries: one query head and split per CTA, all in fp32, so queries keep their 24
@@ -749,14 +770,16 @@ __device__ __forceinline__ void join_splits(const DecodeArgs& a, float* joined, 
 template <typename T, int D>
 __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int NG = D / 32, LANES = NG, ROWS = 128 / LANES;
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem);
   __shared__ SelectScratch select;
   __shared__ float s_acc[4][D], s_m[4], s_l[4];
-  __shared__ float2 s_join;
   const Problem& p = a.p;
   const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, split = blockIdx.y, kvh = hq / p.G;
   const int srow = a.grouped ? b * p.Hkv + kvh : blockIdx.x;
   const int lane = threadIdx.x % LANES, row_in = threadIdx.x / LANES;
+  Inbox* inbox = reinterpret_cast<Inbox*>(reinterpret_cast<char*>(s_keys) + a.inbox);
+  if (a.splits > 1) cluster_arrive_early();
   const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
   const Kept kept = kept_blocks(a, srow, cur, s_keys, select);
   const int n_hist = kept.n;
@@ -844,17 +867,15 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
     ll += s_l[w] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
   }
   const size_t row = (size_t)b * p.Hq + hq;
+  if (a.splits > 1) cluster_wait();  // every CTA of the row has begun
   for (int c = threadIdx.x; c < D; c += 128) {
     float v = 0.f;
     for (int w = 0; w < 4; ++w) v += s_acc[w][c] * (s_m[w] == -INFINITY ? 1.f : fw[w]);
-    if (a.splits > 1) s_acc[0][c] = v;  // (column c is this thread's alone)
+    if (a.splits > 1) send_sum<D>(a, inbox, split, c, v, MM, ll);
     else store_out(reinterpret_cast<T*>(a.O) + row * D + c, ll == 0.f ? 0.f : v / ll);
   }
-  if (threadIdx.x == 0) {
-    s_join = make_float2(MM, ll);
-    if (a.splits == 1) a.LSE[row] = ll == 0.f ? -INFINITY : (MM + log2f(ll)) * GBS_LN2;
-  }
-  if (a.splits > 1) join_splits<T, D>(a, s_acc[0], &s_join, D, split, row);
+  if (a.splits > 1) join_splits<T, D>(a, inbox, D, split, row);
+  else if (threadIdx.x == 0) a.LSE[row] = ll == 0.f ? -INFINITY : (MM + log2f(ll)) * GBS_LN2;
 }
 
 // ------------------------------------------------------------ tensor-core decode
@@ -899,7 +920,7 @@ struct Kv4Tile {
   static constexpr int kStage = kVp + kUnit * PB;
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kWarp = kStages * kStage, kBytes = 4 * kWarp;
-  static_assert(kWarp >= 8 * D * 4, "a warp's sums, and the CTA's behind warp 0's, go into its stages' memory");
+  static_assert(kWarp >= 4 * D * 4, "a warp's sums go into its stages' memory");
   static_assert(kBytes >= 4 * 8192, "a row's keys are held in the stages' memory before copies begin");
 };
 constexpr int kMmaThreads = 128;
@@ -977,7 +998,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   __shared__ float bias_all[4][S], s_m[4][4], s_l[4][4];
   __shared__ int rows_all[4][S], s_abort;
   __shared__ SelectScratch select;
-  __shared__ float2 s_join[4];
+  Inbox* inbox = reinterpret_cast<Inbox*>(smem + a.inbox);
+  if (a.splits > 1) cluster_arrive_early();
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* full = full_all[warp];
@@ -1451,8 +1473,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       }
   }
   __syncthreads();
-  // the warps' sums as one; the splits of a row are a cluster and meet in shared memory
-  float* joined = reinterpret_cast<float*>(smem) + 4 * D;
+  // the warps' sums as one
+  if (a.splits > 1) cluster_wait();  // every CTA of the row has begun
   for (int i = threadIdx.x; i < nh * D; i += kMmaThreads) {
     const int h = i / D;
     float M = -INFINITY, sum = 0.f, v = 0.f;
@@ -1465,15 +1487,14 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       v += reinterpret_cast<const float*>(smem + w * Tile::kWarp)[i] * f;
     }
     if (a.splits > 1) {
-      joined[i] = v;
-      if (i % D == 0) s_join[h] = make_float2(M, sum);
+      send_sum<D>(a, inbox, split, i, v, M, sum);
     } else if (!s_abort) {  // (a wait that ran out is reported in the error word)
       const size_t row = (size_t)b * p.Hq + h0 + h;
       reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + i % D] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
       if (i % D == 0) a.LSE[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * GBS_LN2;
     }
   }
-  if (a.splits > 1) join_splits<__nv_bfloat16, D>(a, joined, s_join, nh * D, split, (size_t)b * p.Hq + h0);
+  if (a.splits > 1) join_splits<__nv_bfloat16, D>(a, inbox, nh * D, split, (size_t)b * p.Hq + h0);
 }
 
 // CTA rows of the tensor-core decode: selection rows, times slices of four heads.
@@ -1511,7 +1532,7 @@ cudaError_t sm_count(int device, int* sms) {
 
 // One launch: rows x splits CTAs, the splits of a row a cluster.
 template <typename T, int D, bool ONE>
-cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
+cudaError_t launch_decode4(DecodeArgs& a, int device, cudaStream_t st) {
   constexpr bool kMma = sizeof(T) == 2;
   void (*kernel)(DecodeArgs);
   size_t smem;
@@ -1522,11 +1543,15 @@ cudaError_t launch_decode4(const DecodeArgs& a, int device, cudaStream_t st) {
     kernel = kv4_decode_simt_kernel<T, D>;
     smem = a.S ? 4 * (size_t)(a.p.Nb > kSelectWork ? a.p.Nb : kSelectWork) : 0;
   }
+  a.inbox = (int)((smem + 15) / 16 * 16);
+  constexpr int kMost = kMma ? Kv4Tile<D>::kBytes : 4 * (kSelectMax + 4);
+  if (a.splits > 1) smem = a.inbox + sizeof(Inbox);
   cudaError_t e;
   static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use large clusters and its memory
   if (device >= 64 || !(ready.load(std::memory_order_acquire) >> device & 1)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && kMma) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost + (int)sizeof(Inbox));
     if (e != cudaSuccess) return e;
     if (device < 64) ready.fetch_or(1ull << device, std::memory_order_release);
   }
@@ -1725,7 +1750,7 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   if (a.splits == 0) a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms);
   if (a.splits > n_ent) a.splits = n_ent;
   if (a.splits > kMaxCluster) a.splits = kMaxCluster;
-  cudaError_t (*launch)(const DecodeArgs&, int, cudaStream_t);
+  cudaError_t (*launch)(DecodeArgs&, int, cudaStream_t);
   if (p.dtype != GBS_BF16) launch = p.d == 64 ? launch_decode4<float, 64, true> : launch_decode4<float, 128, true>;
   else if (!a.grouped || p.G == 1) launch = p.d == 64 ? launch_decode4<__nv_bfloat16, 64, true> : launch_decode4<__nv_bfloat16, 128, true>;
   else launch = p.d == 64 ? launch_decode4<__nv_bfloat16, 64, false> : launch_decode4<__nv_bfloat16, 128, false>;
