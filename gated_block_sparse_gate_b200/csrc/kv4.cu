@@ -1502,17 +1502,28 @@ int decode4_rows(const DecodeArgs& a) {
   return a.grouped ? a.p.B * a.p.Hkv * ((a.p.G + 3) / 4) : a.p.B * a.p.Hq;
 }
 
-// Splits of every CTA row's n_ent blocks. A CTA costs its share and about twelve blocks'
-// worth of selection, beginning and end; while all CTAs fit on the GPU at once the largest
-// share is what counts, beyond that their number (64 x 131072, K = 32: 2048 rows take
-// 142 us with 1 split, 184 with 2, 512 rows 47 and 60; 102 rows of 49 blocks with d = 64
-// take 29 us with 1, 23 with 2, 19 with 4, 27 with 8).
-int decode4_splits(int rows, int n_ent, int slots) {
+// Splits of every CTA row's n_ent blocks, by a model of the call's time in blocks of a CTA
+// that has an SM to itself. A CTA's selection, beginning and end take as long as 36 blocks
+// (fp32 queries, whose blocks take four times as long: 6); where four CTAs share an SM,
+// their blocks take twice (3 times) as long, and their beginnings and ends count as 12 (2)
+// blocks more. The two meet as the root of the sum of squares. Beyond 7/8 of the places, the
+// clusters of a row no longer all find places at once, so half a round more is counted.
+// Microseconds at 1, 2, 4, 6, 8, 16 splits, the rule's own in brackets:
+//   32 rows of 17 blocks    13.8 11.7 9.6 [8.9] 8.7 12.5
+//   64 rows of 33, shared   24.3 18.1 15.0 14.0 15.3 32.3, [15.1] at 5
+//   128 rows of 33          22.2 18.3 17.4 23.7 25.0 46.4, [17.0] at 3
+//   192 rows of 33, shared  28.7 [23.2] 31.0 37.4 41.0 76.9
+//   512 rows of 33          [37.3] 45.2 60.1 71.7 90.4 172
+//   102 rows of 49, d = 64  23.5 18.8 [15.6] 17.6 21.8 33.3
+//   128 rows of 17, fp32    30.6 21.7 20.0 23.7 26.8 45.4, [19.1] at 3
+int decode4_splits(int rows, int n_ent, int slots, bool fp32) {
+  const float ends = fp32 ? 6.f : 36.f, crowd = fp32 ? 3.f : 2.f, more = fp32 ? 2.f : 12.f;
   int best = 1;
   float least = 0.f;
   for (int s = 1; s <= n_ent && s <= kMaxCluster; ++s) {
-    const float load = (float)rows * s / slots;
-    const float cost = (load <= 1.f ? 1.f : load + 0.5f) * ((n_ent + s - 1) / s + 12);
+    const float share = (float)((n_ent + s - 1) / s), load = (float)rows * s / slots;
+    const float alone = share + ends, full = (load <= 0.875f ? load : load + 0.5f) * crowd * (share + more);
+    const float cost = alone * alone + full * full;
     if (s == 1 || cost < least) {
       best = s;
       least = cost;
@@ -1747,7 +1758,7 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   }
   const int n_ent = (p.topk < cur_max ? p.topk : cur_max) + 1;
   a.splits = num_splits;
-  if (a.splits == 0) a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms);
+  if (a.splits == 0) a.splits = decode4_splits(p.dtype == GBS_BF16 ? decode4_rows(a) : p.B * p.Hq, n_ent, 4 * sms, p.dtype != GBS_BF16);
   if (a.splits > n_ent) a.splits = n_ent;
   if (a.splits > kMaxCluster) a.splits = kMaxCluster;
   cudaError_t (*launch)(DecodeArgs&, int, cudaStream_t);
