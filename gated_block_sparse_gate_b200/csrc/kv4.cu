@@ -899,19 +899,23 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 // through a product together: its eight columns are four heads times the two groups of a
 // pair, column c with zeros where the other group's factor would be. So codes need
 // nothing but masks and one shift, the accumulators have no padding but unused heads, and
-// the two groups' logits meet in one exchange between lanes.
+// the two groups' logits meet in one exchange between lanes. A CTA of one head takes groups
+// as columns instead (ONE below).
 //
-// Bytes would bound it (64 sequences x 131072, K = 32, d = 128: 679 MB that differ, 104 us
-// at the copy rate, and the kernel's copies alone take that); instructions do, about 1,300
-// of a warp for 64 keys, most of them masks, factors and the softmax (issue 0.65 a clock, ALU
-// pipe 58%, tensor pipe 18%). Measured: 142 us (4.8 TB/s) with a selection for each head,
-// 47 us (178 MB, floor 27) with one for four heads. Steps, calls per head / shared: one key a
-// thread in fp32 393 / 371 us, products with heads as rows 299 / 101, keys and channels as
-// rows 208 / 73, raw nibbles and a ring for each warp 189 / 70, both groups of a pair as
-// columns 173 / 65, selection and join inside 157 / 50, one path for all scales 148 / 50,
-// one warp ending the selection 145 / 48. Other shapes of it, each against its time's
-// kernel: three CTAs an SM 178 / 74 (161 / 54), five with 96 registers 157 / 58 (148 / 51),
-// three stages a warp 156 / 63 (141 / 47), the loop over channels rolled 167 / 57 (151 / 53).
+// Bound with a selection for each head by memory and the beginnings of its CTAs (64 sequences
+// x 131072, K = 32, d = 128: 679 MB that differ, 104 us at the copy rate): 126 us (5.4 TB/s),
+// of which the products and softmaxes add 13 to the copies and selections alone (112, in which
+// the first CTAs of all SMs select before anything is copied). With one for four heads: 44 us
+// (178 MB, 27 us), the copies alone 31, selections 4, the rest instructions: about 1,300 of a
+// warp for 64 keys, most of them masks, factors and the softmax. Steps, calls per head /
+// shared: one key a thread in fp32 393 / 371 us, products with heads as rows 299 / 101, keys
+// and channels as rows 208 / 73, raw nibbles and a ring for each warp 189 / 70, both groups of
+// a pair as columns 173 / 65, selection and join inside 157 / 50, one path for all scales
+// 148 / 50, one warp ending the selection 142 / 47, one head a kernel of its own 128 / 46,
+// whole bytes as operands 126 / 45. Other shapes of it, each against its time's kernel: three
+// CTAs an SM 178 / 74 (161 / 54), five with 96 registers 157 / 58 (148 / 51) and, of one head,
+// 131 (127), three stages a warp 156 / 63 (141 / 47), the loop over channels rolled 167 / 57
+// (151 / 53).
 constexpr int kUnit = 32;  // keys of a warp's turn
 template <int D>
 struct Kv4Tile {
