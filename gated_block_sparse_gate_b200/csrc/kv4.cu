@@ -427,8 +427,8 @@ __device__ __forceinline__ float keep_largest(const uint32_t (&v)[N], int n, int
                                               SelectScratch& sc, Index idx) {
   const int lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
-  int left, out = 0;
-  const uint32_t T = warp_threshold(v, k, 1 << 20, &left);
+  int left = 0, out = 0;
+  const uint32_t T = k < n ? warp_threshold(v, k, 1 << 20, &left) : 0u;  // (all of them are above 0)
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
