@@ -889,10 +889,11 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 // The inner sums are m16n8k16 products of codes (rows: keys) and q as fp16, both exact: q
 // is scaled by a power of two for each head so that it fits, scales are applied to the
 // fp32 sums, and the minima's part is one more product, of the raw parameter words with
-// the sums of q as two fp16 terms.
+// the sums of q as two fp16 terms, which leaves 2^-23 of them: less than fp32 sums do.
 //   O[channel, head] = sum_key n (s p) + sum_key m p
-// with codes as rows again, p and s p rounded to fp16 (2^-11 each, against the 2^-8 of
-// the bf16 result) and sums in fp32.
+// with codes as rows again. Weights p and products s p go in as two fp16 terms each, which
+// leaves 2^-21 of them, and sums are fp32: with one term (2^-12) one result in seven was a
+// bf16 step beside the nearest, with two one in a hundred.
 //
 // A nibble masked out of a 32-bit word of codes stands for an fp16 pair as it is (kLow,
 // kHigh below), one from a group 2 P (low half) and one from group 2 P + 1. Both go
@@ -903,16 +904,18 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
 // as columns instead (ONE below).
 //
 // Bound with a selection for each head by memory and the beginnings of its CTAs (64 sequences
-// x 131072, K = 32, d = 128: 679 MB that differ, 104 us at the copy rate): 126 us (5.4 TB/s),
-// of which the products and softmaxes add 13 to the copies and selections alone (112, in which
-// the first CTAs of all SMs select before anything is copied). With one for four heads: 44 us
-// (178 MB, 27 us), the copies alone 31, selections 4, the rest instructions: about 1,300 of a
-// warp for 64 keys, most of them masks, factors and the softmax. Steps, calls per head /
+// x 131072, K = 32, d = 128: 679 MB that differ, 104 us at the copy rate): 131 us (5.2 TB/s),
+// of which the products and softmaxes add 18 to the copies and selections alone (112, in which
+// the first CTAs of all SMs select before anything is copied). With one for four heads: 53 us
+// (178 MB, 27 us), the copies alone 31, selections 4, the rest instructions, most of them
+// masks, factors and the softmax; the second terms take 8 (the products of them 1.4, the
+// making of them the rest). Steps, calls per head /
 // shared: one key a thread in fp32 393 / 371 us, products with heads as rows 299 / 101, keys
 // and channels as rows 208 / 73, raw nibbles and a ring for each warp 189 / 70, both groups of
 // a pair as columns 173 / 65, selection and join inside 157 / 50, one path for all scales
 // 148 / 50, one warp ending the selection 142 / 47, one head a kernel of its own 128 / 46,
-// whole bytes as operands 126 / 45. Other shapes of it, each against its time's kernel: three
+// whole bytes as operands 126 / 45, second terms of weights and products 129 / 52, nibbles apart
+// again 131 / 53. Other shapes of it, each against its time's kernel: three
 // CTAs an SM 178 / 74 (161 / 54), five with 96 registers 157 / 58 (148 / 51) and, of one head,
 // 131 (127), three stages a warp 156 / 63 (141 / 47), the loop over channels rolled 167 / 57
 // (151 / 53).
@@ -936,11 +939,9 @@ constexpr float kLift = 10.f, kRoom = 14.f;
 // A nibble alone is the fp16 of its code times 2^-24 (low in its byte) or 2^-20 (high):
 // products take it as it is, exactly, and the power of two goes into what it meets.
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-// Value products take whole bytes, low + 16 high, beside the high nibbles, which are
-// subtracted from the sums at the end: an instruction less for the upper bytes of a word
-// (sums of up to 17 times the low nibbles' in fp32, whose steps stay below 2^-18 of them).
-constexpr uint32_t kByte = 0x00ff00ffu;
-__device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
+// (Whole bytes, low + 16 high, less the high nibbles at the end took an instruction less for
+// the upper bytes of a word, 2 us of 131, but their sums are 17 times as large at equal codes
+// and 241 times at 1 beside 15, and so are the steps of fp32: one low channel in ten was off.)
 
 // c = a b, and c += a b
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -959,6 +960,19 @@ __device__ __forceinline__ void mma16816_add(float (&c)[4], uint32_t a0, uint32_
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
 __device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return as_word(__floats2half2_rn(lo, hi)); }
+// What fp16 leaves of lo and hi, as fp16: *two gets their first terms.
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t* two) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  const float2 f = __half22float2(h);
+  *two = as_word(h);
+  return pack_half2(lo - f.x, hi - f.y);
+}
+// The product of (p + rest) and s as two fp16 terms: p s - top is exact (in steps of 2^-24).
+__device__ __forceinline__ uint32_t product_rest(uint32_t p, uint32_t rest, uint32_t s, uint32_t* top) {
+  const __half2 x = __hmul2(as_half2(p), as_half2(s));
+  *top = as_word(x);
+  return as_word(__hfma2(as_half2(rest), as_half2(s), __hfma2(as_half2(p), as_half2(s), __hneg2(x))));
+}
 
 // The transpose of an 8 x 8 matrix of fp16: a lane's word is row lane / 4, columns 2 (lane % 4) and the next.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
@@ -1105,8 +1119,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       mx = fmaxf(mx, fabsf(v[i]));
     }
   };
-  // channel i of eight: nibble i % 4 of the lane's word i / 4. High nibbles count 16 times;
-  // of q, that rounds only what is below 2^-15 of its largest
+  // channel i of eight: nibble i % 4 of the lane's word i / 4. High nibbles count 16 times; of
+  // q, whose largest is 2^8 or more, that rounds only steps below 2^-20: 2^-29 of the largest
   auto operand = [&](float v, int i, float& sum) {
     const __half x = __float2half_rn(v * down0 * down1);
     sum += __half2float(x);
@@ -1292,24 +1306,27 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
         l[0] += pr;
 #pragma unroll
         for (int k = 0; k < NG; ++k) om[k] = fmaf(pr, high_half(vp[k]), om[k]);
-        // weights as fp16, of product rows 2 t and 2 t + 1 of each eight keys, in every column
+        // weights as two fp16 terms, of product rows 2 t and 2 t + 1 of each eight keys, in every
+        // column: columns 0 to 3 take the products' first terms, 4 to 7 the rest
         const float other = __shfl_xor_sync(0xffffffffu, pr, 4);
-        const uint32_t two = g & 1 ? pack_half2(other, pr) : pack_half2(pr, other);
+        uint32_t two;
+        const uint32_t rest = pack_rest(g & 1 ? other : pr, g & 1 ? pr : other, &two);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t pw = __shfl_sync(0xffffffffu, two, 8 * t + e);
+          const uint32_t pw = __shfl_sync(0xffffffffu, two, 8 * t + e), pl = __shfl_sync(0xffffffffu, rest, 8 * t + e);
           uint32_t vw[2][NP];
           load_words<NP>(lv0, 8 * e * Tile::RB, vw[0]);
           load_words<NP>(lv1, 8 * e * Tile::RB, vw[1]);
           const uint32_t sc = __byte_perm(load_word(lvp0 + 4 * group, 8 * e * Tile::PB),
                                           load_word(lvp1 + 4 * group, 8 * e * Tile::PB), 0x5410);
-          const uint32_t ps = as_word(__hmul2(as_half2(pw), as_half2(sc)));
+          uint32_t top;
+          const uint32_t low = product_rest(pw, pl, sc, &top), ps = g >> 2 ? low : top;
 #pragma unroll
           for (int P = 0; P < NP; ++P) {
-            const uint32_t w0 = vw[0][P], w1 = vw[1][P], h0 = upper_bytes(w0), h1 = upper_bytes(w1);
+            const uint32_t w0 = vw[0][P], w1 = vw[1][P], h0 = w0 >> 8, h1 = w1 >> 8;
             const uint32_t b0 = __byte_perm(ps, 0u, lo_to[P]), b1 = __byte_perm(ps, 0u, hi_to[P]);
-            mma16816_add(o[0], w0 & kByte, w0 & kHigh, w1 & kByte, w1 & kHigh, b0, b1);
-            mma16816_add(o[1], h0, h0 & kHigh, h1, h1 & kHigh, b0, b1);
+            mma16816_add(o[0], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
+            mma16816_add(o[1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
           }
         }
       } else {
@@ -1386,13 +1403,15 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          uint32_t pb[2];  // head g, keys of the columns 2 t and 2 t + 1
+          uint32_t pb[2], pl[2];  // head g, keys of the columns 2 t and 2 t + 1: both terms
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const float p0 = fast_exp2(x[y][2 * v]), p1 = fast_exp2(x[y][2 * v + 1]);
             l[0] += p0;
             l[1] += p1;
-            pb[v] = transpose8x8(pack_half2(p0, p1));
+            const uint32_t rest = pack_rest(p0, p1, &pb[v]);
+            pb[v] = transpose8x8(pb[v]);
+            pl[v] = transpose8x8(rest);
           }
           uint32_t vw[2][2][NP];  // of keys row_v0 and row_v1: four channels g of both groups of a pair
 #pragma unroll
@@ -1409,18 +1428,23 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
               mi[v] = __byte_perm(load_word(lvp0 + 4 * g, r * Tile::PB), load_word(lvp1 + 4 * g, r * Tile::PB), 0x7632);
             }
           mma16816_add(om, mi[0], 0u, mi[1], 0u, pb[0], pb[1]);
+          mma16816_add(om, mi[0], 0u, mi[1], 0u, pl[0], pl[1]);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int r = 16 * y + 8 * v;
-            const uint32_t p0 = __byte_perm(pb[v], 0u, sel0), p1 = __byte_perm(pb[v], 0u, sel1);
 #pragma unroll
             for (int P = 0; P < NP; ++P) {
-              const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = upper_bytes(w0), h1 = upper_bytes(w1);
+              const uint32_t w0 = vw[v][0][P], w1 = vw[v][1][P], h0 = w0 >> 8, h1 = w1 >> 8;
               const int at = r * Tile::PB + 8 * P;
-              const uint32_t b0 = as_word(__hmul2(as_half2(p0), __low2half2(as_half2(load_word(lvp0 + par_v, at)))));
-              const uint32_t b1 = as_word(__hmul2(as_half2(p1), __low2half2(as_half2(load_word(lvp1 + par_v, at)))));
-              mma16816_add(o[2 * P], w0 & kByte, w0 & kHigh, w1 & kByte, w1 & kHigh, b0, b1);
-              mma16816_add(o[2 * P + 1], h0, h0 & kHigh, h1, h1 & kHigh, b0, b1);
+              const uint32_t sc = __byte_perm(load_word(lvp0 + par_v, at), load_word(lvp1 + par_v, at), 0x5410);
+              uint32_t top;
+              const uint32_t low = product_rest(pb[v], pl[v], sc, &top);
+              const uint32_t b0 = __byte_perm(top, 0u, sel0), b1 = __byte_perm(top, 0u, sel1);
+              const uint32_t c0 = __byte_perm(low, 0u, sel0), c1 = __byte_perm(low, 0u, sel1);
+              mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, b0, b1);
+              mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, b0, b1);
+              mma16816_add(o[2 * P], w0 & kLow, w0 & kHigh, w1 & kLow, w1 & kHigh, c0, c1);
+              mma16816_add(o[2 * P + 1], h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, c0, c1);
             }
           }
         }
@@ -1438,13 +1462,16 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     l[0] = warp_sum(l[0]);
 #pragma unroll
     for (int k = 0; k < NG; ++k) om[k] = warp_sum(om[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // both terms' sums, of columns c and c + 4
+      o[i >> 2][i & 3] += __shfl_xor_sync(0xffffffffu, o[i >> 2][i & 3], 2);
     if (t < NP)  // the columns of groups 2 t and 2 t + 1
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float least = t == 0 ? om[c] : om[2 + c];
         *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + 32 * (2 * t + c) + 4 * g) =
-            make_float4(fmaf(o[0][c] - o[0][2 + c], 0x1p24f, least), fmaf(o[0][2 + c], 0x1p20f, least),
-                        fmaf(o[1][c] - o[1][2 + c], 0x1p24f, least), fmaf(o[1][2 + c], 0x1p20f, least));
+            make_float4(fmaf(o[0][c], 0x1p24f, least), fmaf(o[0][2 + c], 0x1p20f, least),
+                        fmaf(o[1][c], 0x1p24f, least), fmaf(o[1][2 + c], 0x1p20f, least));
       }
     if (lane == 0) {
       s_m[warp][0] = m[0];
@@ -1468,8 +1495,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
 #pragma unroll
         for (int P = 0; P < NP; ++P)
           *reinterpret_cast<float4*>(sum + 64 * P) =
-              make_float4(fmaf(o[2 * P][c] - o[2 * P][2 + c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
-                          fmaf(o[2 * P + 1][c] - o[2 * P + 1][2 + c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
+              make_float4(fmaf(o[2 * P][c], 0x1p24f, least[P][c]), fmaf(o[2 * P][2 + c], 0x1p20f, least[P][c]),
+                          fmaf(o[2 * P + 1][c], 0x1p24f, least[P][c]), fmaf(o[2 * P + 1][2 + c], 0x1p20f, least[P][c]));
         if (g == 0 && t < 2) {
           s_m[warp][hc + c] = m[c];
           s_l[warp][hc + c] = l[c];
