@@ -707,6 +707,12 @@ struct Kept {
   const float* gate;  // log gates: gate[e] - lse
   float lse;
 };
+// The log gate of kept block e in powers of two. It stays finite, so that a maximum made of it
+// does: a score of fp32's lowest, as masks have, would give -infinity (a weight of 0 either way).
+__device__ __forceinline__ float log2_gate(const Kept& kept, int e) {
+  const float x = (kept.gate[e] - kept.lse) * GBS_LOG2E;
+  return x < -1e30f ? -1e30f : x;
+}
 __device__ __forceinline__ Kept kept_blocks(const DecodeArgs& a, int srow, int cur, uint32_t* keys, SelectScratch& sc) {
   Kept r = {0, sc.idx, sc.score, 0.f};
   if (a.S) {
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
   for (int e = e0; e < e1; ++e) {
     const bool is_cur = e == n_hist;
     const int c = is_cur ? cur : dcheck(kept.idx[e], 0, cur - 1, a.c.err);
-    const float bias = is_cur ? 0.f : (kept.gate[e] - kept.lse) * GBS_LOG2E;
+    const float bias = is_cur ? 0.f : log2_gate(kept, e);
     const long long row0 = block_row(a, b, kvh, c);
     if (row0 < 0) continue;
     const int nrows = is_cur ? L - cur * kBS : kBS;
@@ -1075,7 +1081,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     if (turn < turns) {
       const bool is_cur = e == n_hist;
       const int c = is_cur ? cur : dcheck(kept.idx[e], 0, cur - 1, a.c.err);
-      my_bias = is_cur ? 0.f : (kept.gate[e] - kept.lse) * GBS_LOG2E;
+      my_bias = is_cur ? 0.f : log2_gate(kept, e);
       const long long row = block_row(a, b, kvh, c);
       my_unit = (int)(row / kUnit) + (warp & 1);
       my_rows = row < 0 ? 0 : min(kUnit, is_cur ? L - cur * kBS - half : kUnit);

@@ -1,0 +1,38 @@
+"""Scores at the ends of fp32's range, as masks make them: the decode over a 4-bit cache gives the definition's result.
+
+Tolerances are those of tests/test_gpu_kv4.py (_check).
+"""
+import pytest
+import torch
+
+from gated_block_sparse_gate_b200 import binding as gb
+from gated_block_sparse_gate_b200.build import build
+from tests.test_gpu_kv4 import _check, _decode_case
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+LOWEST = torch.finfo(F32).min
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build()
+    gb.load_library()
+
+
+@pytest.mark.parametrize("splits", [1, 3, 0])
+@pytest.mark.parametrize("dtype,shared", [(BF, False), (BF, True), (F32, False)])
+@pytest.mark.parametrize("masked", [[0], [0, 1, 2, 3], [0, 5, 9], [4, 12]])
+def test_blocks_masked_by_the_lowest_score(masked, dtype, shared, splits):
+    """All blocks are kept, the masked ones with a weight of 0, wherever they come first."""
+    x = _decode_case(sum(masked), 2, 8, 2, 128, 900, [900, 870], shared, dtype)
+    x["S"][..., masked] = LOWEST
+    _check(x, 900, 20, shared, splits=splits)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_masked_blocks_in_the_longest_rows(dtype):
+    """Rows that are selected from before the decode: five blocks that are not masked, fifteen that are."""
+    x = _decode_case(3, 1, 2, 1, 64, 530000, None, True, dtype, paged=False)
+    x["S"][..., [i for i in range(x["S"].shape[-1]) if i % 1700 != 1]] = LOWEST
+    _check(x, 530000, 20, True)
