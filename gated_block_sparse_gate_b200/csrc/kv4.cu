@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ R
 struct DecodeArgs {
   Problem p;
   Kv4 c;
-  const float* S;  // scores, where the kernel selects for itself; else null and
-  Selection sel;   // the selection's lists
+  const float* S;  // scores
+  Selection sel;   // lists of a selection made before; null where the kernel selects for itself
   const int32_t* seq_lens;
   const void* q;
   void* O;
@@ -421,7 +421,7 @@ static_assert(128 + 2 * kCandidates <= kSelectWork, "");
 
 // The end of a selection, by a warp whose lane l holds keys l, l + 32, ... of n: of the k
 // largest, idx(j) of the j-th key and its score go to sc where `write`; returns the
-// logarithm of the sum of their exponentials (top: the largest score).
+// logarithm of the sum of their exponentials over that of the largest score, top.
 template <int N, typename Index>
 __device__ __forceinline__ float keep_largest(const uint32_t (&v)[N], int n, int k, float top, bool write,
                                               SelectScratch& sc, Index idx) {
@@ -448,12 +448,20 @@ __device__ __forceinline__ float keep_largest(const uint32_t (&v)[N], int n, int
     out += __popc(kept);
     left -= min(left, __popc(is_eq));
   }
-  return top + logf(warp_sum(sum));
+  return logf(warp_sum(sum));
 }
 
+// What a selection leaves beside the lists in its SelectScratch: how many blocks, their largest
+// score and the logarithm of the sum of the exponentials over that one's. Log gates are (score -
+// top) - log_sum: the sum of the two in fp32 would lose the logarithm beside large scores.
+struct Kept {
+  int n;
+  float top, log_sum;
+};
+
 // select_here for r <= 256: every warp alone holds the row.
-__device__ __forceinline__ int select_short(const float* __restrict__ srow, int r, int k, int mode, float log_tau,
-                                            SelectScratch& sc, float* lse) {
+__device__ __forceinline__ Kept select_short(const float* __restrict__ srow, int r, int k, int mode, float log_tau,
+                                             SelectScratch& sc) {
   const int lane = threadIdx.x & 31;
   uint32_t v[kCandidates / 32], hi = 0u;
 #pragma unroll
@@ -471,16 +479,16 @@ __device__ __forceinline__ int select_short(const float* __restrict__ srow, int 
 #pragma unroll
     for (int i = 0; i < kCandidates / 32; ++i) n += v[i] && key_score(v[i]) - all >= log_tau ? 1u : 0u;
     k = min(k, (int)__reduce_add_sync(0xffffffffu, n));
-    if (k == 0) return 0;
+    if (k == 0) return {};
   }
-  *lse = keep_largest(v, r, k, top, threadIdx.x < 32, sc, [](int j) { return j; });
+  const float log_sum = keep_largest(v, r, k, top, threadIdx.x < 32, sc, [](int j) { return j; });
   __syncthreads();
-  return k;
+  return {k, top, log_sum};
 }
 
-// select_here for 256 < r <= 2048 and topk <= 96; -1 where too many keys are candidates.
-__device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
-                                           uint32_t* work, SelectScratch& sc, float* lse) {
+// select_here for 256 < r <= 2048 and topk <= 96; n = -1 where too many keys are candidates.
+__device__ __forceinline__ Kept select_fast(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
+                                            uint32_t* work, SelectScratch& sc) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t *maxima = work, *cand_key = work + 128, *cand_idx = cand_key + kCandidates;
   // a warp holds a contiguous part of the row, 32 at a time
@@ -513,7 +521,7 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
     if (lane == 0) sc.u[1][warp] = n;
     __syncthreads();
     k = min(k, (int)(sc.u[1][0] + sc.u[1][1] + sc.u[1][2] + sc.u[1][3]));
-    if (k == 0) return 0;
+    if (k == 0) return {};
   }
   if (warp == 0) {  // (one warp's instructions: the other CTAs of the SM use the rest)
     int need_eq;
@@ -535,7 +543,7 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
     if (w < warp) at += sc.u[0][w];
     n += sc.u[0][w];
   }
-  if (n > kCandidates) return -1;
+  if (n > kCandidates) return {-1};
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int i = 0; i < kSelectRegs; ++i) {
@@ -565,22 +573,20 @@ __device__ __forceinline__ int select_fast(const float* __restrict__ srow, int r
     if (lane == 0) sc.f[0] = sum;
   }
   __syncthreads();
-  *lse = sc.f[0];
-  return k;
+  return {k, top, sc.f[0]};
 }
 
-// Returns how many are kept; sc.idx gets them in ascending order and sc.score their
-// scores, *lse the logarithm of the sum of their exponentials. keys: r words of shared memory.
-__device__ __forceinline__ int select_here(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
-                                           uint32_t* keys, SelectScratch& sc, float* lse) {
+// sc.idx gets the kept blocks in ascending order and sc.score their scores. keys: r words of
+// shared memory.
+__device__ __forceinline__ Kept select_here(const float* __restrict__ srow, int r, int topk, int mode, float log_tau,
+                                            uint32_t* keys, SelectScratch& sc) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int k = min(topk, r);
-  *lse = 0.f;
-  if (k == 0) return 0;
-  if (r <= kCandidates) return select_short(srow, r, k, mode, log_tau, sc, lse);
+  if (k == 0) return {};
+  if (r <= kCandidates) return select_short(srow, r, k, mode, log_tau, sc);
   if (r <= 128 * kSelectRegs && k <= 96) {
-    const int n = select_fast(srow, r, topk, mode, log_tau, keys, sc, lse);
-    if (n >= 0) return n;
+    const Kept fast = select_fast(srow, r, topk, mode, log_tau, keys, sc);
+    if (fast.n >= 0) return fast;
     __syncthreads();
   }
   uint32_t u[kSelectRegs], hi = 0u, lo = 0xffffffffu;
@@ -635,7 +641,7 @@ __device__ __forceinline__ int select_here(const float* __restrict__ srow, int r
     __syncthreads();
     const float all = top + logf(sc.f[0] + sc.f[1] + sc.f[2] + sc.f[3]);
     k = min(k, count([&](uint32_t x) { return x != 0u && key_score(x) - all >= log_tau; }));
-    if (k == 0) return 0;
+    if (k == 0) return {};
   }
   // keys above T are kept, and the first need_eq of those equal to it
   uint32_t T = lo - 1u;
@@ -696,33 +702,32 @@ __device__ __forceinline__ int select_here(const float* __restrict__ srow, int r
   __syncthreads();
   float s = 0.f;
   for (int j = lane; j < k; j += 32) s += expf(sc.score[j] - top);
-  *lse = top + logf(warp_sum(s));
-  return k;
+  return {k, top, logf(warp_sum(s))};
 }
 
-// Where a CTA finds its row's kept blocks: its own selection, or the lists made before.
-struct Kept {
-  int n;
-  const int32_t* idx;
-  const float* gate;  // log gates: gate[e] - lse
-  float lse;
-};
 // The log gate of kept block e in powers of two. It stays finite, so that a maximum made of it
 // does: a score of fp32's lowest, as masks have, would give -infinity (a weight of 0 either way).
-__device__ __forceinline__ float log2_gate(const Kept& kept, int e) {
-  const float x = (kept.gate[e] - kept.lse) * GBS_LOG2E;
+__device__ __forceinline__ float log2_gate(const Kept& kept, const SelectScratch& sc, int e) {
+  const float x = (sc.score[e] - kept.top - kept.log_sum) * GBS_LOG2E;
   return x < -1e30f ? -1e30f : x;
 }
+
+// A CTA's kept blocks, by its own selection or from the lists made before, into sc.
 __device__ __forceinline__ Kept kept_blocks(const DecodeArgs& a, int srow, int cur, uint32_t* keys, SelectScratch& sc) {
-  Kept r = {0, sc.idx, sc.score, 0.f};
-  if (a.S) {
-    r.n = select_here(a.S + (size_t)srow * a.p.Nb, cur, a.p.topk, a.p.mode, a.p.log_tau, keys, sc, &r.lse);
-  } else {
-    if (cur > 0) r.n = dcheck(a.sel.cnt[srow], 0, min(a.p.topk, cur), a.c.err);
-    r.idx = a.sel.idx + (size_t)srow * a.p.topk;
-    r.gate = a.sel.logg + (size_t)srow * a.p.topk;
+  const float* scores = a.S + (size_t)srow * a.p.Nb;
+  if (!a.sel.idx) return select_here(scores, cur, a.p.topk, a.p.mode, a.p.log_tau, keys, sc);
+  const int n = cur > 0 ? dcheck(a.sel.cnt[srow], 0, min(a.p.topk, cur), a.c.err) : 0;
+  for (int j = threadIdx.x; j < n; j += 128) {
+    const int c = dcheck(a.sel.idx[(size_t)srow * a.p.topk + j], 0, cur - 1, a.c.err);
+    sc.idx[j] = c;
+    sc.score[j] = __ldg(scores + c);
   }
-  return r;
+  __syncthreads();
+  float top = -INFINITY, sum = 0.f;
+  for (int j = threadIdx.x & 31; j < n; j += 32) top = fmaxf(top, sc.score[j]);
+  top = warp_max(top);
+  for (int j = threadIdx.x & 31; j < n; j += 32) sum += expf(sc.score[j] - top);
+  return {n, top, logf(warp_sum(sum))};
 }
 
 // The splits of a row are a cluster and join their sums of n = heads * D channels: every
@@ -800,8 +805,8 @@ __global__ void __launch_bounds__(128) kv4_decode_simt_kernel(const __grid_const
   }
   for (int e = e0; e < e1; ++e) {
     const bool is_cur = e == n_hist;
-    const int c = is_cur ? cur : dcheck(kept.idx[e], 0, cur - 1, a.c.err);
-    const float bias = is_cur ? 0.f : log2_gate(kept, e);
+    const int c = is_cur ? cur : dcheck(select.idx[e], 0, cur - 1, a.c.err);
+    const float bias = is_cur ? 0.f : log2_gate(kept, select, e);
     const long long row0 = block_row(a, b, kvh, c);
     if (row0 < 0) continue;
     const int nrows = is_cur ? L - cur * kBS : kBS;
@@ -1052,7 +1057,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   if (threadIdx.x == 0) s_abort = 0;
   const Kept kept = kept_blocks(a, srow, cur, reinterpret_cast<uint32_t*>(smem), select);
   const int n_hist = kept.n;
-  if (a.S) {
+  if (!a.sel.idx) {
     sm100::fence_proxy_async_smem();  // copies will write over the keys
     __syncthreads();
   }
@@ -1080,8 +1085,8 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
     my_rows = 0;
     if (turn < turns) {
       const bool is_cur = e == n_hist;
-      const int c = is_cur ? cur : dcheck(kept.idx[e], 0, cur - 1, a.c.err);
-      my_bias = is_cur ? 0.f : log2_gate(kept, e);
+      const int c = is_cur ? cur : dcheck(select.idx[e], 0, cur - 1, a.c.err);
+      my_bias = is_cur ? 0.f : log2_gate(kept, select, e);
       const long long row = block_row(a, b, kvh, c);
       my_unit = (int)(row / kUnit) + (warp & 1);
       my_rows = row < 0 ? 0 : min(kUnit, is_cur ? L - cur * kBS - half : kUnit);
@@ -1589,7 +1594,7 @@ cudaError_t launch_decode4(DecodeArgs& a, int device, cudaStream_t st) {
     smem = Kv4Tile<D>::kBytes;
   } else {
     kernel = kv4_decode_simt_kernel<T, D>;
-    smem = a.S ? 4 * (size_t)(a.p.Nb > kSelectWork ? a.p.Nb : kSelectWork) : 0;
+    smem = a.sel.idx ? 0 : 4 * (size_t)(a.p.Nb > kSelectWork ? a.p.Nb : kSelectWork);
   }
   a.inbox = (int)((smem + 15) / 16 * 16);
   constexpr int kMost = kMma ? Kv4Tile<D>::kBytes : 4 * (kSelectMax + 4);
@@ -1786,9 +1791,8 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = sm_count(device, &sms);
   if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/device");
-  if (cur_max <= kSelectMax) {
-    a.S = S;
-  } else {
+  a.S = S;
+  if (cur_max > kSelectMax) {
     e = launch_select(S, p.B * seq.rows_per_seq, p.Nb, 1, seq_lens ? -1 : cur_max, p.topk, p.mode, p.log_tau, a.sel.idx,
                       a.sel.cnt, a.sel.logg, nullptr, st, nullptr, nullptr, 0, seq);
     if (e != cudaSuccess) return cuda_done(e, "gbs_kv4_decode/select");

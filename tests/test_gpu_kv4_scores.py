@@ -7,7 +7,7 @@ import torch
 
 from gated_block_sparse_gate_b200 import binding as gb
 from gated_block_sparse_gate_b200.build import build
-from tests.test_gpu_kv4 import _check, _decode_case
+from tests.test_gpu_kv4 import _check, _decode_case, _run
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -36,3 +36,28 @@ def test_masked_blocks_in_the_longest_rows(dtype):
     x = _decode_case(3, 1, 2, 1, 64, 530000, None, True, dtype, paged=False)
     x["S"][..., [i for i in range(x["S"].shape[-1]) if i % 1700 != 1]] = LOWEST
     _check(x, 530000, 20, True)
+
+
+# blocks a row, budget: rows that a warp, one warp after the others, all warps, and a kernel before select from
+ROWS = [(900, 6), (900, 20), (40000, 32), (40000, 200), (530000, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("L,k", ROWS)
+@pytest.mark.parametrize("shift", [2.0 ** 20, -2.0 ** 20])
+def test_gates_do_not_depend_on_the_scores_level(shift, L, k, dtype):
+    """Scores in steps of 1 / 4, which fp32 holds beside 2^20: the log gates are those without it."""
+    x = _decode_case(k, 1, 2, 1, 64, L, None, True, dtype, paged=False)
+    x["S"] = (4 * x["S"]).round() / 4 + shift
+    _check(x, L, k, True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("L,k", ROWS)
+@pytest.mark.parametrize("level", [1e8, LOWEST, -LOWEST])
+def test_equal_scores_of_any_size(level, L, k, dtype):
+    x = _decode_case(k, 1, 2, 1, 64, L, None, True, dtype, paged=False)
+    x["S"].zero_()
+    want = _run(x, L, k, True)
+    x["S"].fill_(level)
+    assert all(torch.equal(a, b) for a, b in zip(_run(x, L, k, True), want))
