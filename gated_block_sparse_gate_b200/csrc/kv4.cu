@@ -943,6 +943,15 @@ struct Kv4Tile {
 };
 constexpr int kMmaThreads = 128;
 constexpr uint64_t kWaitNs = 4000000000ull;
+// In the debug build a call whose error word already holds GBS_ERR_TIMEOUT takes its first waits
+// for expired, once the copies have come: so tests reach what follows.
+#ifdef GBS_DEBUG
+__device__ __forceinline__ int starts_given_up(const unsigned int* err) { return *err == GBS_ERR_TIMEOUT; }
+__device__ __forceinline__ bool gives_up(int abort) { return abort != 0; }
+#else
+__device__ __forceinline__ int starts_given_up(const unsigned int*) { return 0; }
+__device__ __forceinline__ bool gives_up(int) { return false; }
+#endif
 // Weights are 2^(z - m), with m kLift below the largest z when it was set, and at most
 // 2^kRoom; where scales reach 2^e, e > 0, both are e less. So no product of a weight and a
 // scale leaves fp16, and its steps of 2^-24 are 2^-34 of the largest weight.
@@ -1054,7 +1063,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   }
   const int split = blockIdx.y;
   const int L = sequence_length(a, b), cur = L > 0 ? (L - 1) / kBS : 0;
-  if (threadIdx.x == 0) s_abort = 0;
+  if (threadIdx.x == 0) s_abort = starts_given_up(a.c.err);
   const Kept kept = kept_blocks(a, srow, cur, reinterpret_cast<uint32_t*>(smem), select);
   const int n_hist = kept.n;
   if (!a.sel.idx) {
@@ -1232,7 +1241,7 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
   int s = 0;
   uint32_t parity = 0;
   for (int turn = 0; turn < turns; ++turn) {
-    if (!sm100::mbar_wait(&full[s], parity, &s_abort, a.c.err, kWaitNs)) {
+    if (!sm100::mbar_wait(&full[s], parity, &s_abort, a.c.err, kWaitNs) || gives_up(s_abort)) {
       // given up: no copy may be in flight when the CTA ends
       if (lane == 0)
         for (int i = turn; i < turns && i < turn + S; ++i) sm100::mbar_drain(&full[i % S], (i / S) & 1, 1000000ull);
@@ -1528,9 +1537,10 @@ __global__ void __launch_bounds__(kMmaThreads, 4) kv4_decode_mma_kernel(const __
       sum += s_l[w][h] * f;
       v += reinterpret_cast<const float*>(smem + w * Tile::kWarp)[i] * f;
     }
+    if (s_abort) sum = NAN;  // a wait ran out: the row's results show it, beside the error word
     if (a.splits > 1) {
       send_sum<D>(a, inbox, split, i, v, M, sum);
-    } else if (!s_abort) {  // (a wait that ran out is reported in the error word)
+    } else {
       const size_t row = (size_t)b * p.Hq + h0 + h;
       reinterpret_cast<__nv_bfloat16*>(a.O)[row * D + i % D] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
       if (i % D == 0) a.LSE[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * GBS_LN2;

@@ -412,6 +412,8 @@ GBS_API size_t gbs_kv4_workspace_bytes(const gbs_params* p);
  *   S, LSE  as in gbs_decode_ex.
  *   num_splits  partitions of a row's kept blocks, which join their sums in one
  *          thread-block cluster: of more than 16, 16 are made; 0 = automatic.
+ *   A row one of whose copies does not arrive within seconds has NaN as O and LSE,
+ *          and gbs_check(ws) reports GBS_ERR_TIMEOUT.
  *   ws     gbs_kv4_workspace_bytes(p) bytes (256 up to 8192 blocks a row). */
 GBS_API gbs_status gbs_kv4_decode(const gbs_params* p, const gbs_kv4_cache* cache,
                                   const int32_t* seq_lens, int group_shared, const void* q,
