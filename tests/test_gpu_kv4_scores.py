@@ -61,3 +61,28 @@ def test_equal_scores_of_any_size(level, L, k, dtype):
     want = _run(x, L, k, True)
     x["S"].fill_(level)
     assert all(torch.equal(a, b) for a, b in zip(_run(x, L, k, True), want))
+
+
+@pytest.mark.parametrize("L", [1000, 20000, 140000, 530000])
+@pytest.mark.parametrize("k", [0, 20, 96, 256])
+def test_nan_scores_keep_every_index_in_range(L, k):
+    """Scores have to be finite; with NaNs among them (the one of all bits set too) the debug build finds every kept
+    block inside its row all the same. It clamps a bad index before it is used."""
+    saved, gb._lib = gb._lib, None
+    try:
+        gb.load_library(build(debug=True))
+        for dtype in (BF, F32):
+            for shared in (False, True):
+                x = _decode_case(11, 2, 4, 2, 64, L, [L, L // 3], shared, dtype, paged=False)
+                bits = x["S"].view(torch.int32)
+                bits[0, :1] = -1
+                bits[0, 1, ::3] = 0x7fffffff
+                bits[1, 0, 5::7] = -1
+                p = gb.make_params(2, 4, 2, L, 64, 64, k, "sparse", dtype)
+                ws = torch.zeros(gb.kv4_workspace_bytes(p), dtype=torch.uint8, device="cuda:0")
+                _run(x, L, k, shared, ws=ws)
+                gb.check(ws)
+                _run(x, L, k, shared, tau=1e-3, ws=ws)
+                gb.check(ws)
+    finally:
+        gb._lib = saved
