@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 import struct
 
@@ -81,6 +82,7 @@ def load_library(path: str = LIB_PATH):
         return _lib
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing; build it with gated_block_sparse_gate_b200.build")
+    _load_marshal()
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(Params)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
@@ -155,13 +157,6 @@ def _heads_of(t, dtypes, device_index, shape, token_major, written):
     return None
 
 
-try:
-    from gated_block_sparse_gate_b200 import _marshal
-except ImportError:  # built without the headers: the checks below do all of it
-    _marshal = None
-else:
-    _fits, _heads_of = _marshal.fits, _marshal.heads
-
 # The entry points that csrc/marshal.cpp calls, in its order.
 _NATIVE = ("gbs_qkv_rope_fwd", "gbs_qkv_rope_bwd", "gbs_qkv_rope_workspace_bytes", "gbs_kv4_append", "gbs_kv4_read",
            "gbs_kv4_decode", "gbs_kv4_workspace_bytes")
@@ -172,7 +167,25 @@ class _NoCalls:
     qkv_rope = qkv_rope_backward = kv4_append = kv4_read = kv4_decode = staticmethod(lambda *a: None)
 
 
-_native = _marshal or _NoCalls
+# csrc/marshal.cpp as a module, and what takes whole calls: that module or _NoCalls.
+_marshal, _native = None, _NoCalls
+
+
+def _load_marshal():
+    """Takes csrc/marshal.cpp's checks and calls where it is built; else the checks below do all of it. Called at
+    the import and again when a library is loaded, since build() may have come between the two."""
+    global _marshal, _native, _fits, _heads_of
+    if _marshal is not None:
+        return
+    importlib.invalidate_caches()
+    try:
+        _marshal = importlib.import_module("gated_block_sparse_gate_b200._marshal")
+    except ImportError:
+        return
+    _native, _fits, _heads_of = _marshal, _marshal.fits, _marshal.heads
+
+
+_load_marshal()
 
 
 def _invalid(where, detail):

@@ -1,0 +1,62 @@
+"""Building and loading the library and the binding's native module, in any order and without what the module needs."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+from gated_block_sparse_gate_b200 import binding as gb
+from gated_block_sparse_gate_b200 import build as b
+
+PACKAGE = os.path.dirname(os.path.abspath(b.__file__))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    b.build()
+
+
+@pytest.fixture
+def checkout(tmp_path):
+    """The package's Python files and libgbs.so under another root, without the native module."""
+    to = tmp_path / "gated_block_sparse_gate_b200"
+    to.mkdir()
+    for name in os.listdir(PACKAGE):
+        if name.endswith(".py") or name == "libgbs.so":
+            shutil.copy(os.path.join(PACKAGE, name), to)
+    return to
+
+
+def _run(checkout, code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=checkout.parent, capture_output=True, text=True,
+                       env={**os.environ, "PYTHONPATH": str(checkout.parent)})
+    assert r.returncode == 0, r.stderr[-2000:]
+    return r.stdout.split()
+
+
+def test_a_native_module_built_after_the_import_is_used(checkout):
+    module = b.build_marshal()
+    if module is None:
+        pytest.skip("built without the headers")
+    out = _run(checkout, f"""
+import shutil
+from gated_block_sparse_gate_b200 import binding as gb
+print(gb._native is gb._NoCalls)
+shutil.copy({module!r}, {str(checkout)!r})
+gb.load_library()
+print(gb._native is gb._marshal, gb._fits is gb._marshal.fits, gb._heads_of is gb._marshal.heads)
+""")
+    assert out == ["True"] * 4
+
+
+def test_without_the_native_module_the_binding_loads(checkout):
+    assert _run(checkout, """
+from gated_block_sparse_gate_b200 import binding as gb
+gb.load_library()
+print(gb._native is gb._NoCalls, gb._marshal is None)
+""") == ["True", "True"]
+
+
+def test_the_native_module_is_the_one_loaded_here():
+    assert b.build_marshal() is None or (gb.load_library() and gb._native is gb._marshal)
