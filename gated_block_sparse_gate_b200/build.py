@@ -13,6 +13,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -45,15 +46,18 @@ def _stale(lib=LIB):
 
 def build_marshal(force: bool = False, verbose: bool = False):
     """The binding's argument checks and calls on the tensors themselves (csrc/marshal.cpp),
-    where Python's, torch's and CUDA's headers are installed; the binding does them in Python
-    where the module is missing."""
+    where torch, its headers, Python's and CUDA's and a host compiler are installed. Where one
+    is missing or the compiler fails, that is said and None returned: the binding does the same
+    in Python."""
     src = os.path.join(CSRC, "marshal.cpp")
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > max(
             map(os.path.getmtime, (src, os.path.join(INCLUDE, "gbs.h")))):
         return MARSHAL
-    import torch
-    from torch.utils import cpp_extension
-
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return None
     include = sysconfig.get_paths()["include"]
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     dirs = [include, *cpp_extension.include_paths(), cuda, INCLUDE]
@@ -68,14 +72,26 @@ def build_marshal(force: bool = False, verbose: bool = False):
            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", MARSHAL + ".tmp"]
     if verbose:
         print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+    try:
+        subprocess.run(cmd, check=True)
+    except (OSError, subprocess.CalledProcessError) as e:
+        if os.path.exists(MARSHAL):  # of other sources
+            os.remove(MARSHAL)
+        warnings.warn(f"csrc/marshal.cpp was not built ({e}); the binding checks arguments in Python")
+        return None
     os.replace(MARSHAL + ".tmp", MARSHAL)
     return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    lib = DEBUG_LIB if debug else LIB
+    lib = build_library(force, verbose, debug)
     build_marshal(force, verbose)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+    """The C library, which needs nvcc only."""
+    lib = DEBUG_LIB if debug else LIB
     if not force and not _stale(lib):
         return lib
     nvcc = os.environ.get("NVCC", "nvcc")

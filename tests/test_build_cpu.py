@@ -60,3 +60,32 @@ print(gb._native is gb._NoCalls, gb._marshal is None)
 
 def test_the_native_module_is_the_one_loaded_here():
     assert b.build_marshal() is None or (gb.load_library() and gb._native is gb._marshal)
+
+
+def test_the_library_builds_without_a_host_compiler(monkeypatch, tmp_path):
+    """nvcc is stood in for; the module's compiler does not exist, or fails."""
+    made = []
+    run = subprocess.run
+
+    def nvcc(cmd, **kw):
+        if cmd[0] != "nvcc":
+            return run(cmd, **kw)
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libgbs.so"))
+    monkeypatch.setattr(b, "MARSHAL", str(tmp_path / "_marshal.so"))
+    monkeypatch.setattr(b.subprocess, "run", nvcc)
+    monkeypatch.delenv("NVCC", raising=False)
+    for compiler in (str(tmp_path / "no compiler"), "false"):
+        monkeypatch.setenv("CXX", compiler)
+        open(b.MARSHAL, "w").close()  # made from other sources: not to be loaded
+        with pytest.warns(UserWarning, match="marshal.cpp was not built"):
+            assert b.build(force=True) == b.LIB
+    assert len(made) == 2 and not os.path.exists(b.MARSHAL)
+
+
+def test_the_library_builds_without_torch(monkeypatch, tmp_path):
+    monkeypatch.setattr(b, "MARSHAL", str(tmp_path / "_marshal.so"))
+    monkeypatch.setitem(sys.modules, "torch", None)  # an import of it raises ImportError
+    assert b.build() == b.LIB and b.build_marshal() is None
