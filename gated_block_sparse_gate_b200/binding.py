@@ -8,11 +8,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import importlib
+import importlib.util
 import os
 import struct
 
 import torch
+
+from gated_block_sparse_gate_b200.build import marshal_path
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgbs.so")
@@ -177,11 +179,16 @@ def _load_marshal():
     global _marshal, _native, _fits, _heads_of
     if _marshal is not None:
         return
-    importlib.invalidate_caches()
+    path = marshal_path()
+    if not os.path.exists(path):
+        return
+    spec = importlib.util.spec_from_file_location("gated_block_sparse_gate_b200._marshal", path)
     try:
-        _marshal = importlib.import_module("gated_block_sparse_gate_b200._marshal")
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
     except ImportError:
         return
+    _marshal = module
     _native, _fits, _heads_of = _marshal, _marshal.fits, _marshal.heads
 
 

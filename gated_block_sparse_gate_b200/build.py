@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -21,7 +22,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgbs.so")
 DEBUG_LIB = os.path.join(HERE, "libgbs_debug.so")
-MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,20 +44,31 @@ def _stale(lib=LIB):
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def marshal_path() -> str:
+    """Where the binding's native module for this Python and this torch is: its code is compiled against torch's
+    own structures, so the name holds torch's version and commit. Raises ImportError without torch."""
+    import torch
+
+    tag = re.sub(r"[^\w.+]", "_", f"{torch.__version__}-{(torch.version.git_version or '')[:8]}")
+    return os.path.join(HERE, f"_marshal-{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_marshal(force: bool = False, verbose: bool = False):
     """The binding's argument checks and calls on the tensors themselves (csrc/marshal.cpp),
     where torch, its headers, Python's and CUDA's and a host compiler are installed. Where one
     is missing or the compiler fails, that is said and None returned: the binding does the same
     in Python."""
     src = os.path.join(CSRC, "marshal.cpp")
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > max(
-            map(os.path.getmtime, (src, os.path.join(INCLUDE, "gbs.h")))):
-        return MARSHAL
     try:
         import torch
         from torch.utils import cpp_extension
+
+        module = marshal_path()
     except ImportError:
         return None
+    if not force and os.path.exists(module) and os.path.getmtime(module) > max(
+            map(os.path.getmtime, (src, os.path.join(INCLUDE, "gbs.h")))):
+        return module
     include = sysconfig.get_paths()["include"]
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     dirs = [include, *cpp_extension.include_paths(), cuda, INCLUDE]
@@ -69,18 +80,18 @@ def build_marshal(force: bool = False, verbose: bool = False):
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(x for d in dirs for x in ("-isystem", d)), src, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", MARSHAL + ".tmp"]
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", module + ".tmp"]
     if verbose:
         print(" ".join(cmd))
     try:
         subprocess.run(cmd, check=True)
     except (OSError, subprocess.CalledProcessError) as e:
-        if os.path.exists(MARSHAL):  # of other sources
-            os.remove(MARSHAL)
+        if os.path.exists(module):  # of other sources
+            os.remove(module)
         warnings.warn(f"csrc/marshal.cpp was not built ({e}); the binding checks arguments in Python")
         return None
-    os.replace(MARSHAL + ".tmp", MARSHAL)
-    return MARSHAL
+    os.replace(module + ".tmp", module)
+    return module
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:

@@ -74,18 +74,34 @@ def test_the_library_builds_without_a_host_compiler(monkeypatch, tmp_path):
         open(cmd[cmd.index("-o") + 1], "w").close()
 
     monkeypatch.setattr(b, "LIB", str(tmp_path / "libgbs.so"))
-    monkeypatch.setattr(b, "MARSHAL", str(tmp_path / "_marshal.so"))
+    module = str(tmp_path / "_marshal.so")
+    monkeypatch.setattr(b, "marshal_path", lambda: module)
     monkeypatch.setattr(b.subprocess, "run", nvcc)
     monkeypatch.delenv("NVCC", raising=False)
     for compiler in (str(tmp_path / "no compiler"), "false"):
         monkeypatch.setenv("CXX", compiler)
-        open(b.MARSHAL, "w").close()  # made from other sources: not to be loaded
+        open(module, "w").close()  # made from other sources: not to be loaded
         with pytest.warns(UserWarning, match="marshal.cpp was not built"):
             assert b.build(force=True) == b.LIB
-    assert len(made) == 2 and not os.path.exists(b.MARSHAL)
+    assert len(made) == 2 and not os.path.exists(module)
 
 
-def test_the_library_builds_without_torch(monkeypatch, tmp_path):
-    monkeypatch.setattr(b, "MARSHAL", str(tmp_path / "_marshal.so"))
+def test_the_library_builds_without_torch(monkeypatch):
     monkeypatch.setitem(sys.modules, "torch", None)  # an import of it raises ImportError
     assert b.build() == b.LIB and b.build_marshal() is None
+
+
+def test_the_native_module_of_another_torch_is_not_loaded(checkout):
+    """Its name tells which torch it was compiled against."""
+    module = b.build_marshal()
+    if module is None:
+        pytest.skip("built without the headers")
+    shutil.copy(module, checkout)
+    for change in ("torch.__version__ = '9.9.9+other'", "torch.version.git_version = 'another commit'", ""):
+        assert _run(checkout, f"""
+import torch
+{change}
+from gated_block_sparse_gate_b200 import binding as gb
+gb.load_library()
+print(gb._native is gb._NoCalls)
+""") == [str(bool(change))]
