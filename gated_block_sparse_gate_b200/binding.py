@@ -773,7 +773,7 @@ def _check_kv4(where, cache, B, d, device, block, block_table):
     max_blocks = block_table.shape[1]
     desc = _KV4(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), block_table.data_ptr(), max_blocks, first,
                 rows)
-    return desc, Hkv, max_blocks * block
+    return desc, Hkv, min(max_blocks * block, 2**31 - 1)  # (positions are int32)
 
 
 def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out, dev):

@@ -121,8 +121,9 @@ DecWs carve_dec(const Problem& p, void* ws) {
 
 bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15u) == 0; }
 
-// Validates the parameter block and resolves it into a Problem.
-gbs_status resolve(const gbs_params* in, int op, Problem* out) {
+// Validates the parameter block and resolves it into a Problem. kv4: of a 4-bit cache, whose
+// kernels count its rows in half blocks and take no tensor maps.
+gbs_status resolve(const gbs_params* in, int op, Problem* out, bool kv4 = false) {
   if (!in) return fail(GBS_ERR_INVALID_ARG, "params is NULL");
   const gbs_params& q = *in;
   if (q.B <= 0 || q.Hq <= 0 || q.Hkv <= 0 || q.N <= 0 || q.d <= 0 || q.block <= 0)
@@ -144,10 +145,12 @@ gbs_status resolve(const gbs_params* in, int op, Problem* out) {
   if (q.block != 64) return fail(GBS_ERR_UNSUPPORTED, "block %d: only 64 is built", q.block);
   if (q.d != 64 && q.d != 128) return fail(GBS_ERR_UNSUPPORTED, "d %d: only 64 and 128 are built", q.d);
   const size_t Nb = ((size_t)q.N + q.block - 1) / q.block;
-  if ((size_t)q.B * q.Hq * Nb * Nb > ((size_t)1 << 40) || (size_t)q.B * q.Hq * q.N * q.d > ((size_t)1 << 40))
+  if (kv4 && (size_t)q.B * q.Hq > (size_t)INT32_MAX)  // grid indices
+    return fail(GBS_ERR_INVALID_ARG, "problem too large: B * Hq must be below 2^31");
+  if (!kv4 && ((size_t)q.B * q.Hq * Nb * Nb > ((size_t)1 << 40) || (size_t)q.B * q.Hq * q.N * q.d > ((size_t)1 << 40)))
     return fail(GBS_ERR_INVALID_ARG, "problem too large");
   // token rows are TMA coordinates and grid indices: signed 32-bit
-  if ((size_t)q.B * q.Hq * q.N > (size_t)INT32_MAX)
+  if (!kv4 && (size_t)q.B * q.Hq * q.N > (size_t)INT32_MAX)
     return fail(GBS_ERR_INVALID_ARG, "problem too large: B * Hq * N must be below 2^31");
   Problem& p = *out;
   p.B = q.B; p.Hq = q.Hq; p.Hkv = q.Hkv; p.N = q.N; p.d = q.d; p.bs = q.block;
@@ -183,6 +186,7 @@ unsigned int* err_word(void* ws) { return reinterpret_cast<unsigned int*>(ws); }
 namespace gbs {
 void set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 gbs_status resolve_params(const gbs_params* in, int op, Problem* out) { return resolve(in, op, out); }
+gbs_status resolve_kv4_params(const gbs_params* in, Problem* out) { return resolve(in, GBS_OP_DECODE, out, true); }
 gbs_status fail_status(gbs_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

@@ -28,6 +28,8 @@ struct Problem {
 // Validates a parameter block for one op (GBS_OP_FWD / BWD / DECODE) and
 // resolves it; on failure sets gbs_last_error() and returns the status.
 gbs_status resolve_params(const gbs_params* in, int op, Problem* out);
+// The same for the calls on a 4-bit cache (a decode's parameters, by that cache's limits).
+gbs_status resolve_kv4_params(const gbs_params* in, Problem* out);
 // Most decode splits a call can ask for.
 constexpr int kMaxDecodeSplits = 32;
 // The decode's automatic split count for n_ent blocks per selection row:

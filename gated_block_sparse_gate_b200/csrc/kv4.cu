@@ -1683,7 +1683,7 @@ gbs_status rows_call(const char* where, const gbs_params* in, const gbs_kv4_cach
                      void* stream) {
   set_last_error("");
   Problem p{};
-  gbs_status s = resolve_params(in, GBS_OP_DECODE, &p);
+  gbs_status s = resolve_kv4_params(in, &p);
   if (s != GBS_OK) return s;
   RowArgs a{};
   if ((s = resolve_cache(p, cache, &a.c)) != GBS_OK) return s;
@@ -1759,7 +1759,7 @@ extern "C" gbs_status gbs_kv4_read(const gbs_params* p, const gbs_kv4_cache* cac
 extern "C" size_t gbs_kv4_workspace_bytes(const gbs_params* in) {
   set_last_error("");
   Problem p{};
-  if (resolve_params(in, GBS_OP_DECODE, &p) != GBS_OK) return 0;
+  if (resolve_kv4_params(in, &p) != GBS_OK) return 0;
   DecodeArgs a{};
   return carve_kv4(p, nullptr, &a);
 }
@@ -1770,7 +1770,7 @@ extern "C" gbs_status gbs_kv4_decode(const gbs_params* in, const gbs_kv4_cache* 
   set_last_error("");
   DecodeArgs a{};
   Problem& p = a.p;
-  gbs_status s = resolve_params(in, GBS_OP_DECODE, &p);
+  gbs_status s = resolve_kv4_params(in, &p);
   if (s != GBS_OK) return s;
   if ((s = resolve_cache(p, cache, &a.c)) != GBS_OK) return s;
   const void* ptrs[] = {q, S, O, LSE};

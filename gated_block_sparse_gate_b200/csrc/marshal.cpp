@@ -376,7 +376,7 @@ struct CacheCall {
       c.block_table = x.data_ptr<int32_t>();
       c.max_blocks = whole(x.size(1));
       c.num_pages = whole(first);
-      most = x.size(1) * block;
+      most = std::min<int64_t>(x.size(1) * block, INT32_MAX);  // positions are int32
     }
   }
 };

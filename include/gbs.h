@@ -47,7 +47,8 @@
  *     Hq % Hkv == 0; 0 <= topk <= GBS_MAX_TOPK; dtype bf16 (tensor-core path)
  *     or fp32 (exact SIMT path). S must be finite. B * Hq * N < 2^31 (token
  *     rows are 32-bit TMA coordinates); larger problems return
- *     GBS_ERR_INVALID_ARG.
+ *     GBS_ERR_INVALID_ARG. (The calls on a 4-bit cache have limits of their own:
+ *     B * Hq < 2^31 and those of gbs_kv4_cache.)
  */
 #ifndef GBS_H_
 #define GBS_H_
@@ -379,7 +380,7 @@ typedef struct gbs_kv4_cache {
 /* Writes T tokens of every sequence into the cache: token t of sequence b goes
  * to position start[b] + t.
  *   p      B, Hkv, N (longest length a sequence may reach), d, block and dtype
- *          are read.
+ *          are read. N may be any int: B * Hq * N has no limit of its own here.
  *   K, V   [B, Hkv, T, d] in p->dtype.
  *   start  [B] int32; count NULL or [B] int32: only tokens t < count[b] are
  *          written (a padded batch); rows not written keep their contents.
