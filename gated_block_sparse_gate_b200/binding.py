@@ -490,11 +490,13 @@ def decode_noalloc(q, Kc, Vc, S, L=None, block=64, topk=32, scale=0.0, num_split
 # ------------------------------------------- projections to attention, 4-bit cache
 
 
-def _elsewhere(device, stream):
+def _elsewhere(where, device, stream):
     """What a call has to enter before it allocates and launches: ``stream``, so that
     temporaries belong to the stream that uses them, or the tensors' device. None
     where both are current already."""
     if stream is not None:
+        if stream.device != device:  # (its kernels would start on another stream, of the tensors' device)
+            raise _invalid(where, f"stream is on {stream.device}; expected {device}")
         return torch.cuda.stream(stream)
     if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
@@ -649,7 +651,7 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
             return r[1:]
     lib = load_library()
     dev = _device(where, "q", q)
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(where, dev, stream)
     if ctx is not None:
         with ctx:
             return qkv_rope(q, k, v, cos, sin, pos, wq, wk, eps, axes, interleaved, out, ws)
@@ -690,7 +692,7 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
             return r[1:]
     lib = load_library()
     dev = _device(where, "q", q)
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(where, dev, stream)
     if ctx is not None:
         with ctx:
             return qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV, wq, wk, eps, axes, interleaved, grads, ws)
@@ -811,7 +813,7 @@ def kv4_append(K, V, cache, start, block_table=None, count=None, block=64, ws=No
             return
     fn = load_library().gbs_kv4_append
     dev = _device(where, "K", K)
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(where, dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_append(K, V, cache, start, block_table, count, block, ws)
@@ -832,7 +834,7 @@ def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16
             return r[1:]
     fn = load_library().gbs_kv4_read
     dev = _device(where, "start", start)
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(where, dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_read(cache, start, T, block_table, count, dtype, block, out, ws)
@@ -875,7 +877,7 @@ def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block
             return r[1:]
     lib = load_library()
     dev = _device(where, "q", q)
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(where, dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_decode(q, cache, S, L, block, topk, scale, num_splits, block_table, seq_lens, group_shared,

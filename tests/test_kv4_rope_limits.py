@@ -28,3 +28,20 @@ def test_a_block_table_of_more_rows_than_int32_holds(on_meta):
     pages = gb.kv4_cache(2, 2, 64, num_pages=8, device="meta")
     assert gb._check_kv4("x", pages, 2, 64, torch.device("meta"), 64, wide)[2] == 2 ** 31 - 1
     gb.kv4_append(meta(2, 2, 5, 64), meta(2, 2, 5, 64), pages, meta(2, dtype=I32), block_table=wide)
+
+
+def test_calls_enter_the_device_and_the_stream_of_their_tensors(monkeypatch):
+    """With stand-ins for the current device, for entering one and for streams."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: ("device", d))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: ("stream", s))
+    here, there = torch.device("cuda", 0), torch.device("cuda", 1)
+    assert gb._elsewhere("x", here, None) is None
+    assert gb._elsewhere("x", there, None) == ("device", there)
+
+    class Stream:
+        device = there
+
+    side = Stream()
+    assert gb._elsewhere("x", there, side) == ("stream", side)
+    assert "stream is on cuda:1" in rejected(gb._elsewhere, "x", here, side)
