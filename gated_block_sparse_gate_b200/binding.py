@@ -641,7 +641,8 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
     ``cos``, ``sin``: fp32 [max_pos, rot / 2] (``rope_tables``); the first rot
     channels are rotated in pairs of halves or, ``interleaved``, of neighbours.
     ``pos``: int32 [B, N], or [B, N, axes] with ``axes`` the axis of every pair
-    (``rope_axes``). ``out``: (Q, K, V) to write to, strided too. Returns (Q, K, V)."""
+    (``rope_axes``; without them every pair is on the first). ``out``: (Q, K, V) to write
+    to, strided too, in no memory of the inputs. Returns (Q, K, V)."""
     where = "gbs_qkv_rope_fwd"
     if stream is None:
         r = _native.qkv_rope(load_library().native, q, k, v, cos, sin, pos, wq, wk, eps, axes, interleaved, out, ws)
@@ -681,7 +682,7 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
     dV [B, Hkv, N, d] (what ``backward`` returns; dV may be None) to
     (dq, dk, dv, dwq, dwk): dq [B, N, Hq, d], dk, dv [B, N, Hkv, d] and fp32
     dwq, dwk [d] (None without weights). ``grads``: (dq, dk, dv) to write to,
-    such as parts of one packed tensor."""
+    such as parts of one packed tensor, in no memory of the inputs."""
     where = "gbs_qkv_rope_bwd"
     if stream is None:
         r = _native.qkv_rope_backward(load_library().native, q, k, cos, sin, pos, dQ, dK, dV, wq, wk, eps, axes,

@@ -212,6 +212,34 @@ gbs_status resolve_heads(const gbs_heads* t, const char* name, int esize, bool o
   return GBS_OK;
 }
 
+bool share_memory(const Heads& a, int heads_a, const Heads& b, int heads_b, int B, int N, int d, int esize) {
+  const long long size_a[] = {B, heads_a, N}, step_a[] = {a.sb, a.sh, a.sn};
+  const long long size_b[] = {B, heads_b, N}, step_b[] = {b.sb, b.sh, b.sn};
+  // elements that a tensor spans within a period; 0 where the period does not divide its longer steps
+  auto span = [&](const long long* size, const long long* step, long long period) {
+    long long n = d;
+    for (int i = 0; i < 3; ++i) {
+      if (size[i] < 2) continue;
+      if (period && step[i] >= period) {
+        if (step[i] % period) return 0ll;
+      } else {
+        n += (size[i] - 1) * step[i];
+      }
+    }
+    return n;
+  };
+  const long long apart = ((const char*)b.ptr - (const char*)a.ptr) / esize;  // (both are 16-byte aligned)
+  if (apart >= span(size_a, step_a, 0) || -apart >= span(size_b, step_b, 0)) return false;
+  for (int i = 0; i < 6; ++i) {
+    const long long period = i < 3 ? step_a[i] : step_b[i - 3];
+    if ((i < 3 ? size_a[i] : size_b[i - 3]) < 2 || period <= 0) continue;
+    const long long n_a = span(size_a, step_a, period), n_b = span(size_b, step_b, period);
+    const long long at = (apart % period + period) % period;
+    if (n_a && n_b && at >= n_a && at + n_b <= period) return false;
+  }
+  return true;
+}
+
 cudaError_t decode_auto_splits(const Problem& p, bool grouped, int n_ent, int* splits) {
   // Shares of at most 17 blocks per CTA, and at least two waves of the split
   // kernel's resident CTAs. On the 64 x 131072, K = 32 decode both variants

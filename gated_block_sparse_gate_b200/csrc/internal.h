@@ -104,6 +104,9 @@ struct Heads {
 };
 // Validates a gbs_heads (NULL unless `optional`, alignment, strides) into *out.
 gbs_status resolve_heads(const gbs_heads* t, const char* name, int esize, bool optional, Heads* out);
+// Whether two [B, heads, N, d] tensors may share an element: not where their ranges are apart,
+// or where both fall into ranges apart of every period of some stride (parts of one tensor).
+bool share_memory(const Heads& a, int heads_a, const Heads& b, int heads_b, int B, int N, int d, int esize);
 // Sets gbs_last_error() from a format and returns `s`.
 gbs_status fail_status(gbs_status s, const char* fmt, ...);
 

@@ -1698,6 +1698,8 @@ gbs_status rows_call(const char* where, const gbs_params* in, const gbs_kv4_cach
   const long long rows = (long long)p.B * p.Hkv * T;
   if (rows > INT32_MAX) return fail_status(GBS_ERR_INVALID_ARG, "problem too large: B * Hkv * T must be below 2^31");
   if (rows == 0) return GBS_OK;
+  if (READ && share_memory(a.t[0], p.Hkv, a.t[1], p.Hkv, p.B, T, p.d, es))
+    return fail_status(GBS_ERR_INVALID_ARG, "K and V share memory");
   a.B = p.B; a.Hkv = p.Hkv; a.T = T; a.N = p.N;
   a.start = start; a.count = count;
   a.c.err = static_cast<unsigned int*>(ws);

@@ -439,6 +439,23 @@ gbs_status check_side(const RopeArgs& a, const void* wq, const void* wk, const f
   return GBS_OK;
 }
 
+// That no output shares memory with an input or another output: in (n_in of them, heads[i] each)
+// and out, of which the pointers that are null are left out.
+gbs_status check_apart(const gbs_rope_params& p, int n_in, const Heads* in, const int* in_heads, const char* const* in_names,
+                       const Heads* out, const char* const* out_names) {
+  const int es = p.dtype == GBS_BF16 ? 2 : 4, out_heads[] = {p.Hq, p.Hkv, p.Hkv};
+  for (int o = 0; o < 3; ++o) {
+    if (!out[o].ptr) continue;
+    for (int i = 0; i < n_in; ++i)
+      if (in[i].ptr && share_memory(out[o], out_heads[o], in[i], in_heads[i], p.B, p.N, p.d, es))
+        return fail_status(GBS_ERR_INVALID_ARG, "%s and %s share memory", in_names[i], out_names[o]);
+    for (int i = 0; i < o; ++i)
+      if (out[i].ptr && share_memory(out[o], out_heads[o], out[i], out_heads[i], p.B, p.N, p.d, es))
+        return fail_status(GBS_ERR_INVALID_ARG, "%s and %s share memory", out_names[i], out_names[o]);
+  }
+  return GBS_OK;
+}
+
 constexpr int kSms = 148;
 constexpr int kMaxBwdCtas = 512;  // of a tensor
 
@@ -517,6 +534,8 @@ extern "C" gbs_status gbs_qkv_rope_fwd(const gbs_rope_params* p, const gbs_heads
   }
   if ((s = check_side(a, wq, wk, cos_tab, sin_tab, pos)) != GBS_OK) return s;
   if ((uintptr_t)ws & 255u) return fail_status(GBS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  const int in_heads[] = {p->Hq, p->Hkv, p->Hkv};
+  if ((s = check_apart(*p, 3, a.in, in_heads, names, a.out, names + 3)) != GBS_OK) return s;
   a.wq = wq; a.wk = wk; a.norm = wq != nullptr;
   a.cos_tab = cos_tab; a.sin_tab = sin_tab; a.pos = pos;
   a.err = static_cast<unsigned int*>(ws);
@@ -556,6 +575,10 @@ extern "C" gbs_status gbs_qkv_rope_bwd(const gbs_rope_params* p, const gbs_heads
   if (!ws) return fail_status(GBS_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
   if ((uintptr_t)ws & 255u) return fail_status(GBS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   if (ws_bytes < need) return fail_status(GBS_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  const Heads read[] = {a.in[0], a.in[1], a.in[2], a.x[0], a.x[1]};
+  const int in_heads[] = {p->Hq, p->Hkv, p->Hkv, p->Hq, p->Hkv};
+  const char* read_names[] = {"dQ", "dK", "dV", "q", "k"};
+  if ((s = check_apart(*p, wq ? 5 : 3, read, in_heads, read_names, a.out, names + 3)) != GBS_OK) return s;
   a.wq = wq; a.wk = wk; a.norm = wq != nullptr;
   a.cos_tab = cos_tab; a.sin_tab = sin_tab; a.pos = pos;
   a.err = static_cast<unsigned int*>(ws);

@@ -325,7 +325,8 @@ GBS_API size_t gbs_qkv_rope_workspace_bytes(const gbs_rope_params* p);
  *   cos_tab, sin_tab  [max_pos, rot / 2] fp32, 16-byte aligned (not read with rot = 0).
  *   pos       [B, N, n_axes] int32; a position outside [0, max_pos) is clamped
  *             and reported by gbs_check(ws) as GBS_ERR_INVALID_ARG.
- *   Q, K, V   outputs, the same shapes; they must not overlap the inputs.
+ *   Q, K, V   outputs, the same shapes. They share no memory with the inputs or with
+ *             each other (parts of one tensor, such as of a packed projection, do not).
  *   ws        NULL (nothing is reported) or device memory of >= 256 bytes. */
 GBS_API gbs_status gbs_qkv_rope_fwd(const gbs_rope_params* p, const gbs_heads* q,
                                     const gbs_heads* k, const gbs_heads* v, const void* wq,
@@ -338,7 +339,8 @@ GBS_API gbs_status gbs_qkv_rope_fwd(const gbs_rope_params* p, const gbs_heads* q
  *   dx = r (h - xh mean(h xh)) (dx = g without weights),
  *   dw = sum over batch, heads and tokens of g xh.
  *   dQ, dK, dV  upstream gradients (what gbs_bwd returns); dV may be NULL.
- *   dq, dk, dv  out; dv NULL exactly if dV is. They must not overlap the inputs.
+ *   dq, dk, dv  out; dv NULL exactly if dV is. They share no memory with the inputs
+ *               or with each other, as above.
  *   dwq, dwk    [d] fp32 out, with weights only; sums in a fixed order, so equal
  *               inputs give equal bits.
  *   ws          gbs_qkv_rope_workspace_bytes(p) bytes. */

@@ -45,3 +45,91 @@ def test_calls_enter_the_device_and_the_stream_of_their_tensors(monkeypatch):
     side = Stream()
     assert gb._elsewhere("x", there, side) == ("stream", side)
     assert "stream is on cuda:1" in rejected(gb._elsewhere, "x", here, side)
+
+
+# ------------------------------------------------------------------ outputs apart from inputs
+
+B, N, HQ, HKV, D = 2, 8, 4, 2, 64
+PACKED = dict(b=N * (HQ + 2 * HKV) * D, h=D, n=(HQ + 2 * HKV) * D)  # of a projection's q, k and v
+FAR = 1 << 30
+
+
+def parts(at, es=2):
+    return [heads(at + i * D * es, **PACKED) for i in (0, HQ, HQ + HKV)]
+
+
+def planes(at, es=2):
+    """Three head-major tensors, one after another."""
+    return [heads(at + i * B * N * D * es, b=h * N * D, h=N * D, n=D) for i, h in ((0, HQ), (HQ, HKV), (HQ + HKV, HKV))]
+
+
+def apart(call):
+    """The library's answer: True where the tensors' places are accepted (and the launch fails without a GPU)."""
+    s = call()
+    assert s in (1, 3) if not torch.cuda.is_available() else s == 1
+    return s == 3
+
+
+def test_outputs_that_share_memory_are_refused(lib):
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls have no memory behind them")
+    p = rope_params(B=B, N=N, Hq=HQ, Hkv=HKV, d=D)
+    ws = lib.gbs_qkv_rope_workspace_bytes(ctypes.byref(p))
+
+    def fwd(ins, outs):
+        return apart(lambda: lib.gbs_qkv_rope_fwd(ctypes.byref(p), *ins, OK, OK, OK, OK, OK, *outs, None, None))
+
+    def bwd(x, ins, outs, w=OK):
+        return apart(lambda: lib.gbs_qkv_rope_bwd(ctypes.byref(p), *x[:2], w, w, OK, OK, OK, *ins, *outs, OK, OK, OK,
+                                                  ws, None))
+
+    total = B * N * (HQ + 2 * HKV) * D * 2
+    assert fwd(parts(FAR), planes(FAR + total)) and fwd(parts(FAR + total), planes(FAR))
+    assert not fwd(parts(FAR), planes(FAR)) and not fwd(parts(FAR), parts(FAR))
+    assert not fwd(parts(FAR), planes(FAR + total - 16)) and not fwd(parts(FAR + total - 16), planes(FAR))
+    q, k, v = planes(FAR + total)
+    assert not fwd(parts(FAR), [q, q, v]) and not fwd(parts(FAR), [q, k, k])
+    assert b"K and V share memory" in lib.gbs_last_error()
+    # the heads of outputs between those of the inputs, in tokens of both
+    wide = dict(b=2 * PACKED["b"], h=D, n=2 * PACKED["n"])
+    ins = [heads(FAR + i * D * 2, **wide) for i in (0, HQ, HQ + HKV)]
+    outs = [heads(FAR + (i + HQ + 2 * HKV) * D * 2, **wide) for i in (0, HQ, HQ + HKV)]
+    assert fwd(ins, outs) and fwd(outs, ins)
+    assert not fwd(ins, [heads(FAR + (i + HQ + 2 * HKV - 1) * D * 2, **wide) for i in (0, HQ, HQ + HKV)])
+    # the gradient where the projection is: refused where it is read, not without a norm
+    assert bwd(parts(FAR + total), planes(FAR), parts(FAR + 2 * total))
+    assert not bwd(parts(FAR + total), planes(FAR), parts(FAR + total))
+    assert b"q and dq share memory" in lib.gbs_last_error()
+    assert bwd(parts(FAR + total), planes(FAR), parts(FAR + total), w=None)
+    assert not bwd(parts(FAR + total), planes(FAR), parts(FAR), w=None)
+    c = cache(kc=FAR, kp=FAR, vc=FAR, vp=FAR)
+    params = gb.make_params(B, HKV, HKV, 250, D, 64, 4, "sparse")
+
+    def read(K, V):
+        return apart(lambda: lib.gbs_kv4_read(ctypes.byref(params), ctypes.byref(c), K, V, N, OK, None, None, None))
+
+    assert read(k, v) and not read(k, k)
+
+
+def test_what_is_found_to_share_memory(lib):
+    """Random places and strides against the elements themselves: nothing that shares one is accepted."""
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls have no memory behind them")
+    import random
+
+    rng, found = random.Random(0), {False: 0, True: 0}
+    params = gb.make_params(2, 2, 2, 250, D, 64, 4, "sparse")
+    c = cache(kc=FAR, kp=FAR, vc=FAR, vp=FAR)
+    for _ in range(3000):
+        places, args = [], []
+        for _ in "kv":
+            steps = rng.sample([D, 2 * D, 4 * D, 8 * D, 3 * D, 24 * D], 3)
+            at = rng.randrange(0, 40) * D // rng.choice((1, 2))
+            places.append({at + b * steps[0] + h * steps[1] + n * steps[2] + x for b in range(2) for h in range(2)
+                           for n in range(3) for x in range(0, D, 8)})
+            args.append(heads(FAR + 2 * at, *steps))
+        ok = apart(lambda: lib.gbs_kv4_read(ctypes.byref(params), ctypes.byref(c), *args, 3, OK, None, None, None))
+        shares = bool(places[0] & places[1])
+        assert not (ok and shares)
+        found[ok == (not shares)] += 1
+    assert found[True] > 2000  # and most that share none are
