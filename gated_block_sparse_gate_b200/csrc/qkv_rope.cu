@@ -128,6 +128,12 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(x): of fp32 rows rounded to nearest, as their results keep all of its bits.
+template <typename T>
+__device__ __forceinline__ float inv_root(float x) {
+  return sizeof(T) == 4 ? __frsqrt_rn(x) : rsqrtf(x);
+}
+
 // What a lane keeps of its token: the angles of its four pairs, sin with either sign.
 struct Angles {
   f32x2 c[2], s[2], minus_s[2];
@@ -261,7 +267,7 @@ __device__ __forceinline__ void forward_tensor(const RopeArgs& a, const Role& ro
     for (int u = 0; u < kRows; ++u, h += role.per_token) {
       if (WHICH < 2) {
         Pairs v = widen<INTER>(raw[u][0], raw[u][1]);
-        if (a.norm) v = times(v, times(w, rsqrtf(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps)));
+        if (a.norm) v = times(v, times(w, inv_root<T>(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps)));
         if (rotates) rotate<false>(v, ang);
         narrow<INTER>(v, &raw[u][0], &raw[u][1]);
       }
@@ -342,7 +348,7 @@ __device__ __forceinline__ void backward_tensor(const RopeArgs& a, const Role& r
           if (rotates) rotate<true>(g, ang);
           if (a.norm) {
             const Pairs v = widen<INTER>(rx[u][0], rx[u][1]), hw = times(g, w);
-            const float r = rsqrtf(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps);
+            const float r = inv_root<T>(row_sum<LANES>(dot(v, v)) * (1.f / D) + a.eps);
             // mean(h xh) xh = x r^2 mean(h x)
             const float back = row_sum<LANES>(dot(hw, v)) * (1.f / D) * r * r;
             dw = fma(times(g, r), v, dw);  // rows left out have g = 0
