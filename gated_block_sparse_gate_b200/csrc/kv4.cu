@@ -1561,13 +1561,13 @@ int decode4_rows(const DecodeArgs& a) {
 // blocks more. The two meet as the root of the sum of squares. Beyond 7/8 of the places, the
 // clusters of a row no longer all find places at once, so half a round more is counted.
 // Microseconds at 1, 2, 4, 6, 8, 16 splits, the rule's own in brackets:
-//   32 rows of 17 blocks    13.8 11.7 9.6 [8.9] 8.7 12.5
-//   64 rows of 33, shared   24.3 18.1 15.0 14.0 15.3 32.3, [15.1] at 5
-//   128 rows of 33          22.2 18.3 17.4 23.7 25.0 46.4, [17.0] at 3
-//   192 rows of 33, shared  28.7 [23.2] 31.0 37.4 41.0 76.9
-//   512 rows of 33          [37.3] 45.2 60.1 71.7 90.4 172
-//   102 rows of 49, d = 64  23.5 18.8 [15.6] 17.6 21.8 33.3
-//   128 rows of 17, fp32    30.6 21.7 20.0 23.7 26.8 45.4, [19.1] at 3
+//   32 rows of 17 blocks    15.4 12.8 11.5 [10.8] 10.8 15.4
+//   64 rows of 33, shared   27.9 20.2 16.6 15.5 16.8 34.9, [16.6] at 5
+//   128 rows of 33          22.8 18.5 17.7 24.2 26.2 48.5, [17.1] at 3
+//   192 rows of 33, shared  34.0 [27.2] 36.6 41.5 46.3 85.2
+//   512 rows of 33          [41.3] 49.8 66.8 80.8 102 195
+//   102 rows of 49, d = 64  24.9 19.0 15.6 23.4 23.1 36.7, [15.4] at 5
+//   128 rows of 17, fp32    31.7 23.4 20.8 26.2 29.5 52.3, [20.3] at 3
 int decode4_splits(int rows, int n_ent, int slots, bool fp32) {
   const float ends = fp32 ? 6.f : 36.f, crowd = fp32 ? 3.f : 2.f, more = fp32 ? 2.f : 12.f;
   int best = 1;
