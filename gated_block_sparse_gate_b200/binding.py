@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import importlib.util
+import operator
 import os
 import struct
 
@@ -512,11 +513,24 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _in_layout(fmt):
+    """pack(where, values...) of a C structure; a value that does not fit is refused in ``where``'s name."""
+    pack = struct.Struct(fmt).pack
+
+    def packed(where, *values):
+        try:
+            return pack(*values)
+        except (struct.error, OverflowError) as e:
+            raise _invalid(where, f"a size or number cannot be passed: {e}") from None
+
+    return packed
+
+
 # The structures of include/gbs.h that the calls below pass, in C layout.
-_PARAMS = struct.Struct("9i2f").pack
+_PARAMS = _in_layout("9i2f")
 _HEADS = struct.Struct("P3q").pack
 _KV4 = struct.Struct("5P3i4x").pack
-_ROPE = struct.Struct("8i64s3if").pack
+_ROPE = _in_layout("8i64s3if")
 assert struct.calcsize("9i2f") == ctypes.sizeof(Params) and struct.calcsize("P3q") == ctypes.sizeof(Heads)
 assert struct.calcsize("5P3i4x") == ctypes.sizeof(Kv4CacheDesc)
 assert struct.calcsize("8i64s3if") == ctypes.sizeof(RopeParams)
@@ -617,7 +631,11 @@ def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev):
     _need(where, "pos", pos, (B, N) if pos.dim() == 2 else (B, N, n_axes), _I32, dev)
     if half > 64:
         raise _invalid(where, f"cos has {half} columns; at most d / 2 = {d // 2} pairs are rotated")
-    axis = _axis_bytes(_ONE_AXIS[:half] if axes is None else tuple(axes), half, n_axes)
+    try:
+        axes = _ONE_AXIS[:half] if axes is None else tuple(map(operator.index, axes))
+    except TypeError:
+        raise _invalid(where, "axes must be whole numbers, one of each pair") from None
+    axis = _axis_bytes(axes, half, n_axes)
     if type(axis) is str:
         raise _invalid(where, axis)
     if (wq is None) != (wk is None):
@@ -627,7 +645,7 @@ def _rope_call(where, q, k, cos, sin, pos, wq, wk, eps, axes, interleaved, dev):
         _need(where, "wq", wq, (d,), _WEIGHTS, dev)
         _need(where, "wk", wk, (d,), (wq.dtype,), dev)
         w_dtype = DTYPES[wq.dtype]
-    return _ROPE(B, N, Hq, Hkv, d, 2 * half, 1 if interleaved else 0, n_axes, axis, max_pos, DTYPES[q.dtype],
+    return _ROPE(where, B, N, Hq, Hkv, d, 2 * half, 1 if interleaved else 0, n_axes, axis, max_pos, DTYPES[q.dtype],
                  w_dtype, eps), (B, N, Hq, Hkv, d)
 
 
@@ -661,7 +679,7 @@ def qkv_rope(q, k, v, cos, sin, pos, wq=None, wk=None, eps=1e-6, axes=None, inte
     hq = _heads(where, "q", q, (B, N, Hq, d), act, dev, True)
     hk = _heads(where, "k", k, (B, N, Hkv, d), act, dev, True)
     hv = None if v is None else _heads(where, "v", v, (B, N, Hkv, d), act, dev, True)
-    if out is not None and (len(out) != 3 or (out[2] is None) != (v is None)):
+    if out is not None and (not isinstance(out, (tuple, list)) or len(out) != 3 or (out[2] is None) != (v is None)):
         raise _invalid(where, "out must be (Q, K, V), V None exactly if v is")
     _check_ws(where, ws, dev)
     Q, K, V = out if out is not None else (
@@ -704,7 +722,8 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
     zq = _heads(where, "dQ", dQ, (B, Hq, N, d), act, dev)
     zk = _heads(where, "dK", dK, (B, Hkv, N, d), act, dev)
     zv = None if dV is None else _heads(where, "dV", dV, (B, Hkv, N, d), act, dev)
-    if grads is not None and (len(grads) != 3 or (grads[2] is None) != (dV is None)):
+    if grads is not None and (not isinstance(grads, (tuple, list)) or len(grads) != 3
+                              or (grads[2] is None) != (dV is None)):
         raise _invalid(where, "grads must be (dq, dk, dv), dv None exactly if dV is")
     if ws is not None:
         _need(where, "ws", ws, None, _U8, dev)
@@ -726,10 +745,11 @@ def qkv_rope_backward(q, k, cos, sin, pos, dQ, dK, dV=None, wq=None, wk=None, ep
 def qkv_rope_workspace_bytes(q, k, rot):
     """Bytes of ``ws`` for ``qkv_rope_backward`` (``qkv_rope`` takes the same one)."""
     B, N, Hq, d = q.shape
-    p = _ROPE(B, N, Hq, k.shape[2], d, rot, 0, 1, b"", 1, DTYPES[q.dtype], 1, 0.0)
+    where = "gbs_qkv_rope_workspace_bytes"
+    p = _ROPE(where, B, N, Hq, k.shape[2], d, rot, 0, 1, b"", 1, DTYPES[q.dtype], 1, 0.0)
     n = int(load_library().gbs_qkv_rope_workspace_bytes(p))
     if n == 0:
-        raise GbsError(1, "gbs_qkv_rope_workspace_bytes", load_library().gbs_last_error().decode())
+        raise GbsError(1, where, load_library().gbs_last_error().decode())
     return n
 
 
@@ -794,7 +814,7 @@ def _kv4_rows(where, fn, K, V, cache, start, block_table, count, ws, block, out,
     _check_ws(where, ws, dev)
     if T == 0:
         return
-    s = fn(_PARAMS(B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[K.dtype], 0.0, 0.0), desc, hk, hv, T, start.data_ptr(),
+    s = fn(_PARAMS(where, B, Hkv, Hkv, L, d, block, 0, 0, DTYPES[K.dtype], 0.0, 0.0), desc, hk, hv, T, start.data_ptr(),
            _addr(count), _addr(ws), _current(dev))
     if s:
         _check(s, where)
@@ -844,11 +864,15 @@ def kv4_read(cache, start, T, block_table=None, count=None, dtype=torch.bfloat16
         raise _invalid(where, "cache must be (key codes, key parameters, value codes, value parameters)")
     if dtype not in DTYPES:
         raise _invalid(where, f"dtype {dtype}; expected torch.bfloat16 or torch.float32")
-    if T < 0:
-        raise _invalid(where, "T must not be negative")
+    if not isinstance(T, int) or T < 0:
+        raise _invalid(where, "T must be a whole number and not negative")
+    if start.dim() != 1:
+        raise _invalid(where, "start must be [B]")
     if out is None:
         shape = (start.shape[0], cache[0].shape[1], T, 2 * cache[0].shape[3])
         K, V = start.new_empty(shape, dtype=dtype), start.new_empty(shape, dtype=dtype)
+    elif not isinstance(out, (tuple, list)) or len(out) != 2:
+        raise _invalid(where, "out must be (K, V)")
     else:
         K, V = out
         _device(where, "K", K)
@@ -896,7 +920,7 @@ def kv4_decode(q, cache, S, L, block=64, topk=32, scale=0.0, num_splits=0, block
         _need(where, "seq_lens", seq_lens, (B,), _I32, dev)
     if ws is not None:
         _need(where, "ws", ws, None, _U8, dev)
-    p = _PARAMS(B, Hq, Hkv, L, d, block, topk, 1 if tau is None else 2, DTYPES[q.dtype], scale,
+    p = _PARAMS(where, B, Hq, Hkv, L, d, block, topk, 1 if tau is None else 2, DTYPES[q.dtype], scale,
                 0.0 if tau is None else tau)
     if out is None:
         out = torch.empty_like(q)

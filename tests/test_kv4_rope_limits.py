@@ -133,3 +133,29 @@ def test_what_is_found_to_share_memory(lib):
         assert not (ok and shares)
         found[ok == (not shares)] += 1
     assert found[True] > 2000  # and most that share none are
+
+
+# ------------------------------------------------------------------ the binding's own refusals
+
+
+def test_arguments_of_another_kind_are_refused_in_words(on_meta):
+    """GbsError where an argument has a form that nothing can be made of: what is not a tuple, a number or that large."""
+    qkv = meta(2, 9, 8, 64)
+    q, k, v = qkv.split((4, 2, 2), 2)
+    t, pos = meta(32, 32, dtype=F32), meta(2, 9, dtype=I32)
+    rope = lambda **kw: gb.qkv_rope(q, k, v, t, t, pos, **kw)  # noqa: E731
+    back = lambda **kw: gb.qkv_rope_backward(q, k, t, t, pos, meta(2, 4, 9, 64), meta(2, 2, 9, 64), None,  # noqa: E731
+                                             **kw)
+    flat, start = gb.kv4_cache(3, 2, 64, L=200, device="meta"), meta(3, dtype=I32)
+    qs, S = meta(3, 4, 64), meta(3, 4, 4, dtype=F32)
+    decode = lambda **kw: gb.kv4_decode(qs, flat, S, 200, **kw)  # noqa: E731
+    for call, text in ((lambda: rope(axes=[0.0] * 32), "whole numbers"), (lambda: rope(axes=3), "whole numbers"),
+                       (lambda: rope(out=3), "out must be"), (lambda: back(grads=q), "grads must be"),
+                       (lambda: rope(eps="a"), "cannot be passed"), (lambda: decode(topk=2 ** 40), "cannot be passed"),
+                       (lambda: decode(topk=2.5), "cannot be passed"),
+                       (lambda: gb.kv4_read(flat, meta(dtype=I32), 4), "start must be"),
+                       (lambda: gb.kv4_read(flat, start, 4.0), "T must be"),
+                       (lambda: gb.kv4_read(flat, start, 4, out=(qs,)), "out must be"),
+                       (lambda: gb.kv4_read(flat, start, 4, out=qs), "out must be")):
+        assert text in rejected(call)
+    rope(axes=torch.zeros(32, dtype=torch.int64))  # anything that counts as whole numbers
