@@ -360,7 +360,9 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __fl
 
 // Selection of the decode (that of select.cu: the min(topk, r) largest of r scores, ties
 // to the lower index, in threshold mode those whose gate reaches tau) by the 128 threads
-// of a CTA. The k-th largest key is found by bisection between the smallest and the
+// of a CTA. (The decode over unpacked caches keeps its lists from select.cu: its CTAs walk chunks
+// of them, and rows of more than kSelectMax blocks need them here too. A change to what is kept
+// is one to both.) The k-th largest key is found by bisection between the smallest and the
 // largest, on scores first and on their ordered bits at the end, until a threshold has k
 // keys on its upper side; no histogram, in which the few exponents of real scores would
 // all meet. Rows of up to 2048 blocks first drop what cannot be among k <= 96 kept ones:
