@@ -215,6 +215,7 @@ gbs_status resolve_heads(const gbs_heads* t, const char* name, int esize, bool o
 bool share_memory(const Heads& a, int heads_a, const Heads& b, int heads_b, int B, int N, int d, int esize) {
   const long long size_a[] = {B, heads_a, N}, step_a[] = {a.sb, a.sh, a.sn};
   const long long size_b[] = {B, heads_b, N}, step_b[] = {b.sb, b.sh, b.sn};
+  constexpr long long kFar = 1ll << 60;
   // elements that a tensor spans within a period; 0 where the period does not divide its longer steps
   auto span = [&](const long long* size, const long long* step, long long period) {
     long long n = d;
@@ -223,7 +224,8 @@ bool share_memory(const Heads& a, int heads_a, const Heads& b, int heads_b, int 
       if (period && step[i] >= period) {
         if (step[i] % period) return 0ll;
       } else {
-        n += (size[i] - 1) * step[i];
+        // (a range of more than 2^60 elements, which no memory has, counts as that)
+        n += step[i] && size[i] - 1 > kFar / step[i] ? kFar : (size[i] - 1) * step[i];
       }
     }
     return n;

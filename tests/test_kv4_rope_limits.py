@@ -159,3 +159,14 @@ def test_arguments_of_another_kind_are_refused_in_words(on_meta):
                        (lambda: gb.kv4_read(flat, start, 4, out=qs), "out must be")):
         assert text in rejected(call)
     rope(axes=torch.zeros(32, dtype=torch.int64))  # anything that counts as whole numbers
+
+
+def test_ranges_beyond_64_bits_are_not_taken_for_apart(lib):
+    """The largest strides with the most tokens: the same place is refused whatever its end would be."""
+    if torch.cuda.is_available():
+        pytest.skip("no memory behind them")
+    for n in (1 << 28, 3 << 26, (1 << 29) - 1):
+        p = rope_params(B=1, N=n, Hq=HQ, Hkv=HKV, d=D)
+        t = [heads(FAR, b=0, h=D, n=1 << 42) for _ in "qkv"]
+        s = lib.gbs_qkv_rope_fwd(ctypes.byref(p), *t, None, None, OK, OK, OK, *t, None, None)
+        assert s == 1 and b"share memory" in lib.gbs_last_error()
